@@ -34,7 +34,7 @@
  *     for the last failing call on the calling thread.
  *   - Layouts are row-major.  Weight matrices are stored "output rows x
  *     input columns" with the input dimension contiguous.
- *   - T == 0 is a no-op returning MOE_OK.
+ *   - T == 0 is a no-op returning MOE_OK (but see moe_add_rmsnorm_backward).
  *   - Global state: the kernel timer below (off by default), the gate mode
  *     (moe_set_gate_mode, split by default), kernel attributes set once per
  *     process on first use, the two fork/join events of moe_forward_overlap (per device and host
@@ -67,10 +67,14 @@ typedef enum {
     MOE_F32 = 0,       /* IEEE binary32                                        */
     MOE_BF16 = 1,      /* bfloat16                                             */
     MOE_FP8_E4M3 = 2,  /* OCP e4m3fn + fp32 scale per 128x128 block (weights)  */
-    MOE_FP8_E4M3_E8M0 = 3  /* OCP e4m3fn + power-of-two fp32 scale per 128x128
+    MOE_FP8_E4M3_E8M0 = 3, /* OCP e4m3fn + power-of-two fp32 scale per 128x128
                               block (weights); the activations get
                               power-of-two 1x128 scales too, and the matrix
                               cores apply the scales (packed weights only)  */
+    MOE_INT4_G128 = 4, /* 4-bit weights, one bf16 scale per 128 inputs of each
+                          output row (bf16 activations, packed weights only,
+                          forward only; see moe_pack_quantized)               */
+    MOE_INT4_G32 = 5   /* the same, one bf16 scale per 32 inputs               */
 } moe_dtype;
 
 /* Layer shape: the MoEGate constructor arguments of the first page's
@@ -87,8 +91,8 @@ typedef struct {
     moe_dtype act_dtype;              /* x, expert outputs and layer output:
                                          MOE_F32 or MOE_BF16                        */
     moe_dtype weight_dtype;           /* expert and shared weights: MOE_F32 (with
-                                         act F32), MOE_BF16 or MOE_FP8_E4M3 (with
-                                         act BF16)                                  */
+                                         act F32), MOE_BF16, MOE_FP8_E4M3* or
+                                         MOE_INT4_* (with act BF16)                 */
 } moe_config;
 
 /* Layer weights.  The gate weight and the selection bias are always fp32.
@@ -98,7 +102,9 @@ typedef struct {
  * MOE_FP8_E4M3_E8M0 every scale must be a power of two (the kernels read its
  * exponent field); the scales are ignored (may be NULL) otherwise.  ws13/ws2 (+scales) may be NULL iff Is == 0.
  * packed = 0: w13, w2, ws13, ws2 are row-major as shown; packed = 1: all four
- * were rearranged by moe_pack_weight (bf16 or e4m3 weights; scales unchanged). */
+ * were rearranged by moe_pack_weight (bf16 or e4m3 weights; scales unchanged).
+ * MOE_INT4_* weights are always packed, by moe_pack_quantized, which stores
+ * their scales among the codes: the *_scale arrays are ignored. */
 typedef struct {
     const float* gate_w;     /* [E, H]                                           */
     const float* bias;       /* [E]  e_score_correction_bias                     */
@@ -188,10 +194,23 @@ moe_status moe_permute(const moe_config* cfg, int64_t T, const int32_t* topk_idx
  * x and h quantised with power-of-two 1x128 scales, and the scaled e4m3
  * MFMA applies both scales inside the matrix core over the whole k loop
  * (its accumulation carries about 13 fraction bits per instruction, below
- * the bf16 rounding of the outputs).  f32: fp32 arithmetic throughout. */
+ * the bf16 rounding of the outputs).  4-bit weights: bf16 MFMA on the codes
+ * as bf16 numbers (exact), each group's scale applied to its fp32 sum, h kept
+ * in bf16.  f32: fp32 arithmetic throughout. */
 moe_status moe_expert_ffn(const moe_config* cfg, int64_t T, const void* x, const int32_t* perm,
                           const int32_t* offsets, const moe_weights* w, void* y, void* y_shared,
                           void* ws, size_t ws_bytes, void* stream);
+
+/* moe_expert_ffn on token rows that are already e4m3 with one fp32 scale per
+ * 1x128 tile, as moe_quantize_act or moe_add_rmsnorm writes them: the same
+ * products without quantising x again.
+ *   xq [T, H] uint8, xs [T, H/128] fp32 (powers of two for MOE_FP8_E4M3_E8M0);
+ *   the rest as moe_expert_ffn.  MOE_ERR_UNSUPPORTED unless the weights are
+ *   e4m3. */
+moe_status moe_expert_ffn_quantized(const moe_config* cfg, int64_t T, const uint8_t* xq,
+                                    const float* xs, const int32_t* perm, const int32_t* offsets,
+                                    const moe_weights* w, void* y, void* y_shared, void* ws,
+                                    size_t ws_bytes, void* stream);
 
 /* Combine: out[t] = y_shared[t] + sum_k topk_w[t,k] * y[pos[t*K+k]], fp32
  * accumulation in k order, rounded once to act_dtype.
@@ -298,6 +317,74 @@ moe_status moe_forward_noalloc(const moe_config* cfg, int64_t T, const void* x,
  *   xq [rows, H] uint8 out, xs [rows, H/128] fp32 out. */
 moe_status moe_quantize_act(const moe_config* cfg, int64_t rows, const void* x, uint8_t* xq,
                             float* xs, void* stream);
+
+/* Residual add and RMS norm, what stands in front of the layer:
+ *   sum = x + residual (rounded to act_dtype; sum = x without a residual),
+ *   y = sum * rstd * weight,  rstd = 1 / sqrt(mean(sum^2) + eps),
+ * and on request y in e4m3 with one fp32 scale per 1x128 tile (the rule of
+ * moe_quantize_act, taken from the fp32 y: one rounding).  The norm reads the
+ * rounded sum, so that the backward needs nothing but the stored stream.
+ *   x, residual [rows, H] act_dtype (residual may be NULL); weight [H] fp32;
+ *   eps finite and > 0 (a row of zeros gives zeros).
+ *   sum [rows, H] act_dtype out, may be NULL, may be x or residual itself;
+ *   y [rows, H] act_dtype out; yq [rows, H] uint8 and ys [rows, H/128] fp32 out
+ *   (both or neither; bf16 activations, H % 128 == 0; power-of-two scales with
+ *   weight_dtype MOE_FP8_E4M3_E8M0).  y or yq may be NULL, not both.
+ * A NaN in a row makes the whole row NaN (in e4m3 too); squares are summed in
+ * fp32, so values above about 1e19 overflow to rstd = 0.  No workspace. */
+moe_status moe_add_rmsnorm(const moe_config* cfg, int64_t rows, const void* x,
+                           const void* residual, const float* weight, float eps, void* sum,
+                           void* y, uint8_t* yq, float* ys, void* stream);
+
+/* Backward of moe_add_rmsnorm.  With n = sum * rstd and g = dy * weight:
+ *   dx = rstd (g - n mean(g n)) + dsum   (the gradient of x and of residual),
+ *   dweight = sum over the rows of dy n  (fp32, fixed order).
+ *   sum [rows, H] as the forward stored it, dy [rows, H] the gradient of y,
+ *   dsum [rows, H] the gradient of sum from its other uses (NULL: none), all
+ *   act_dtype; dx [rows, H] act_dtype out (may be dy or dsum itself);
+ *   dweight [H] fp32 out, written whole, zeros for rows == 0 (the one output
+ *   that a call without rows writes).
+ * rstd is computed again from sum.  Workspace:
+ * moe_add_rmsnorm_backward_workspace_bytes(cfg, rows) bytes, 256-byte
+ * aligned (not needed for rows == 0). */
+size_t moe_add_rmsnorm_backward_workspace_bytes(const moe_config* cfg, int64_t rows);
+moe_status moe_add_rmsnorm_backward(const moe_config* cfg, int64_t rows, const void* sum,
+                                    const float* weight, float eps, const void* dy,
+                                    const void* dsum, void* dx, float* dweight, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* Token rows in the sorted order of the experts, for experts outside the
+ * library (first page, section 2.3, the dispatch): rows[pos[t*K+k]] = x[t].
+ *   x [T, H] act_dtype; pos [T*K] as moe_permute writes it; rows [T*K, H] out.
+ * Here and in the three calls below a position outside [0, T*K) is a slot
+ * without a row (a dropped token): its row is neither read nor written.  Two
+ * slots must not share a position. */
+moe_status moe_dispatch(const moe_config* cfg, int64_t T, const void* x, const int32_t* pos,
+                        void* rows, void* stream);
+
+/* The same for rows in e4m3 ("深入理解 DeepSeek-V3…", section 3.2) with their
+ * 1x128 scales: xq [T, H], xs [T, H/128]; rows_q [T*K, H], rows_s [T*K, H/128]
+ * out.  H % 128 == 0, bf16 activations. */
+moe_status moe_dispatch_quantized(const moe_config* cfg, int64_t T, const uint8_t* xq,
+                                  const float* xs, const int32_t* pos, uint8_t* rows_q,
+                                  float* rows_s, void* stream);
+
+/* Backward of the dispatch: dx[t] = dx_add[t] + sum_k drows[pos[t*K+k]], fp32
+ * in that order, rounded once.
+ *   drows [T*K, H]: gradients of the sorted rows (moe_expert_ffn_backward's
+ *   dx); dx_add [T, H]: a gradient to add (its dx_shared; may be NULL, may be
+ *   dx itself); dx [T, H] out; all act_dtype. */
+moe_status moe_dispatch_backward(const moe_config* cfg, int64_t T, const void* drows,
+                                 const void* dx_add, const int32_t* pos, void* dx, void* stream);
+
+/* Backward of moe_combine: dy[pos[t*K+k]] = topk_w[t,k] dout[t] (rounded to
+ * act_dtype), dtopk_w[t,k] = <dout[t], y[pos[t*K+k]]> (fp32; 0 for a slot
+ * without a row).  The gradient of y_shared is dout itself.
+ *   dout [T, H], y [T*K, H] act_dtype; dy [T*K, H] act_dtype out (what
+ *   moe_expert_ffn_backward takes; may be y itself); dtopk_w [T, K] fp32 out. */
+moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* dout, const void* y,
+                                const int32_t* pos, const float* topk_w, void* dy,
+                                float* dtopk_w, void* stream);
 
 /* Backward of the grouped SwiGLU expert FFN, for training.  The experts are
  * SwiGLU FFNs (mqxn.cn/news/19449, section 3.1) over the routed rows and the
@@ -428,6 +515,30 @@ moe_status moe_bias_update(const moe_config* cfg, const int32_t* counts, float g
 size_t moe_packed_bytes(const moe_config* cfg, moe_weight_id which);
 moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const void* src,
                            void* dst, void* stream);
+
+/* 4-bit expert weights (MOE_INT4_G128, MOE_INT4_G32): every output row is cut
+ * into groups of g = 128 or 32 consecutive inputs,
+ *   W[n][k] = scale[n][k / g] * (code[n][k] - 8),  code in 0..15.
+ * Row-major form: codes [experts, rows, kd / 2] uint8 (column 2j in the low
+ * nibble, 2j + 1 in the high one), scales [experts, rows, kd / g] bf16, with
+ * the rows and kd of the matrix as in moe_weights (w13: 2I rows, kd = H).
+ *   moe_quantize_weight: codes and scales of a row-major bf16 matrix, per
+ *     group scale = bf16(max |w| / 7), code = round(w / scale) + 8, ties to
+ *     even, clamped to 0..15 (scale 0 and codes 8 for a group of zeros).
+ *   moe_pack_quantized: the layout that the kernels stream, codes and scales
+ *     together, into a device buffer of moe_packed_bytes(cfg, which) bytes.
+ *     Per (expert, output tile, 128-k step) one block: eight 1 KiB fragments
+ *     of 16 weight rows (tile: 64 h columns of gate and of up for w13 / ws13,
+ *     128 output rows for w2 / ws2), [lane 64] x 16 bytes, lane l holding row
+ *     l % 16 and in its dword f the codes of k = 128 step + 32 f + 8 (l / 16)
+ *     + 0..7; then the scales [group][row of 16][fragment 8] bf16.
+ * moe_forward and its variants (but moe_forward_decode_fused) and
+ * moe_expert_ffn take the packed weights; the backward does not
+ * (MOE_ERR_UNSUPPORTED), and moe_pack_weight refuses them. */
+moe_status moe_quantize_weight(const moe_config* cfg, moe_weight_id which, const void* src,
+                               uint8_t* codes, void* scales, void* stream);
+moe_status moe_pack_quantized(const moe_config* cfg, moe_weight_id which, const uint8_t* codes,
+                              const void* scales, void* dst, void* stream);
 
 /* Reads the device error flag in ws, which each moe_permute / moe_forward
  * call rewrites; synchronises `stream`.  Returns MOE_OK, MOE_ERR_DEVICE_CHECK

@@ -17,6 +17,10 @@ from ._lib import (EXPORTS, MOE_BF16, MOE_ERR_DEVICE_CHECK, MOE_ERR_HIP, MOE_ERR
                    moe_gate, moe_get_device_error,
                    moe_kernel_timer_enable, moe_kernel_timer_read, moe_last_error,
                    moe_permute, moe_quantize_act, moe_strerror, moe_workspace_bytes, weights,
-                   moe_set_gate_mode, MOE_GATE_SPLIT, MOE_GATE_FUSED)
+                   moe_set_gate_mode, MOE_GATE_SPLIT, MOE_GATE_FUSED,
+                   MOE_INT4_G128, MOE_INT4_G32, moe_quantize_weight, moe_pack_quantized,
+                   moe_expert_ffn_quantized, moe_add_rmsnorm, moe_add_rmsnorm_backward,
+                   moe_add_rmsnorm_backward_workspace_bytes, moe_dispatch,
+                   moe_dispatch_quantized, moe_dispatch_backward, moe_combine_backward)
 
 __all__ = [n for n in dir() if not n.startswith("_")]

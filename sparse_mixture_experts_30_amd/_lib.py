@@ -13,6 +13,7 @@ SO_PATH = os.path.join(HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP, \
     MOE_ERR_DEVICE_CHECK = range(6)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_E8M0 = 0, 1, 2, 3
+MOE_INT4_G128, MOE_INT4_G32 = 4, 5
 
 # Every function declared in include/moe.h.
 EXPORTS = ("moe_workspace_bytes", "moe_gate", "moe_permute", "moe_expert_ffn", "moe_combine",
@@ -21,7 +22,11 @@ EXPORTS = ("moe_workspace_bytes", "moe_gate", "moe_permute", "moe_expert_ffn", "
            "moe_get_device_error", "moe_strerror", "moe_last_error", "moe_kernel_timer_enable",
            "moe_kernel_timer_read", "moe_bias_update", "moe_expert_ffn_backward",
            "moe_expert_ffn_backward_workspace_bytes", "moe_backward",
-           "moe_backward_workspace_bytes", "moe_set_gate_mode")
+           "moe_backward_workspace_bytes", "moe_set_gate_mode", "moe_expert_ffn_quantized",
+           "moe_quantize_weight", "moe_pack_quantized", "moe_add_rmsnorm",
+           "moe_add_rmsnorm_backward", "moe_add_rmsnorm_backward_workspace_bytes",
+           "moe_dispatch", "moe_dispatch_quantized", "moe_dispatch_backward",
+           "moe_combine_backward")
 MOE_W13, MOE_W2, MOE_WS13, MOE_WS2 = 0, 1, 2, 3
 
 
@@ -82,6 +87,19 @@ def lib():
                                             vp, vp, vp, vp, vp, vp, sz, vp]),
             "moe_packed_bytes": (sz, [cfgp, ctypes.c_int]),
             "moe_pack_weight": (ctypes.c_int, [cfgp, ctypes.c_int, vp, vp, vp]),
+            "moe_quantize_weight": (ctypes.c_int, [cfgp, ctypes.c_int, vp, vp, vp, vp]),
+            "moe_pack_quantized": (ctypes.c_int, [cfgp, ctypes.c_int, vp, vp, vp, vp]),
+            "moe_expert_ffn_quantized": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, wp, vp, vp, vp,
+                                                        sz, vp]),
+            "moe_add_rmsnorm": (ctypes.c_int, [cfgp, i64, vp, vp, vp, ctypes.c_float, vp, vp, vp,
+                                               vp, vp]),
+            "moe_add_rmsnorm_backward_workspace_bytes": (sz, [cfgp, i64]),
+            "moe_add_rmsnorm_backward": (ctypes.c_int, [cfgp, i64, vp, vp, ctypes.c_float, vp, vp,
+                                                        vp, vp, vp, sz, vp]),
+            "moe_dispatch": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp]),
+            "moe_dispatch_quantized": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, vp, vp]),
+            "moe_dispatch_backward": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, vp]),
+            "moe_combine_backward": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, vp, vp, vp]),
             "moe_get_device_error": (ctypes.c_int, [vp, sz, vp]),
             "moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
             "moe_last_error": (ctypes.c_char_p, []),
@@ -109,6 +127,14 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _flat(t) -> Optional[int]:
+    """_ptr of a tensor whose values must lie row-major without gaps."""
+    if t is not None and not isinstance(t, int) and not t.is_contiguous():
+        raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not "
+                         f"contiguous")
+    return _ptr(t)
+
+
 def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
@@ -128,7 +154,8 @@ def _check(status: int):
 
 
 def config(H, E, G, TG, K, I, Is, rho, act="bf16", wdtype="bf16") -> MoeConfig:
-    dt = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3, "fp8e8m0": MOE_FP8_E4M3_E8M0}
+    dt = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3, "fp8e8m0": MOE_FP8_E4M3_E8M0,
+          "int4g128": MOE_INT4_G128, "int4g32": MOE_INT4_G32}
     return MoeConfig(H, E, G, TG, K, I, Is, float(rho), dt[act], dt[wdtype])
 
 
@@ -246,6 +273,71 @@ def moe_packed_bytes(cfg: MoeConfig, which: int) -> int:
 
 def moe_pack_weight(cfg, which, src, dst, stream=None):
     _check(lib().moe_pack_weight(ctypes.byref(cfg), which, _ptr(src), _ptr(dst), _stream(stream)))
+
+
+def moe_quantize_weight(cfg, which, src, codes, scales, stream=None):
+    """4-bit codes and bf16 group scales of a row-major bf16 weight matrix."""
+    _check(lib().moe_quantize_weight(ctypes.byref(cfg), which, _flat(src), _flat(codes),
+                                     _flat(scales), _stream(stream)))
+
+
+def moe_pack_quantized(cfg, which, codes, scales, dst, stream=None):
+    """The packed streaming layout of 4-bit codes and their scales."""
+    _check(lib().moe_pack_quantized(ctypes.byref(cfg), which, _flat(codes), _flat(scales),
+                                    _flat(dst), _stream(stream)))
+
+
+def moe_expert_ffn_quantized(cfg, T, xq, xs, perm, offsets, w: MoeWeights, y, y_shared, ws,
+                             stream=None):
+    """moe_expert_ffn on token rows already in e4m3 with 1x128 scales."""
+    _check(lib().moe_expert_ffn_quantized(ctypes.byref(cfg), T, _flat(xq), _flat(xs), _flat(perm),
+                                          _flat(offsets), ctypes.byref(w), _flat(y),
+                                          _flat(y_shared), _flat(ws),
+                                          _nbytes(ws) if ws is not None else 0, _stream(stream)))
+
+
+def moe_add_rmsnorm(cfg, rows, x, residual, weight, eps, sum=None, y=None, yq=None, ys=None,
+                    stream=None):
+    """sum = x + residual, y = rmsnorm(sum) * weight, (yq, ys) = y in e4m3 with 1x128 scales."""
+    _check(lib().moe_add_rmsnorm(ctypes.byref(cfg), rows, _flat(x), _flat(residual),
+                                 _flat(weight), float(eps), _flat(sum), _flat(y), _flat(yq),
+                                 _flat(ys), _stream(stream)))
+
+
+def moe_add_rmsnorm_backward_workspace_bytes(cfg: MoeConfig, rows: int) -> int:
+    return lib().moe_add_rmsnorm_backward_workspace_bytes(ctypes.byref(cfg), rows)
+
+
+def moe_add_rmsnorm_backward(cfg, rows, sum, weight, eps, dy, dx, dweight, ws, dsum=None,
+                             stream=None):
+    _check(lib().moe_add_rmsnorm_backward(ctypes.byref(cfg), rows, _flat(sum), _flat(weight),
+                                          float(eps), _flat(dy), _flat(dsum), _flat(dx),
+                                          _flat(dweight), _flat(ws),
+                                          _nbytes(ws) if ws is not None else 0, _stream(stream)))
+
+
+def moe_dispatch(cfg, T, x, pos, rows, stream=None):
+    """rows[pos[t, k]] = x[t]: the token rows in the order of the sorted experts."""
+    _check(lib().moe_dispatch(ctypes.byref(cfg), T, _flat(x), _flat(pos), _flat(rows),
+                              _stream(stream)))
+
+
+def moe_dispatch_quantized(cfg, T, xq, xs, pos, rows_q, rows_s, stream=None):
+    """moe_dispatch of e4m3 rows and their 1x128 scales."""
+    _check(lib().moe_dispatch_quantized(ctypes.byref(cfg), T, _flat(xq), _flat(xs), _flat(pos),
+                                        _flat(rows_q), _flat(rows_s), _stream(stream)))
+
+
+def moe_dispatch_backward(cfg, T, drows, pos, dx, dx_add=None, stream=None):
+    """dx[t] = dx_add[t] + sum_k drows[pos[t, k]]."""
+    _check(lib().moe_dispatch_backward(ctypes.byref(cfg), T, _flat(drows), _flat(dx_add),
+                                       _flat(pos), _flat(dx), _stream(stream)))
+
+
+def moe_combine_backward(cfg, T, dout, y, pos, topk_w, dy, dtopk_w, stream=None):
+    """dy[pos[t, k]] = topk_w[t, k] dout[t], dtopk_w[t, k] = <dout[t], y[pos[t, k]]>."""
+    _check(lib().moe_combine_backward(ctypes.byref(cfg), T, _flat(dout), _flat(y), _flat(pos),
+                                      _flat(topk_w), _flat(dy), _flat(dtopk_w), _stream(stream)))
 
 
 def moe_get_device_error(ws, stream=None) -> int:

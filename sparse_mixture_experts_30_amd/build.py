@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["gate.hip", "permute.hip", "ffn_sched.hip", "ffn_bf16.hip", "ffn_bf16_packed.hip",
            "ffn_fp8.hip", "ffn_fp8_packed.hip", "ffn_fp8_mx.hip",
            "ffn_f32.hip", "combine.hip", "bias.hip", "ffn_backward.hip", "ffn_backward_fp8.hip", "decode.hip", "decode_layer.hip",
-           "layer_backward.hip", "moe_api.cpp",
+           "layer_backward.hip", "ffn_int4.hip", "norm.hip", "dispatch.hip", "moe_api.cpp",
            "timer.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -35,6 +35,16 @@ inline size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 // e4m3 weights, with block scales a / 448 or powers of two.
 bool is_fp8(moe_dtype w) { return w == MOE_FP8_E4M3 || w == MOE_FP8_E4M3_E8M0; }
 
+// 4-bit weights with bf16 scales per group of 128 or 32 inputs.
+bool is_int4(moe_dtype w) { return w == MOE_INT4_G128 || w == MOE_INT4_G32; }
+int int4_group(moe_dtype w) { return w == MOE_INT4_G32 ? 32 : 128; }
+
+// Configurations of the expert and layer backward: 4-bit weights are for
+// serving and have none.
+bool has_backward(const moe_config* c) {
+  return c->act_dtype == MOE_BF16 && (c->weight_dtype == MOE_BF16 || is_fp8(c->weight_dtype));
+}
+
 // Shape checks shared by every entry point.
 moe_status check_cfg(const moe_config* c) {
   if (!c) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
@@ -56,7 +66,7 @@ moe_status check_cfg(const moe_config* c) {
   const moe_dtype a = c->act_dtype, w = c->weight_dtype;
   if (a != MOE_F32 && a != MOE_BF16)
     return fail(MOE_ERR_INVALID_ARG, "act_dtype must be MOE_F32 or MOE_BF16");
-  if (w != MOE_F32 && w != MOE_BF16 && !is_fp8(w))
+  if (w != MOE_F32 && w != MOE_BF16 && !is_fp8(w) && !is_int4(w))
     return fail(MOE_ERR_INVALID_ARG, "unknown weight_dtype");
   // Valid for the method, not handled by these kernels:
   if (E > 512) return fail(MOE_ERR_UNSUPPORTED, "n_routed_experts > 512");
@@ -64,7 +74,7 @@ moe_status check_cfg(const moe_config* c) {
   if (K > 64) return fail(MOE_ERR_UNSUPPORTED, "num_experts_per_tok > 64");
   if ((a == MOE_F32) != (w == MOE_F32))
     return fail(MOE_ERR_UNSUPPORTED, "fp32 activations need fp32 weights and vice versa");
-  const int mult = is_fp8(w) ? 128 : 64;
+  const int mult = is_fp8(w) || is_int4(w) ? 128 : 64;
   if (H % mult || I % mult || Is % mult)
     return fail(MOE_ERR_UNSUPPORTED, "hidden and FFN sizes must be multiples of %d", mult);
   return MOE_OK;
@@ -113,8 +123,9 @@ Layout layout(const moe_config* c, int64_t T) {
   L.pos = take((size_t)N * 4);
   L.hist = take((size_t)moe::permute_nblk(N) * (E + 1) * 4);
   moe::FfnDims d{T, N, (int)H, (int)I, (int)Is, (int)E, (int)K};
-  L.tiles = take(moe::ffn_tiles_bytes(d));
-  L.tiles2 = take(moe::ffn_tiles_bytes(d));   // the shared expert's list on a second stream
+  const size_t tiles = is_int4(c->weight_dtype) ? moe::int4_tiles_bytes(d) : moe::ffn_tiles_bytes(d);
+  L.tiles = take(tiles);
+  L.tiles2 = take(tiles);   // the shared expert's list on a second stream
   const size_t hel = (size_t)(N * I + T * Is);
   if (fp8) {
     L.h = take(hel);
@@ -202,11 +213,13 @@ moe_status run_permute(const moe_config* c, int64_t T, const int32_t* idx, int32
 
 // groups: which groups to compute (moe::kGroupRouted / kGroupShared);
 // tiles: the tile list to use (built here unless tiles_ready); quantize: fp8
-// weights only, quantise x first (else xq / xs already hold it).
+// weights only, quantise x first (else the workspace's xq / xs already hold
+// it, or given_q / given_s do).
 moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t* perm,
                    const int32_t* offsets, const moe_weights* wt, void* y, void* ys, void* ws,
                    const Layout& L, hipStream_t s, int groups = moe::kGroupsAll,
-                   int32_t* tiles = nullptr, bool tiles_ready = false, bool quantize = true) {
+                   int32_t* tiles = nullptr, bool tiles_ready = false, bool quantize = true,
+                   const uint8_t* given_q = nullptr, const float* given_s = nullptr) {
   moe::FfnDims d{T, T * c->num_experts_per_tok, c->hidden_size, c->moe_intermediate_size,
                  c->shared_intermediate_size, c->n_routed_experts, c->num_experts_per_tok};
   d.groups = groups;
@@ -236,11 +249,19 @@ moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t*
                 "ffn bf16");
       }
       break;
+    case MOE_INT4_G128:
+    case MOE_INT4_G32:
+      HIPCALL(moe::launch_ffn_int4(d, int4_group(c->weight_dtype), (const uint16_t*)x, perm,
+                                   offsets, wt->w13, wt->w2, wt->ws13, wt->ws2,
+                                   at<uint16_t>(ws, L.h), tiles, (uint16_t*)y, (uint16_t*)ys, s),
+              "ffn int4");
+      break;
     case MOE_FP8_E4M3_E8M0: {
-      uint8_t* xq = at<uint8_t>(ws, L.xq);
-      float* xs = at<float>(ws, L.xs);
+      const uint8_t* xq = given_q ? given_q : at<uint8_t>(ws, L.xq);
+      const float* xs = given_q ? given_s : at<float>(ws, L.xs);
       if (quantize)
-        HIPCALL(moe::launch_quant_rows((const uint16_t*)x, T, c->hidden_size, xq, xs, true, s),
+        HIPCALL(moe::launch_quant_rows((const uint16_t*)x, T, c->hidden_size,
+                                       at<uint8_t>(ws, L.xq), at<float>(ws, L.xs), true, s),
                 "quantise x");
       HIPCALL(moe::launch_ffn_fp8_mx(d, xq, xs, perm, offsets, wt->w13, wt->w13_scale, wt->w2,
                                      wt->w2_scale, wt->ws13, wt->ws13_scale, wt->ws2,
@@ -250,10 +271,11 @@ moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t*
       break;
     }
     case MOE_FP8_E4M3: {
-      uint8_t* xq = at<uint8_t>(ws, L.xq);
-      float* xs = at<float>(ws, L.xs);
+      const uint8_t* xq = given_q ? given_q : at<uint8_t>(ws, L.xq);
+      const float* xs = given_q ? given_s : at<float>(ws, L.xs);
       if (quantize)
-        HIPCALL(moe::launch_quant_rows((const uint16_t*)x, T, c->hidden_size, xq, xs, false, s),
+        HIPCALL(moe::launch_quant_rows((const uint16_t*)x, T, c->hidden_size,
+                                       at<uint8_t>(ws, L.xq), at<float>(ws, L.xs), false, s),
                 "quantise x");
       if (wt->packed) {
         HIPCALL(moe::launch_ffn_fp8_packed(d, xq, xs, perm, offsets, wt->w13, wt->w13_scale,
@@ -282,6 +304,8 @@ moe_status check_weights(const moe_config* c, const moe_weights* w, bool need_ga
     return fail(MOE_ERR_INVALID_ARG, "moe_weights.packed must be 0 or 1");
   if (w->packed && c->weight_dtype == MOE_F32)
     return fail(MOE_ERR_UNSUPPORTED, "the packed weight layout is for bf16 and fp8 weights");
+  if (!w->packed && is_int4(c->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "4-bit weights must be packed (moe_pack_quantized)");
   if (need_gate) {
     NONNULL(w->gate_w);
     NONNULL(w->bias);
@@ -411,6 +435,37 @@ moe_status forward_impl(const moe_config* cfg, int64_t T, const void* x, const m
   HIPCALL(moe::launch_combine(y, ys, pos, wt, out, T, cfg->hidden_size, cfg->num_experts_per_tok,
                               cfg->act_dtype == MOE_BF16, s),
           "combine");
+  return MOE_OK;
+}
+
+// One expert weight matrix: its experts, output columns n (of gate and up
+// each, for gate_up) and input columns kd.
+struct Matrix {
+  bool gate_up;
+  int64_t experts;
+  int n, kd;
+};
+
+moe_status weight_matrix(const moe_config* c, moe_weight_id which, Matrix* m) {
+  if (which < MOE_W13 || which > MOE_WS2) return fail(MOE_ERR_INVALID_ARG, "unknown weight id");
+  const bool shared = which == MOE_WS13 || which == MOE_WS2;
+  if (shared && c->shared_intermediate_size == 0)
+    return fail(MOE_ERR_INVALID_ARG, "no shared expert (shared_intermediate_size == 0)");
+  const int inter = shared ? c->shared_intermediate_size : c->moe_intermediate_size;
+  m->gate_up = which == MOE_W13 || which == MOE_WS13;
+  m->experts = shared ? 1 : c->n_routed_experts;
+  m->n = m->gate_up ? inter : c->hidden_size;
+  m->kd = m->gate_up ? c->hidden_size : inter;
+  return MOE_OK;
+}
+
+// rstd of a zero row is 1 / sqrt(eps): eps must be > 0.
+moe_status check_norm(const moe_config* c, int64_t rows, float eps) {
+  CHECK(check_cfg(c));
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows < 0");
+  if (rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "rows exceeds int32 indexing");
+  if (!(isfinite(eps) && eps > 0.0f))
+    return fail(MOE_ERR_INVALID_ARG, "eps must be finite and > 0");
   return MOE_OK;
 }
 
@@ -574,7 +629,7 @@ moe_status moe_forward_overlap(const moe_config* cfg, int64_t T, const void* x,
 
 size_t moe_expert_ffn_backward_workspace_bytes(const moe_config* cfg, int64_t T) {
   if (check_cfg(cfg) != MOE_OK || check_T(T, cfg) != MOE_OK) return 0;
-  if (cfg->act_dtype != MOE_BF16 || cfg->weight_dtype == MOE_F32) return 0;
+  if (!has_backward(cfg)) return 0;
   moe::FfnDims d{T, T * cfg->num_experts_per_tok, cfg->hidden_size, cfg->moe_intermediate_size,
                  cfg->shared_intermediate_size, cfg->n_routed_experts,
                  cfg->num_experts_per_tok};
@@ -591,7 +646,7 @@ moe_status moe_expert_ffn_backward(const moe_config* cfg, int64_t T, const void*
   CHECK(check_cfg(cfg));
   CHECK(check_T(T, cfg));
   const bool fp8 = is_fp8(cfg->weight_dtype);
-  if (cfg->act_dtype != MOE_BF16 || cfg->weight_dtype == MOE_F32)
+  if (!has_backward(cfg))
     return fail(MOE_ERR_UNSUPPORTED,
                 "the expert backward takes bf16 activations with bf16 or e4m3 weights");
   if (T == 0) return MOE_OK;
@@ -655,7 +710,7 @@ moe_status moe_expert_ffn_backward(const moe_config* cfg, int64_t T, const void*
 
 size_t moe_backward_workspace_bytes(const moe_config* cfg, int64_t T) {
   if (check_cfg(cfg) != MOE_OK || check_T(T, cfg) != MOE_OK) return 0;
-  if (cfg->weight_dtype == MOE_F32 || cfg->act_dtype != MOE_BF16) return 0;
+  if (!has_backward(cfg)) return 0;
   moe::FfnDims d{T, T * cfg->num_experts_per_tok, cfg->hidden_size, cfg->moe_intermediate_size,
                  cfg->shared_intermediate_size, cfg->n_routed_experts,
                  cfg->num_experts_per_tok};
@@ -671,7 +726,7 @@ moe_status moe_backward(const moe_config* cfg, int64_t T, const void* x, const m
   CHECK(check_cfg(cfg));
   CHECK(check_T(T, cfg));
   const bool fp8 = is_fp8(cfg->weight_dtype);
-  if (cfg->act_dtype != MOE_BF16 || cfg->weight_dtype == MOE_F32)
+  if (!has_backward(cfg))
     return fail(MOE_ERR_UNSUPPORTED,
                 "the layer backward takes bf16 activations with bf16 or e4m3 weights");
   if (T == 0) return MOE_OK;
@@ -734,6 +789,143 @@ moe_status moe_backward(const moe_config* cfg, int64_t T, const void* x, const m
   return MOE_OK;
 }
 
+moe_status moe_expert_ffn_quantized(const moe_config* cfg, int64_t T, const uint8_t* xq,
+                                    const float* xs, const int32_t* perm, const int32_t* offsets,
+                                    const moe_weights* w, void* y, void* y_shared, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  CHECK(check_cfg(cfg));
+  CHECK(check_T(T, cfg));
+  if (!is_fp8(cfg->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "e4m3 activation rows need e4m3 weights");
+  if (T == 0) return MOE_OK;
+  NONNULL(xq);
+  NONNULL(xs);
+  NONNULL(perm);
+  NONNULL(offsets);
+  NONNULL(y);
+  CHECK(check_weights(cfg, w, false));
+  if (cfg->shared_intermediate_size > 0) NONNULL(y_shared);
+  const Layout L = layout(cfg, T);
+  CHECK(check_ws(ws, ws_bytes, L));
+  return run_ffn(cfg, T, nullptr, perm, offsets, w, y,
+                 cfg->shared_intermediate_size > 0 ? y_shared : nullptr, ws, L,
+                 (hipStream_t)stream, moe::kGroupsAll, nullptr, false, false, xq, xs);
+}
+
+moe_status moe_add_rmsnorm(const moe_config* cfg, int64_t rows, const void* x,
+                           const void* residual, const float* weight, float eps, void* sum,
+                           void* y, uint8_t* yq, float* ys, void* stream) {
+  CHECK(check_norm(cfg, rows, eps));
+  if (!yq != !ys) return fail(MOE_ERR_INVALID_ARG, "yq and ys go together");
+  if (yq && cfg->act_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "the e4m3 output takes bf16 activations");
+  if (yq && cfg->hidden_size % 128) return fail(MOE_ERR_UNSUPPORTED, "hidden_size %% 128 != 0");
+  if (rows == 0) return MOE_OK;
+  NONNULL(x);
+  NONNULL(weight);
+  if (!y && !yq) return fail(MOE_ERR_INVALID_ARG, "y and yq are both NULL");
+  HIPCALL(moe::launch_add_rmsnorm(x, residual, weight, eps, rows, cfg->hidden_size,
+                                  cfg->act_dtype == MOE_BF16, sum, y, yq, ys,
+                                  cfg->weight_dtype == MOE_FP8_E4M3_E8M0, (hipStream_t)stream),
+          "rmsnorm");
+  return MOE_OK;
+}
+
+size_t moe_add_rmsnorm_backward_workspace_bytes(const moe_config* cfg, int64_t rows) {
+  if (check_norm(cfg, rows, 1.0f) != MOE_OK) return 0;
+  return moe::rmsnorm_backward_ws_bytes(rows, cfg->hidden_size);
+}
+
+moe_status moe_add_rmsnorm_backward(const moe_config* cfg, int64_t rows, const void* sum,
+                                    const float* weight, float eps, const void* dy,
+                                    const void* dsum, void* dx, float* dweight, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  CHECK(check_norm(cfg, rows, eps));
+  NONNULL(dweight);
+  if (rows) {
+    NONNULL(sum);
+    NONNULL(weight);
+    NONNULL(dy);
+    NONNULL(dx);
+    const size_t need = moe::rmsnorm_backward_ws_bytes(rows, cfg->hidden_size);
+    if (!ws || ws_bytes < need || ((uintptr_t)ws & 255))
+      return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
+  }
+  HIPCALL(moe::launch_add_rmsnorm_backward(sum, weight, eps, dy, dsum, rows, cfg->hidden_size,
+                                           cfg->act_dtype == MOE_BF16, dx, dweight, (float*)ws,
+                                           (hipStream_t)stream),
+          "rmsnorm backward");
+  return MOE_OK;
+}
+
+moe_status moe_dispatch(const moe_config* cfg, int64_t T, const void* x, const int32_t* pos,
+                        void* rows, void* stream) {
+  CHECK(check_cfg(cfg));
+  CHECK(check_T(T, cfg));
+  if (T == 0) return MOE_OK;
+  NONNULL(x);
+  NONNULL(pos);
+  NONNULL(rows);
+  HIPCALL(moe::launch_dispatch(x, (int64_t)cfg->hidden_size * act_bytes(cfg), nullptr, 0, pos, T,
+                               cfg->num_experts_per_tok, rows, nullptr, (hipStream_t)stream),
+          "dispatch");
+  return MOE_OK;
+}
+
+moe_status moe_dispatch_quantized(const moe_config* cfg, int64_t T, const uint8_t* xq,
+                                  const float* xs, const int32_t* pos, uint8_t* rows_q,
+                                  float* rows_s, void* stream) {
+  CHECK(check_cfg(cfg));
+  CHECK(check_T(T, cfg));
+  if (cfg->act_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "e4m3 rows belong to bf16 activations");
+  if (cfg->hidden_size % 128) return fail(MOE_ERR_UNSUPPORTED, "hidden_size %% 128 != 0");
+  if (T == 0) return MOE_OK;
+  NONNULL(xq);
+  NONNULL(xs);
+  NONNULL(pos);
+  NONNULL(rows_q);
+  NONNULL(rows_s);
+  HIPCALL(moe::launch_dispatch(xq, cfg->hidden_size, xs, cfg->hidden_size / 128, pos, T,
+                               cfg->num_experts_per_tok, rows_q, rows_s, (hipStream_t)stream),
+          "dispatch");
+  return MOE_OK;
+}
+
+moe_status moe_dispatch_backward(const moe_config* cfg, int64_t T, const void* drows,
+                                 const void* dx_add, const int32_t* pos, void* dx, void* stream) {
+  CHECK(check_cfg(cfg));
+  CHECK(check_T(T, cfg));
+  if (T == 0) return MOE_OK;
+  NONNULL(drows);
+  NONNULL(pos);
+  NONNULL(dx);
+  HIPCALL(moe::launch_dispatch_backward(drows, dx_add, pos, T, cfg->hidden_size,
+                                        cfg->num_experts_per_tok, cfg->act_dtype == MOE_BF16, dx,
+                                        (hipStream_t)stream),
+          "dispatch backward");
+  return MOE_OK;
+}
+
+moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* dout, const void* y,
+                                const int32_t* pos, const float* topk_w, void* dy,
+                                float* dtopk_w, void* stream) {
+  CHECK(check_cfg(cfg));
+  CHECK(check_T(T, cfg));
+  if (T == 0) return MOE_OK;
+  NONNULL(dout);
+  NONNULL(y);
+  NONNULL(pos);
+  NONNULL(topk_w);
+  NONNULL(dy);
+  NONNULL(dtopk_w);
+  HIPCALL(moe::launch_combine_backward(dout, y, pos, topk_w, T, cfg->hidden_size,
+                                       cfg->num_experts_per_tok, cfg->act_dtype == MOE_BF16, dy,
+                                       dtopk_w, (hipStream_t)stream),
+          "combine backward");
+  return MOE_OK;
+}
+
 moe_status moe_bias_update(const moe_config* cfg, const int32_t* counts, float gamma,
                            float* bias, void* stream) {
   CHECK(check_cfg(cfg));
@@ -769,7 +961,12 @@ size_t moe_packed_bytes(const moe_config* cfg, moe_weight_id which) {
   if (check_cfg(cfg) != MOE_OK || cfg->weight_dtype == MOE_F32) return 0;
   const int H = cfg->hidden_size, I = cfg->moe_intermediate_size,
             Is = cfg->shared_intermediate_size, E = cfg->n_routed_experts;
-  auto bytes = is_fp8(cfg->weight_dtype) ? moe::packed8_bytes : moe::packed_bytes;
+  auto bytes = [cfg](bool gate_up, int64_t experts, int n, int kd) {
+    if (is_int4(cfg->weight_dtype))
+      return moe::packed4_bytes(gate_up, experts, n, kd, int4_group(cfg->weight_dtype));
+    return is_fp8(cfg->weight_dtype) ? moe::packed8_bytes(gate_up, experts, n, kd)
+                                     : moe::packed_bytes(gate_up, experts, n, kd);
+  };
   switch (which) {
     case MOE_W13: return bytes(true, E, I, H);
     case MOE_W2: return bytes(false, E, H, I);
@@ -784,25 +981,55 @@ moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const voi
   CHECK(check_cfg(cfg));
   if (cfg->weight_dtype == MOE_F32)
     return fail(MOE_ERR_UNSUPPORTED, "the packed weight layout is for bf16 and fp8 weights");
-  if (which < MOE_W13 || which > MOE_WS2) return fail(MOE_ERR_INVALID_ARG, "unknown weight id");
-  const int H = cfg->hidden_size, I = cfg->moe_intermediate_size,
-            Is = cfg->shared_intermediate_size, E = cfg->n_routed_experts;
-  if ((which == MOE_WS13 || which == MOE_WS2) && Is == 0)
-    return fail(MOE_ERR_INVALID_ARG, "no shared expert (shared_intermediate_size == 0)");
+  if (is_int4(cfg->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "4-bit weights are packed with their scales by "
+                "moe_pack_quantized");
+  Matrix m;
+  CHECK(weight_matrix(cfg, which, &m));
   NONNULL(src);
   NONNULL(dst);
-  const bool gate_up = which == MOE_W13 || which == MOE_WS13;
-  const int64_t experts = (which == MOE_W13 || which == MOE_W2) ? E : 1;
-  const int inter = (which == MOE_W13 || which == MOE_W2) ? I : Is;
-  const int n = gate_up ? inter : H, kd = gate_up ? H : inter;
   if (is_fp8(cfg->weight_dtype))
-    HIPCALL(moe::launch_pack8(gate_up, (const uint8_t*)src, dst, experts, n, kd,
+    HIPCALL(moe::launch_pack8(m.gate_up, (const uint8_t*)src, dst, m.experts, m.n, m.kd,
                               (hipStream_t)stream),
             "pack weight");
   else
-    HIPCALL(moe::launch_pack(gate_up, (const uint16_t*)src, dst, experts, n, kd,
+    HIPCALL(moe::launch_pack(m.gate_up, (const uint16_t*)src, dst, m.experts, m.n, m.kd,
                              (hipStream_t)stream),
             "pack weight");
+  return MOE_OK;
+}
+
+moe_status moe_quantize_weight(const moe_config* cfg, moe_weight_id which, const void* src,
+                               uint8_t* codes, void* scales, void* stream) {
+  CHECK(check_cfg(cfg));
+  if (!is_int4(cfg->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_quantize_weight makes 4-bit weights (MOE_INT4_*)");
+  Matrix m;
+  CHECK(weight_matrix(cfg, which, &m));
+  NONNULL(src);
+  NONNULL(codes);
+  NONNULL(scales);
+  HIPCALL(moe::launch_quantize_int4(int4_group(cfg->weight_dtype), (const uint16_t*)src,
+                                    m.experts * (m.gate_up ? 2 : 1) * m.n, m.kd, codes,
+                                    (uint16_t*)scales, (hipStream_t)stream),
+          "quantise weight");
+  return MOE_OK;
+}
+
+moe_status moe_pack_quantized(const moe_config* cfg, moe_weight_id which, const uint8_t* codes,
+                              const void* scales, void* dst, void* stream) {
+  CHECK(check_cfg(cfg));
+  if (!is_int4(cfg->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_pack_quantized packs 4-bit weights (MOE_INT4_*)");
+  Matrix m;
+  CHECK(weight_matrix(cfg, which, &m));
+  NONNULL(codes);
+  NONNULL(scales);
+  NONNULL(dst);
+  HIPCALL(moe::launch_pack_int4(m.gate_up, int4_group(cfg->weight_dtype), codes,
+                                (const uint16_t*)scales, dst, m.experts, m.n, m.kd,
+                                (hipStream_t)stream),
+          "pack quantised weight");
   return MOE_OK;
 }
 

@@ -1,0 +1,200 @@
+"""The 64-bit references of the operators around the layer against central
+differences and hand-worked values, and the refusals of their entry points
+(no GPU)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import sparse_mixture_experts_30_amd as moe
+from oracle import block
+
+FAKE = 0x1000  # never dereferenced: every call below fails validation first
+
+
+def _differences(f, a, h=1e-6):
+    g = np.zeros_like(a)
+    for i in np.ndindex(a.shape):
+        p, m = a.copy(), a.copy()
+        p[i] += h
+        m[i] -= h
+        g[i] = (f(p) - f(m)) / (2 * h)
+    return g
+
+
+@pytest.mark.parametrize("T,H", [(1, 4), (3, 7), (2, 16)])
+def test_rmsnorm_gradient_is_the_forwards_difference(T, H):
+    rng = np.random.default_rng(T * 10 + H)
+    r, dy, ds = (rng.standard_normal((T, H)) for _ in range(3))
+    w, eps = 1 + 0.3 * rng.standard_normal(H), 1e-3
+    dx, dw = block.rmsnorm_backward(r, w, eps, dy, ds)
+    # difference of step h: truncation h^2 ~ 1e-12, rounding 1e-16 / h ~ 1e-10
+    assert np.allclose(dx, _differences(lambda a: (dy * block.rmsnorm(a, w, eps)).sum() + (ds * a).sum(), r),
+                       rtol=0, atol=1e-8)
+    assert np.allclose(dw, _differences(lambda a: (dy * block.rmsnorm(r, a, eps)).sum(), w), rtol=0, atol=1e-8)
+
+
+def test_rmsnorm_of_a_zero_row_is_zero():
+    y = block.rmsnorm(np.zeros((1, 8)), np.ones(8), 1e-6)
+    assert np.all(y == 0)
+    dx, dw = block.rmsnorm_backward(np.zeros((1, 8)), np.full(8, 2.0), 0.25, np.ones((1, 8)))
+    assert np.all(dx == 4.0) and np.all(dw == 0)   # rstd = 2, weight 2
+
+
+def test_combine_gradient_is_the_forwards_difference():
+    rng = np.random.default_rng(5)
+    T, K, H = 3, 2, 5
+    y, w, dout = rng.standard_normal((T * K, H)), rng.random((T, K)), rng.standard_normal((T, H))
+    pos = rng.permutation(T * K).astype(np.int32)
+    pos[2] = -1
+    f = lambda yy, ww: (dout * block.combine(yy, pos, ww, T * K)).sum()  # noqa: E731
+    assert np.allclose(block.combine_backward_w(dout, y, pos, K), _differences(lambda a: f(y, a), w), rtol=0, atol=1e-8)
+    dy = _differences(lambda a: f(a, w), y)
+    for t in range(T):
+        for k in range(K):
+            if pos[t * K + k] >= 0:
+                assert np.allclose(dy[pos[t * K + k]], w[t, k] * dout[t], rtol=0, atol=1e-8)
+
+
+def test_int4_rule_by_hand():
+    w = np.zeros((1, 32), np.float32)
+    w[0, :6] = [7.0, -7.0, 0.5, 1.5, -3.49, 3.51]
+    q, s = block.quantize_int4(w, 32)
+    assert s.tolist() == [[1.0]]
+    assert q[0, :7].tolist() == [15, 1, 8, 10, 5, 12, 8]     # halves to even
+    assert np.array_equal(block.dequantize_int4(q, s, 32)[0, :6], [7, -7, 0, 2, -3, 4])
+    q, s = block.quantize_int4(np.zeros((1, 32), np.float32), 32)
+    assert s[0, 0] == 0 and np.all(q == 8)
+    # the rounding of the scale to bf16 can leave the largest value at most half a step past 7
+    w = np.random.default_rng(0).standard_normal((64, 256)).astype(np.float32)
+    q, s = block.quantize_int4(block.bf16(w), 128)
+    d = np.abs(block.dequantize_int4(q, s, 128) - block.bf16(w))
+    assert np.all(d <= 0.5 * np.repeat(s, 128, axis=1) * (1 + 2 ** -5))
+    assert block.pack_nibbles(np.array([[1, 2, 15, 0]], np.uint8)).tolist() == [[0x21, 0x0F]]
+
+
+def _cfg(**kw):
+    b = dict(H=256, E=8, G=2, TG=1, K=2, I=128, Is=128, rho=1.0, act="bf16", wdtype="bf16")
+    b.update(kw)
+    return moe.config(b["H"], b["E"], b["G"], b["TG"], b["K"], b["I"], b["Is"], b["rho"], b["act"], b["wdtype"])
+
+
+INV, UNS, WS = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_ERR_WORKSPACE
+
+
+def _call(name, cfg, *args):
+    return getattr(moe.lib(), name)(ctypes.byref(cfg), *args, None)
+
+
+@pytest.mark.parametrize("kw,args,status", [
+    ({}, (4, None, FAKE, FAKE, 1e-6, FAKE, FAKE, None, None), INV),          # x
+    ({}, (4, FAKE, FAKE, None, 1e-6, FAKE, FAKE, None, None), INV),          # weight
+    ({}, (4, FAKE, None, FAKE, 1e-6, None, None, None, None), INV),          # neither y nor yq
+    ({}, (4, FAKE, None, FAKE, 1e-6, None, FAKE, FAKE, None), INV),          # yq without ys
+    ({}, (4, FAKE, None, FAKE, 1e-6, None, FAKE, None, FAKE), INV),
+    ({}, (4, FAKE, None, FAKE, 0.0, None, FAKE, None, None), INV),           # eps
+    ({}, (4, FAKE, None, FAKE, float("nan"), None, FAKE, None, None), INV),
+    ({}, (4, FAKE, None, FAKE, float("inf"), None, FAKE, None, None), INV),
+    ({}, (-1, FAKE, None, FAKE, 1e-6, None, FAKE, None, None), INV),
+    ({}, (1 << 31, FAKE, None, FAKE, 1e-6, None, FAKE, None, None), UNS),
+    (dict(act="f32", wdtype="f32"), (4, FAKE, None, FAKE, 1e-6, None, FAKE, FAKE, FAKE), UNS),
+    (dict(H=192), (4, FAKE, None, FAKE, 1e-6, None, FAKE, FAKE, FAKE), UNS),  # e4m3 needs H % 128
+    (dict(K=0), (4, FAKE, None, FAKE, 1e-6, None, FAKE, None, None), INV),
+    ({}, (0, None, None, None, 1e-6, None, None, None, None), moe.MOE_OK),
+])
+def test_add_rmsnorm_refusals(kw, args, status):
+    assert _call("moe_add_rmsnorm", _cfg(**kw), *args) == status, moe.moe_last_error()
+
+
+def test_add_rmsnorm_backward_refusals():
+    def f(rows=4, s=FAKE, w=FAKE, eps=1e-6, dy=FAKE, dx=FAKE, dw=FAKE, ws=FAKE * 256, n=1 << 40):
+        return _call("moe_add_rmsnorm_backward", _cfg(), rows, s, w, eps, dy, None, dx, dw, ws, n)
+    for kw in (dict(s=None), dict(w=None), dict(dy=None), dict(dx=None), dict(dw=None), dict(eps=-1.0),
+               dict(rows=-1), dict(rows=0, dw=None)):
+        assert f(**kw) == INV, kw
+    for kw in (dict(ws=None), dict(n=100), dict(ws=FAKE * 256 + 4)):
+        assert f(**kw) == WS, kw
+    assert moe.moe_add_rmsnorm_backward_workspace_bytes(_cfg(), -1) == 0
+    assert moe.moe_add_rmsnorm_backward_workspace_bytes(_cfg(), 0) == 0
+    assert moe.moe_add_rmsnorm_backward_workspace_bytes(_cfg(), 1) >= 4 * 256
+
+
+@pytest.mark.parametrize("name,n,nullable", [("moe_dispatch", 3, ()), ("moe_dispatch_quantized", 5, ()),
+                                             ("moe_dispatch_backward", 4, (1,)), ("moe_combine_backward", 6, ())])
+def test_row_operator_refusals(name, n, nullable):
+    for i in range(n):
+        args = [FAKE] * n
+        args[i] = None
+        if i not in nullable:
+            assert _call(name, _cfg(), 4, *args) == INV, (name, i)
+    assert _call(name, _cfg(), -1, *[FAKE] * n) == INV
+    assert _call(name, _cfg(), 1 << 31, *[FAKE] * n) == UNS          # T * top_k past int32
+    assert _call(name, _cfg(E=7), 4, *[FAKE] * n) == INV
+    assert _call(name, _cfg(), 0, *[None] * n) == moe.MOE_OK
+    if name == "moe_dispatch_quantized":
+        assert _call(name, _cfg(H=192), 4, *[FAKE] * n) == UNS
+        assert _call(name, _cfg(act="f32", wdtype="f32"), 4, *[FAKE] * n) == UNS
+
+
+@pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
+def test_int4_refusals(wd):
+    c, L = _cfg(wdtype=wd), moe.lib()
+    for kw in (dict(H=192), dict(I=192), dict(Is=64)):
+        assert moe.moe_workspace_bytes(_cfg(wdtype=wd, **kw), 4) == 0
+        assert "128" in moe.moe_last_error()
+    assert moe.moe_workspace_bytes(_cfg(wdtype=wd, act="f32"), 4) == 0
+    group = 32 if wd == "int4g32" else 128
+    for which, weights in ((moe.MOE_W13, 8 * 256 * 256), (moe.MOE_W2, 8 * 256 * 128), (moe.MOE_WS13, 256 * 256),
+                           (moe.MOE_WS2, 256 * 128)):
+        assert moe.moe_packed_bytes(c, which) == weights // 2 + weights // group * 2
+    assert moe.moe_packed_bytes(_cfg(wdtype=wd, Is=0), moe.MOE_WS2) == 0
+    for f in ("moe_quantize_weight", "moe_pack_quantized"):
+        for i in range(3):
+            args = [FAKE] * 3
+            args[i] = None
+            assert _call(f, c, moe.MOE_W13, *args) == INV
+        assert _call(f, c, 4, FAKE, FAKE, FAKE) == INV
+        assert _call(f, c, -1, FAKE, FAKE, FAKE) == INV
+        assert _call(f, _cfg(wdtype=wd, Is=0), moe.MOE_WS13, FAKE, FAKE, FAKE) == INV
+        for other in ("bf16", "fp8", "fp8e8m0"):
+            assert _call(f, _cfg(wdtype=other), moe.MOE_W13, FAKE, FAKE, FAKE) == UNS
+    assert _call("moe_pack_weight", c, moe.MOE_W13, FAKE, FAKE) == UNS
+    row = moe.weights(gate_w=FAKE, bias=FAKE, w13=FAKE, w2=FAKE, ws13=FAKE, ws2=FAKE)
+    packed = moe.weights(gate_w=FAKE, bias=FAKE, w13=FAKE, w2=FAKE, ws13=FAKE, ws2=FAKE, packed=True)
+    ffn = lambda w: L.moe_expert_ffn(ctypes.byref(c), 4, FAKE, FAKE, FAKE, ctypes.byref(w), FAKE, FAKE,  # noqa: E731
+                                     FAKE * 256, 16, None)
+    assert ffn(row) == UNS and "packed" in moe.moe_last_error()
+    assert ffn(packed) == WS
+    # forward only: neither backward takes them, and the one-launch decode layer does not
+    assert moe.moe_backward_workspace_bytes(c, 4) == moe.moe_expert_ffn_backward_workspace_bytes(c, 4) == 0
+    assert L.moe_expert_ffn_backward(ctypes.byref(c), 4, FAKE, FAKE, FAKE, ctypes.byref(row), FAKE, FAKE, None, None,
+                                     FAKE, FAKE, FAKE, FAKE, FAKE * 256, 1 << 40, None) == UNS
+    assert L.moe_backward(ctypes.byref(c), 4, FAKE, ctypes.byref(row), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
+                          FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE * 256, 1 << 40, None) == UNS
+    assert L.moe_forward_decode_fused(ctypes.byref(c), 4, FAKE, ctypes.byref(packed), FAKE, None, None, None, None,
+                                      None, FAKE * 256, 1 << 40, None) == UNS
+
+
+def test_quantized_rows_need_e4m3_weights():
+    w = moe.weights(w13=FAKE, w2=FAKE, ws13=FAKE, ws2=FAKE, packed=True)
+    for wd in ("bf16", "int4g128"):
+        c = _cfg(wdtype=wd)
+        assert moe.lib().moe_expert_ffn_quantized(ctypes.byref(c), 4, FAKE, FAKE, FAKE, FAKE, ctypes.byref(w), FAKE,
+                                                  FAKE, FAKE * 256, 1 << 40, None) == UNS
+    c = _cfg(wdtype="fp8")
+    w = moe.weights(w13=FAKE, w13_scale=FAKE, w2=FAKE, w2_scale=FAKE, ws13=FAKE, ws13_scale=FAKE, ws2=FAKE,
+                    ws2_scale=FAKE, packed=True)
+    for i in range(4):
+        a = [FAKE] * 4
+        a[i] = None
+        assert moe.lib().moe_expert_ffn_quantized(ctypes.byref(c), 4, *a, ctypes.byref(w), FAKE, FAKE, FAKE * 256,
+                                                  1 << 40, None) == INV
+    assert moe.lib().moe_expert_ffn_quantized(ctypes.byref(c), 4, FAKE, FAKE, FAKE, FAKE, ctypes.byref(w), FAKE, FAKE,
+                                              FAKE * 256, 100, None) == WS
+
+
+def test_binding_refuses_gaps():
+    import torch
+    t = torch.zeros(8, 512, dtype=torch.bfloat16)[:, :256]
+    with pytest.raises(ValueError, match="contiguous"):
+        moe.moe_add_rmsnorm(_cfg(), 8, t, None, FAKE, 1e-6, y=FAKE, stream=0)
