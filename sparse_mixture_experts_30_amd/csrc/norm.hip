@@ -13,12 +13,11 @@
 #include "rows_device.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 
 namespace {
-
-constexpr int kNormThreads = 256;
 
 // fp32 -> e4m3fn bits as f32_to_e4m3, with NaN kept NaN.
 __device__ __forceinline__ uint32_t e4m3_code(float v) {
@@ -46,38 +45,55 @@ __device__ __forceinline__ uint2 quant_chunk(const float (&v)[8], bool pow2, flo
   return make_uint2(lo, hi);
 }
 
+// r = x + residual of one chunk, rounded as the stream stores it.
 template <typename IO>
-__device__ __forceinline__ void add_chunk(const IO* x, const IO* residual, float (&r)[8]) {
-  load_chunk(x, r);
-  if (!residual) return;
+__device__ __forceinline__ void add_chunk(const RawChunk<IO>& x, bool has_residual,
+                                          const RawChunk<IO>& residual, float (&r)[8]) {
+  x.to(r);
+  if (!has_residual) return;
   float b[8];
-  load_chunk(residual, b);
+  residual.to(b);
 #pragma unroll
   for (int j = 0; j < 8; ++j) r[j] = as_stored<IO>(r[j] + b[j]);
 }
 
-// One workgroup per row, two passes over it.
+// Sums of a and b over the workgroup in a fixed order, one barrier; red holds
+// 2 * 16 floats that the previous call does not use (calls alternate halves).
+__device__ __forceinline__ void workgroup_sums(float& a, float& b, float* red) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    a += __shfl_xor(a, off, 64);
+    b += __shfl_xor(b, off, 64);
+  }
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0) {
+    red[threadIdx.x >> 6] = a;
+    red[16 + (threadIdx.x >> 6)] = b;
+  }
+  __syncthreads();
+  a = b = 0.0f;
+  for (int w = 0; w < waves; ++w) {
+    a += red[w];
+    b += red[16 + w];
+  }
+}
+
+// One workgroup per row.  A row of up to NC * blockDim.x chunks stays in
+// registers between the sum of squares and the output (NC > 0); longer rows
+// (NC = 0) are read twice.
 // sum may be x or residual itself: a thread rewrites only chunks that it
 // alone reads, after reading them.
-template <typename IO>
-__global__ void __launch_bounds__(kNormThreads)
+template <typename IO, int NC>
+__global__ void __launch_bounds__(1024)
 add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ weight, float eps,
                    int H, IO* sum, IO* y, uint8_t* __restrict__ yq, float* __restrict__ ys,
                    bool pow2) {
-  __shared__ float red[kNormThreads / 64];
+  __shared__ float red[32];
   const int64_t row = (int64_t)blockIdx.x * H;
   const int nc = H / kChunk;
-  float ss = 0.0f;
-  for (int c = threadIdx.x; c < nc; c += kNormThreads) {
-    float r[8];
-    add_chunk(x + row + c * 8, residual ? residual + row + c * 8 : nullptr, r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(r[j], r[j], ss);
-  }
-  const float rstd = 1.0f / sqrtf(workgroup_sum<kNormThreads>(ss, red) / (float)H + eps);
-  for (int c = threadIdx.x; c < nc; c += kNormThreads) {
-    float r[8], w[8];
-    add_chunk(x + row + c * 8, residual ? residual + row + c * 8 : nullptr, r);
+  auto finish = [&](int c, float (&r)[8], float rstd) {
+    float w[8];
     load_chunk(weight + c * 8, w);
     if (sum) store_chunk(sum + row + c * 8, r);
 #pragma unroll
@@ -88,65 +104,228 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
       *reinterpret_cast<uint2*>(yq + row + c * 8) = quant_chunk(r, pow2, scale);
       if ((c & 15) == 0) ys[(row >> 7) + (c >> 4)] = scale;
     }
+  };
+  auto load = [&](int c, float (&r)[8]) {
+    RawChunk<IO> a, b{};
+    a.load(x + row + c * 8);
+    if (residual) b.load(residual + row + c * 8);
+    add_chunk(a, residual != nullptr, b, r);
+  };
+  float ss = 0.0f, none = 0.0f;
+  if constexpr (NC > 0) {
+    RawChunk<IO> a[NC], b[NC];
+    float r[NC][8];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < nc) a[i].load(x + row + c * 8);
+    }
+    if (residual) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < nc) b[i].load(residual + row + c * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c >= nc) break;
+      add_chunk(a[i], residual != nullptr, b[i], r[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
+    }
+    workgroup_sums(ss, none, red);
+    const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < nc) finish(c, r[i], rstd);
+    }
+  } else {
+    float r[8];
+    for (int c = threadIdx.x; c < nc; c += blockDim.x) {
+      load(c, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(r[j], r[j], ss);
+    }
+    workgroup_sums(ss, none, red);
+    const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
+    for (int c = threadIdx.x; c < nc; c += blockDim.x) {
+      load(c, r);
+      finish(c, r, rstd);
+    }
   }
 }
 
-// Workgroup b takes rows b, b + gridDim.x, ...; its share of dw is kept in
-// its row of `part` [gridDim.x][H].
-template <typename IO>
-__global__ void __launch_bounds__(kNormThreads)
+// Workgroup b takes rows b, b + gridDim.x, ... and writes its share of dw to
+// its row of `part` [gridDim.x][H].  Rows of up to NC * blockDim.x chunks
+// (NC > 0): each thread keeps its columns' weight and dw in registers, reads
+// every value once, and has the next row's loads in flight during the sums.
+// Longer rows (NC = 0) are read twice and dw is kept in `part`.
+template <typename IO, int NC>
+__global__ void __launch_bounds__(1024)
 add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict__ weight,
                             float eps, const IO* dy, const IO* dsum, int64_t rows, int H, IO* dx,
                             float* __restrict__ part) {
-  __shared__ float red[kNormThreads / 64];
+  __shared__ float red[2][32];
   const int nc = H / kChunk;
   float* mine = part + (int64_t)blockIdx.x * H;
-  for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
-    const int64_t row = t * H;
-    float ss = 0.0f, dot = 0.0f;
-    for (int c = threadIdx.x; c < nc; c += kNormThreads) {
-      float r[8], g[8], w[8];
-      load_chunk(sum + row + c * 8, r);
-      load_chunk(dy + row + c * 8, g);
-      load_chunk(weight + c * 8, w);
+  int turn = 0;
+  if constexpr (NC > 0) {
+    float w[NC][8], dw[NC][8];
+    RawChunk<IO> r[NC], g[NC], nr[NC], ng[NC];
+    auto fetch = [&](int64_t t) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss = fmaf(r[j], r[j], ss);
-        dot = fmaf(g[j] * w[j], r[j], dot);
+      for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c >= nc) break;
+        nr[i].load(sum + t * H + c * 8);
+        ng[i].load(dy + t * H + c * 8);
+      }
+    };
+    fetch(blockIdx.x);   // the grid has at most `rows` workgroups
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < nc) load_chunk(weight + c * 8, w[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    }
+    for (int64_t t = blockIdx.x; t < rows; t += gridDim.x, turn ^= 1) {
+      float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        r[i] = nr[i];
+        g[i] = ng[i];
+      }
+      RawChunk<IO> d[NC];
+      if (dsum) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = threadIdx.x + i * blockDim.x;
+          if (c < nc) d[i].load(dsum + t * H + c * 8);
+        }
+      }
+      if (t + gridDim.x < rows) fetch(t + gridDim.x);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c >= nc) break;
+        float rv[8], gv[8];
+        r[i].to(rv);
+        g[i].to(gv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ss = fmaf(rv[j], rv[j], ss);
+          dot = fmaf(gv[j] * w[i][j], rv[j], dot);
+        }
+      }
+      workgroup_sums(ss, dot, red[turn]);
+      const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
+      const float mean = dot * rstd / (float)H;   // mean(g * n)
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c >= nc) break;
+        float rv[8], gv[8], dv[8];
+        r[i].to(rv);
+        g[i].to(gv);
+        if (dsum) d[i].to(dv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float n = rv[j] * rstd;
+          dw[i][j] = fmaf(gv[j], n, dw[i][j]);
+          rv[j] = rstd * (gv[j] * w[i][j] - n * mean) + (dsum ? dv[j] : 0.0f);
+        }
+        store_chunk(dx + t * H + c * 8, rv);
       }
     }
-    ss = workgroup_sum<kNormThreads>(ss, red);
-    dot = workgroup_sum<kNormThreads>(dot, red);
-    const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
-    const float mean = dot * rstd / (float)H;   // mean(g * n)
-    for (int c = threadIdx.x; c < nc; c += kNormThreads) {
-      float r[8], g[8], w[8], a[8], d[8];
-      load_chunk(sum + row + c * 8, r);
-      load_chunk(dy + row + c * 8, g);
-      load_chunk(weight + c * 8, w);
-      if (dsum) load_chunk(dsum + row + c * 8, d);
-      if (t != blockIdx.x) load_chunk(mine + c * 8, a);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = r[j] * rstd;
-        a[j] = (t != blockIdx.x ? a[j] : 0.0f) + g[j] * n;
-        r[j] = rstd * (g[j] * w[j] - n * mean) + (dsum ? d[j] : 0.0f);
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < nc) store_chunk(mine + c * 8, dw[i]);
+    }
+  } else {
+    for (int64_t t = blockIdx.x; t < rows; t += gridDim.x, turn ^= 1) {
+      const int64_t row = t * H;
+      float ss = 0.0f, dot = 0.0f;
+      for (int c = threadIdx.x; c < nc; c += blockDim.x) {
+        float r[8], g[8], w[8];
+        load_chunk(sum + row + c * 8, r);
+        load_chunk(dy + row + c * 8, g);
+        load_chunk(weight + c * 8, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ss = fmaf(r[j], r[j], ss);
+          dot = fmaf(g[j] * w[j], r[j], dot);
+        }
       }
-      store_chunk(mine + c * 8, a);
-      store_chunk(dx + row + c * 8, r);
+      workgroup_sums(ss, dot, red[turn]);
+      const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
+      const float mean = dot * rstd / (float)H;
+      for (int c = threadIdx.x; c < nc; c += blockDim.x) {
+        float r[8], g[8], w[8], a[8], d[8];
+        load_chunk(sum + row + c * 8, r);
+        load_chunk(dy + row + c * 8, g);
+        load_chunk(weight + c * 8, w);
+        if (dsum) load_chunk(dsum + row + c * 8, d);
+        if (t != blockIdx.x) load_chunk(mine + c * 8, a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float n = r[j] * rstd;
+          a[j] = fmaf(g[j], n, t != blockIdx.x ? a[j] : 0.0f);
+          r[j] = rstd * (g[j] * w[j] - n * mean) + (dsum ? d[j] : 0.0f);
+        }
+        store_chunk(mine + c * 8, a);
+        store_chunk(dx + row + c * 8, r);
+      }
     }
   }
 }
 
-// dw[h] = sum of part[b][h] over b in order; zeros for nparts = 0.
-__global__ void __launch_bounds__(kNormThreads)
+// dw[h] = sum of part[b][h] over b; zeros for nparts = 0.  A workgroup takes
+// 32 columns (one 128-byte line of every part): thread (q, slice) sums the
+// parts slice, slice + 32, ... of columns 4q..4q+3, and the 32 slices are
+// joined through LDS in a fixed order.
+constexpr int kDwCols = 32, kDwSlices = 32;
+__global__ void __launch_bounds__(256)
 rmsnorm_dweight_kernel(const float* __restrict__ part, int nparts, int H,
                        float* __restrict__ dweight) {
-  const int h = blockIdx.x * kNormThreads + threadIdx.x;
-  if (h >= H) return;
-  float a = 0.0f;
-  for (int b = 0; b < nparts; ++b) a += part[(int64_t)b * H + h];
-  dweight[h] = a;
+  __shared__ f32x4 lds[kDwSlices][kDwCols / 4 + 1];
+  const int q = threadIdx.x & 7, slice = threadIdx.x >> 3;
+  const int h = blockIdx.x * kDwCols + q * 4;   // H is a multiple of 64
+  f32x4 a = {0.f, 0.f, 0.f, 0.f};
+  constexpr int B = 8;   // parts whose loads are issued together
+  for (int b0 = slice; b0 < nparts; b0 += B * kDwSlices) {
+    f32x4 v[B];
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      const int b = b0 + u * kDwSlices;
+      v[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      if (b < nparts) v[u] = *reinterpret_cast<const f32x4*>(part + (int64_t)b * H + h);
+    }
+#pragma unroll
+    for (int u = 0; u < B; ++u) a += v[u];
+  }
+  lds[slice][q] = a;
+  __syncthreads();
+  if (slice >= 4) return;
+  // thread (q, slice): column quad q, sums 8 slices each, then lane shuffles
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int u = 0; u < kDwSlices / 4; ++u) s += lds[slice * (kDwSlices / 4) + u][q];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    s[j] += __shfl_xor(s[j], 8, 64);
+    s[j] += __shfl_xor(s[j], 16, 64);
+  }
+  if (slice == 0) *reinterpret_cast<f32x4*>(dweight + h) = s;
+}
+
+// Threads of a workgroup for rows held as NC chunks a thread.
+int norm_threads(int H, int nc) {
+  return std::min(1024, (H / kChunk + 64 * nc - 1) / (64 * nc) * 64);
 }
 
 constexpr int64_t kNormParts = 512;   // row sums of dw kept apart at most
@@ -157,14 +336,25 @@ size_t rmsnorm_backward_ws_bytes(int64_t rows, int H) {
   return ((size_t)std::min(rows, kNormParts) * H * sizeof(float) + 255) / 256 * 256;
 }
 
+// Chunks of a row that a thread holds in registers: two, four from H = 16384
+// on, none (the row is read twice) past 32768.
+#define MOE_NORM_BY_WIDTH(H, call) \
+  ((H) <= 16384 ? call(2) : (H) <= 32768 ? call(4) : call(0))
+
 template <typename IO>
 static hipError_t add_rmsnorm(const void* x, const void* residual, const float* weight, float eps,
                               int64_t rows, int H, void* sum, void* y, uint8_t* yq, float* ys,
                               bool pow2, hipStream_t s) {
-  MOE_TIMED_LAUNCH(s, "add_rmsnorm_kernel",
-    hipLaunchKernelGGL(add_rmsnorm_kernel<IO>, dim3((unsigned)rows), dim3(kNormThreads), 0, s,
-                       (const IO*)x, (const IO*)residual, weight, eps, H, (IO*)sum, (IO*)y, yq, ys,
-                       pow2));
+  auto run = [&](auto nc) {
+    constexpr int NC = decltype(nc)::value;
+    MOE_TIMED_LAUNCH(s, "add_rmsnorm_kernel",
+      hipLaunchKernelGGL((add_rmsnorm_kernel<IO, NC>), dim3((unsigned)rows),
+                         dim3(norm_threads(H, NC ? NC : 4)), 0, s, (const IO*)x,
+                         (const IO*)residual, weight, eps, H, (IO*)sum, (IO*)y, yq, ys, pow2));
+  };
+#define MOE_CALL(nc) run(std::integral_constant<int, nc>{})
+  MOE_NORM_BY_WIDTH(H, MOE_CALL);
+#undef MOE_CALL
   return hipGetLastError();
 }
 
@@ -181,16 +371,25 @@ static hipError_t add_rmsnorm_backward(const void* sum, const float* weight, flo
                                        void* dx, float* dweight, float* part, hipStream_t s) {
   const int64_t parts = std::min(rows, kNormParts);
   if (parts) {
-    MOE_TIMED_LAUNCH(s, "add_rmsnorm_backward_kernel",
-      hipLaunchKernelGGL(add_rmsnorm_backward_kernel<IO>, dim3((unsigned)parts),
-                         dim3(kNormThreads), 0, s, (const IO*)sum, weight, eps, (const IO*)dy,
-                         (const IO*)dsum, rows, H, (IO*)dx, part));
+    auto run = [&](auto nc) {
+      constexpr int NC = decltype(nc)::value;
+      MOE_TIMED_LAUNCH(s, "add_rmsnorm_backward_kernel",
+        hipLaunchKernelGGL((add_rmsnorm_backward_kernel<IO, NC>), dim3((unsigned)parts),
+                           dim3(norm_threads(H, NC ? NC : 4)), 0, s, (const IO*)sum, weight, eps,
+                           (const IO*)dy, (const IO*)dsum, rows, H, (IO*)dx, part));
+    };
+    // wider rows leave no registers for a thread's share of dw
+    constexpr int NC = sizeof(IO) == 2 ? 2 : 1;
+    if (H <= 1024 * NC * kChunk)
+      run(std::integral_constant<int, NC>{});
+    else
+      run(std::integral_constant<int, 0>{});
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   MOE_TIMED_LAUNCH(s, "rmsnorm_dweight_kernel",
-    hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((H + kNormThreads - 1) / kNormThreads),
-                       dim3(kNormThreads), 0, s, part, (int)parts, H, dweight));
+    hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3(H / kDwCols), dim3(256), 0, s, part,
+                       (int)parts, H, dweight));
   return hipGetLastError();
 }
 
