@@ -529,7 +529,8 @@ moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const voi
  *     together, into a device buffer of moe_packed_bytes(cfg, which) bytes.
  *     Per (expert, output tile, 128-k step) one block: eight 1 KiB fragments
  *     of 16 weight rows (tile: 64 h columns of gate and of up for w13 / ws13,
- *     128 output rows for w2 / ws2), [lane 64] x 16 bytes, lane l holding row
+ *     128 output rows for w2 / ws2; fragments 0, 1, 4, 5 of a w13 / ws13 tile
+ *     are its gate rows, 2, 3, 6, 7 the up rows), [lane 64] x 16 bytes, lane l holding row
  *     l % 16 and in its dword f the codes of k = 128 step + 32 f + 8 (l / 16)
  *     + 0..7; then the scales [group][row of 16][fragment 8] bf16.
  * moe_forward and its variants (but moe_forward_decode_fused) and

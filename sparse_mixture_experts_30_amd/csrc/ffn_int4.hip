@@ -16,12 +16,14 @@
 // 1 KiB fragments of 16 rows, then the scales [group][row of 16][fragment 8].
 // Lane l of fragment b holds row l % 16; its dword f covers
 // k = 128 step + 32 f + 8 (l / 16) + 0..7, value 2i in nibble i, value 2i + 1
-// in nibble i + 4.  Fragments 0-3 of a gate/up tile are gate rows, 4-7 the up
-// rows of the same columns.
+// in nibble i + 4.  Fragments 0, 1 and 4, 5 of a gate/up tile are gate rows of
+// its first and second 32 columns, 2, 3 and 6, 7 the up rows of the same.
 //
-// Each workgroup computes one tile for up to 16 * NRB rows; its four waves
-// take a quarter of the k steps each and their sums are joined through LDS in
-// wave order.
+// Two kernels.  Batches with few rows per expert (decode) read their
+// activations straight from L2, 16 rows per tile, and split the k steps over
+// the four waves of a workgroup.  Batches with more rows share the
+// activations of up to 64 rows through LDS and split the output columns over
+// the waves.
 #include "moe_internal.hpp"
 
 #include <algorithm>
@@ -64,134 +66,136 @@ __device__ __forceinline__ bf16x8 codes_bf16(uint32_t d) {
   return as_bf16x8(r);
 }
 
-template <bool kGateUp, int kGroup, int NRB>
-__device__ __forceinline__ void int4_tile(const Int4Args& p, float* lds, int g, int row0,
-                                          int nrows, int ntile) {
+// The eight scales of a vector as fp32.
+__device__ __forceinline__ void scales_f32(u32x4 v, float (&s)[kFrags]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s[2 * i] = __uint_as_float(v[i] << 16);
+    s[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ bf16x8 minus_136() {
+  return as_bf16x8((u32x4){0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u});
+}
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- few rows
+// A tile of at most 16 rows: wave w takes a quarter of the k steps, D of them
+// in flight, and the four waves' sums are joined through LDS in wave order.
+constexpr int kFewRows = 16;
+
+template <bool kGateUp, int kGroup, int D, bool kStream>
+__device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int g, int row0,
+                                              int nrows, int ntile) {
   constexpr int kUnits = step_units(kGroup);
   constexpr int kScales = kStepK / kGroup;   // scale vectors per step
+  constexpr int kF = 4 / kScales;            // k fragments per group
   const bool sh = (g == p.E);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
   const int nsteps = (sh ? p.kdim_s : p.kdim_r) / kStepK;
   const int s0 = nsteps * wave / 4, s1 = nsteps * (wave + 1) / 4;
-  const uint16_t* A = sh ? p.a_s : p.a_r;
-  const int64_t lda = sh ? p.lda_s : p.lda_r;
   const u32x4* bw = (sh ? p.b_s : p.b_r + (int64_t)g * p.nt_r * nsteps * kUnits) +
                     (int64_t)ntile * nsteps * kUnits;
-  // This lane's activation rows (rows past the end re-read the first; their
-  // results are never stored).
-  const uint16_t* ap[NRB];
-#pragma unroll
-  for (int r = 0; r < NRB; ++r) {
-    const int row = r * 16 + lr;
-    const int rr = row < nrows ? row : 0;
-    const int a = (!sh && kGateUp) ? p.perm[row0 + rr] / p.K : row0 + rr;
-    ap[r] = A + (int64_t)a * lda + lq * 8;
-  }
-  const u32x4 offs_bits = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};   // -136
-  const bf16x8 offs = as_bf16x8(offs_bits);
 
-  f32x4 acc[NRB][kFrags];
-#pragma unroll
-  for (int r = 0; r < NRB; ++r)
-#pragma unroll
-    for (int b = 0; b < kFrags; ++b) acc[r][b] = (f32x4){0.f, 0.f, 0.f, 0.f};
-
-  u32x4 rb[kFrags], sc[kScales], ra[NRB][4];
-  auto load = [&](int step) {
-    const u32x4* src = bw + (int64_t)step * kUnits;
-#pragma unroll
-    for (int b = 0; b < kFrags; ++b) rb[b] = __builtin_nontemporal_load(src + b * 64 + lane);
-#pragma unroll
-    for (int q = 0; q < kScales; ++q) sc[q] = src[kCodes16 + q * 16 + lr];
-#pragma unroll
-    for (int r = 0; r < NRB; ++r)
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-        ra[r][f] = *reinterpret_cast<const u32x4*>(ap[r] + step * kStepK + f * 32);
-  };
-  for (int s = s0; s < s1; ++s) {
-    load(s);
-#pragma unroll
-    for (int q = 0; q < kScales; ++q) {
-      constexpr int kF = 4 / kScales;   // fragments of k per group
-      float sv[kFrags];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sv[2 * i] = __uint_as_float(sc[q][i] << 16);
-        sv[2 * i + 1] = __uint_as_float(sc[q][i] & 0xFFFF0000u);
-      }
-#pragma unroll
-      for (int r = 0; r < NRB; ++r) {
-        f32x4 corr = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int f = q * kF; f < (q + 1) * kF; ++f)
-          corr = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(ra[r][f]), offs, corr, 0, 0, 0);
-#pragma unroll
-        for (int b = 0; b < kFrags; ++b) {
-          f32x4 part = corr;
-#pragma unroll
-          for (int f = q * kF; f < (q + 1) * kF; ++f)
-            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(ra[r][f]),
-                                                           codes_bf16(rb[b][f]), part, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][b][i] = fmaf(sv[b], part[i], acc[r][b][i]);
-        }
-      }
-    }
-  }
-
-  // Join the four waves' sums, one row block at a time: [wave][frag][row quad
-  // 4][i 4][col 16].
-  uint16_t* C = sh ? p.c_s : p.c_r;
-  const int64_t ldc = sh ? p.ldc_s : p.ldc_r;
-#pragma unroll
-  for (int r = 0; r < NRB; ++r) {
-    if (r) __syncthreads();
+  u32x4 rb[D][kFrags], sc[D][kScales], ra[D][4];
+  // Steps past the wave's last one load its last one again.
+  auto load_w = [&](int slot, int step) {
+    const u32x4* src = bw + (int64_t)min(step, nsteps - 1) * kUnits;
 #pragma unroll
     for (int b = 0; b < kFrags; ++b)
+      rb[slot][b] = kStream ? __builtin_nontemporal_load(src + b * 64 + lane) : src[b * 64 + lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        lds[((wave * kFrags + b) * 16 + 4 * lq + i) * 16 + lr] = acc[r][b][i];
-    __syncthreads();
-    const int row = tid >> 4;
-    if (r * 16 + row >= nrows) continue;   // the barrier above is passed by all threads
-    uint16_t* crow = C + (int64_t)(row0 + r * 16 + row) * ldc;
-    if (kGateUp) {
-      const int col = (tid & 15) * 4, b = col >> 4;
-      float h[4];
-      f32x4 gv = {0.f, 0.f, 0.f, 0.f}, uv = {0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < kScales; ++q) sc[slot][q] = src[kCodes16 + q * 16 + lr];
+  };
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        gv += *reinterpret_cast<const f32x4*>(
-            lds + ((w * kFrags + b) * 16 + row) * 16 + (col & 15));
-        uv += *reinterpret_cast<const f32x4*>(
-            lds + ((w * kFrags + 4 + b) * 16 + row) * 16 + (col & 15));
+  for (int d = 0; d < D; ++d) load_w(d, s0 + d);
+  // This lane's activation row (past the end the first one; those results are
+  // never stored).
+  const int rr = lr < nrows ? lr : 0;
+  const int arow = (!sh && kGateUp) ? p.perm[row0 + rr] / p.K : row0 + rr;
+  const uint16_t* ap = (sh ? p.a_s : p.a_r) + (int64_t)arow * (sh ? p.lda_s : p.lda_r) + lq * 8;
+  auto load_a = [&](int slot, int step) {
+    const uint16_t* src = ap + min(step, nsteps - 1) * kStepK;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) ra[slot][f] = *reinterpret_cast<const u32x4*>(src + f * 32);
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load_a(d, s0 + d);
+
+  f32x4 acc[kFrags];
+#pragma unroll
+  for (int b = 0; b < kFrags; ++b) acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int s = s0; s < s1; s += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (s + d < s1) {
+#pragma unroll
+        for (int q = 0; q < kScales; ++q) {
+          float sv[kFrags];
+          scales_f32(sc[d][q], sv);
+          f32x4 corr = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int f = q * kF; f < (q + 1) * kF; ++f)
+            corr = mfma16(as_bf16x8(ra[d][f]), minus_136(), corr);
+#pragma unroll
+          for (int b = 0; b < kFrags; ++b) {
+            f32x4 part = corr;
+#pragma unroll
+            for (int f = q * kF; f < (q + 1) * kF; ++f)
+              part = mfma16(as_bf16x8(ra[d][f]), codes_bf16(rb[d][b][f]), part);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[b][i] = fmaf(sv[b], part[i], acc[b][i]);
+          }
+        }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = gv[j] / (1.0f + __expf(-gv[j])) * uv[j];
-      *reinterpret_cast<uint2*>(crow + ntile * 64 + col) =
-          make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
-    } else {
-      const int col = (tid & 15) * 8, b = col >> 4;
-      f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          v[j] += *reinterpret_cast<const f32x4*>(
-              lds + ((w * kFrags + b) * 16 + row) * 16 + (col & 15) + 4 * j);
-      *reinterpret_cast<u32x4*>(crow + ntile * 128 + col) =
-          (u32x4){pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
-                  pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3])};
+      load_w(d, s + d + D);
+      load_a(d, s + d + D);
     }
+  }
+
+  // [wave][frag][row 16][col 16]
+#pragma unroll
+  for (int b = 0; b < kFrags; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      lds[((wave * kFrags + b) * 16 + 4 * lq + i) * 16 + lr] = acc[b][i];
+  __syncthreads();
+  const int row = tid >> 4;
+  if (row >= nrows) return;
+  uint16_t* crow = (sh ? p.c_s : p.c_r) + (int64_t)(row0 + row) * (sh ? p.ldc_s : p.ldc_r);
+  auto joined = [&](int b, int col) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      v += *reinterpret_cast<const f32x4*>(lds + ((w * kFrags + b) * 16 + row) * 16 + col);
+    return v;
+  };
+  if (kGateUp) {
+    const int col = (tid & 15) * 4, b = (col >> 5) * 4 + (col >> 4 & 1);
+    const f32x4 gv = joined(b, col & 15), uv = joined(b + 2, col & 15);
+    float h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = gv[j] / (1.0f + __expf(-gv[j])) * uv[j];
+    *reinterpret_cast<uint2*>(crow + ntile * 64 + col) =
+        make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+  } else {
+    const int col = (tid & 15) * 8, b = col >> 4;
+    const f32x4 v = joined(b, col & 15), w = joined(b, (col & 15) + 4);
+    *reinterpret_cast<u32x4*>(crow + ntile * 128 + col) =
+        (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(w[0], w[1]),
+                pack_bf16x2(w[2], w[3])};
   }
 }
 
-// MAXRB: 16-row blocks of the tallest tile of the list.
-template <bool kGateUp, int kGroup, int MAXRB>
-__global__ void __launch_bounds__(kThreads4) grouped_gemm_int4(Int4Args p) {
+template <bool kGateUp, int kGroup>
+__global__ void __launch_bounds__(kThreads4) grouped_gemm_int4_few(Int4Args p) {
   __shared__ __align__(16) float lds[4 * kFrags * 256];
+  constexpr int D = 2;
   const int64_t work = (int64_t)p.tiles[0] * p.ntn;
   const int64_t w = xcd_chunked(blockIdx.x, work);
   if (w < 0) return;
@@ -199,19 +203,186 @@ __global__ void __launch_bounds__(kThreads4) grouped_gemm_int4(Int4Args p) {
   const int32_t* ent = decode_work(p.tiles, w, p.ntn, ntile);
   const int g = ent[0], row0 = ent[1], nrows = ent[2];
   if (ntile >= (g == p.E ? p.nt_s : p.nt_r)) return;
-  switch ((nrows + 15) >> 4) {
-    case 1:
-      int4_tile<kGateUp, kGroup, 1>(p, lds, g, row0, nrows, ntile);
+  // A weight tile that only this row tile reads is not kept in cache.
+  if (ent[4] == 1)
+    int4_few_tile<kGateUp, kGroup, D, true>(p, lds, g, row0, nrows, ntile);
+  else
+    int4_few_tile<kGateUp, kGroup, D, false>(p, lds, g, row0, nrows, ntile);
+}
+
+// --------------------------------------------------------------- many rows
+// A tile of at most 64 rows and two packed output tiles: each wave takes four
+// fragments over the whole k range, the rows' activations pass through two
+// LDS buffers in fragment order (lane-linear 16-byte reads and writes).
+constexpr int kManyRows = 64;
+
+template <bool kGateUp, int kGroup, int NRB, bool kStream>
+__device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, int g, int row0,
+                                               int nrows, int npair) {
+  constexpr int kUnits = step_units(kGroup);
+  constexpr int kScales = kStepK / kGroup;
+  constexpr int kF = 4 / kScales;
+  constexpr int D = 2;                       // weight steps in flight
+  const bool sh = (g == p.E);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lr = lane & 15, lq = lane >> 4;
+  const int nsteps = (sh ? p.kdim_s : p.kdim_r) / kStepK;
+  const int nt = sh ? p.nt_s : p.nt_r;
+  // An odd number of packed tiles leaves the last pair's second half to no
+  // one: its waves load the first half's weights and store nothing.
+  const int ntile = npair * 2 + (wave >> 1);
+  const bool mine = ntile < nt;
+  const u32x4* bw = (sh ? p.b_s : p.b_r + (int64_t)g * nt * nsteps * kUnits) +
+                    (int64_t)(mine ? ntile : ntile - 1) * nsteps * kUnits;
+  const int fh = wave & 1;   // this wave's half of the tile's fragments
+
+  const uint16_t* ap[NRB];
+#pragma unroll
+  for (int r = 0; r < NRB; ++r) {
+    const int rr = r * 16 + lr < nrows ? r * 16 + lr : 0;
+    const int arow = (!sh && kGateUp) ? p.perm[row0 + rr] / p.K : row0 + rr;
+    ap[r] = (sh ? p.a_s : p.a_r) + (int64_t)arow * (sh ? p.lda_s : p.lda_r) + wave * 32 + lq * 8;
+  }
+  u32x4 rb[D][4], st[NRB];
+  uint2 sc[D][kScales];
+  auto load_w = [&](int slot, int step) {
+    const u32x4* src = bw + (int64_t)min(step, nsteps - 1) * kUnits;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      rb[slot][b] = kStream ? __builtin_nontemporal_load(src + (fh * 4 + b) * 64 + lane)
+                            : src[(fh * 4 + b) * 64 + lane];
+#pragma unroll
+    for (int q = 0; q < kScales; ++q)
+      sc[slot][q] = reinterpret_cast<const uint2*>(src + kCodes16 + q * 16 + lr)[fh];
+  };
+  // Wave w stages k fragment w of every row block.
+  auto load_a = [&](int step) {
+#pragma unroll
+    for (int r = 0; r < NRB; ++r)
+      st[r] = *reinterpret_cast<const u32x4*>(ap[r] + min(step, nsteps - 1) * kStepK);
+  };
+  auto store_a = [&](int buf) {
+#pragma unroll
+    for (int r = 0; r < NRB; ++r) lds[((buf * NRB + r) * 4 + wave) * 64 + lane] = st[r];
+  };
+
+  load_a(0);
+#pragma unroll
+  for (int d = 0; d < D; ++d) load_w(d, d);
+  f32x4 acc[NRB][4];
+#pragma unroll
+  for (int r = 0; r < NRB; ++r)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[r][b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  store_a(0);
+  load_a(1);
+  __syncthreads();
+
+  for (int s = 0; s < nsteps; s += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (s + d < nsteps) {   // the same for the whole workgroup
+#pragma unroll
+        for (int q = 0; q < kScales; ++q) {
+          u32x4 a[NRB][kF];
+#pragma unroll
+          for (int r = 0; r < NRB; ++r)
+#pragma unroll
+            for (int f = 0; f < kF; ++f)
+              a[r][f] = lds[((d * NRB + r) * 4 + q * kF + f) * 64 + lane];
+          const float sv[4] = {__uint_as_float(sc[d][q].x << 16),
+                               __uint_as_float(sc[d][q].x & 0xFFFF0000u),
+                               __uint_as_float(sc[d][q].y << 16),
+                               __uint_as_float(sc[d][q].y & 0xFFFF0000u)};
+          f32x4 corr[NRB];
+#pragma unroll
+          for (int r = 0; r < NRB; ++r) {
+            corr[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int f = 0; f < kF; ++f)
+              corr[r] = mfma16(as_bf16x8(a[r][f]), minus_136(), corr[r]);
+          }
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            f32x4 part[NRB];
+#pragma unroll
+            for (int f = 0; f < kF; ++f) {
+              const bf16x8 w = codes_bf16(rb[d][b][q * kF + f]);
+#pragma unroll
+              for (int r = 0; r < NRB; ++r)
+                part[r] = mfma16(as_bf16x8(a[r][f]), w, f == 0 ? corr[r] : part[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < NRB; ++r)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[r][b][i] = fmaf(sv[b], part[r][i], acc[r][b][i]);
+          }
+        }
+        load_w(d, s + d + D);
+        store_a(d ^ 1);      // read again after the barrier; last read before the previous one
+        load_a(s + d + 2);
+        __syncthreads();
+      }
+    }
+  }
+
+  // Results through LDS (the buffers are free after the last barrier), each
+  // wave its own part: [row][its 64 output or 32 h columns] bf16.
+  constexpr int kCols = kGateUp ? 32 : 64;
+  uint16_t* out = reinterpret_cast<uint16_t*>(lds) + wave * (NRB * 16 * kCols);
+#pragma unroll
+  for (int r = 0; r < NRB; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint16_t* o = out + (r * 16 + 4 * lq + i) * kCols + lr;
+      if (kGateUp) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float gv = acc[r][b][i], uv = acc[r][2 + b][i];
+          o[b * 16] = (uint16_t)f32_to_bf16_bits(gv / (1.0f + __expf(-gv)) * uv);
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) o[b * 16] = (uint16_t)f32_to_bf16_bits(acc[r][b][i]);
+      }
+    }
+  __syncthreads();
+  if (!mine) return;
+  const int col0 = kGateUp ? ntile * 64 + fh * 32 : ntile * 128 + fh * 64;
+  uint16_t* C = (sh ? p.c_s : p.c_r) + col0;
+  const int64_t ldc = sh ? p.ldc_s : p.ldc_r;
+  constexpr int kPer = kCols / 8;            // 16-byte pieces per row
+  for (int i = lane; i < NRB * 16 * kPer; i += 64) {
+    const int row = i / kPer, c = (i % kPer) * 8;
+    if (row < nrows)
+      *reinterpret_cast<u32x4*>(C + (int64_t)(row0 + row) * ldc + c) =
+          *reinterpret_cast<const u32x4*>(out + row * kCols + c);
+  }
+}
+
+template <bool kGateUp, int kGroup>
+__global__ void __launch_bounds__(kThreads4, 2) grouped_gemm_int4_many(Int4Args p) {
+  __shared__ u32x4 lds[2 * (kManyRows / 16) * 4 * 64];   // 32 KiB
+  const int64_t work = (int64_t)p.tiles[0] * p.ntn;
+  const int64_t w = xcd_chunked(blockIdx.x, work);
+  if (w < 0) return;
+  int npair;
+  const int32_t* ent = decode_work(p.tiles, w, p.ntn, npair);
+  const int g = ent[0], row0 = ent[1], nrows = ent[2];
+  if (2 * npair >= (g == p.E ? p.nt_s : p.nt_r)) return;
+  switch (((nrows + 15) >> 4) * 2 + (ent[4] == 1 ? 1 : 0)) {
+#define MOE_INT4_CASE(n)                                                               \
+    case 2 * n:                                                                        \
+      int4_many_tile<kGateUp, kGroup, n, false>(p, lds, g, row0, nrows, npair);        \
+      break;                                                                           \
+    case 2 * n + 1:                                                                    \
+      int4_many_tile<kGateUp, kGroup, n, true>(p, lds, g, row0, nrows, npair);         \
       break;
-    case 2:
-      if (MAXRB >= 2) int4_tile<kGateUp, kGroup, MAXRB >= 2 ? 2 : 1>(p, lds, g, row0, nrows, ntile);
-      break;
-    case 3:
-      if (MAXRB >= 3) int4_tile<kGateUp, kGroup, MAXRB >= 3 ? 3 : 1>(p, lds, g, row0, nrows, ntile);
-      break;
-    case 4:
-      if (MAXRB >= 4) int4_tile<kGateUp, kGroup, MAXRB >= 4 ? 4 : 1>(p, lds, g, row0, nrows, ntile);
-      break;
+    MOE_INT4_CASE(1)
+    MOE_INT4_CASE(2)
+    MOE_INT4_CASE(3)
+    MOE_INT4_CASE(4)
+#undef MOE_INT4_CASE
     default:
       break;
   }
@@ -235,7 +406,7 @@ pack_int4_kernel(bool gate_up, int group, const uint8_t* __restrict__ codes,
   // Row of fragment b, lane row r in this tile.
   auto row_of = [&](int b, int r) -> int64_t {
     if (!gate_up) return (int64_t)tile * 128 + b * 16 + r;
-    return (b < 4 ? 0 : n) + (int64_t)tile * 64 + (b & 3) * 16 + r;
+    return (b & 2 ? n : 0) + (int64_t)tile * 64 + (b >> 2) * 32 + (b & 1) * 16 + r;
   };
   u32x4 out = {0u, 0u, 0u, 0u};
   if (o < kCodes16) {
@@ -300,30 +471,31 @@ quantize_int4_kernel(int group, const uint16_t* __restrict__ src, int64_t chunks
 }
 
 template <bool kGateUp, int kGroup>
-hipError_t launch_gemm(const Int4Args& a, int maxrb, int64_t work, hipStream_t s) {
-  const dim3 grid(xcd_grid(work));
-#define MOE_INT4_LAUNCH(rb)                                                              \
-  MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4<true>" : "grouped_gemm_int4<false>",  \
-    hipLaunchKernelGGL((grouped_gemm_int4<kGateUp, kGroup, rb>), grid, dim3(kThreads4), 0, s, a))
-  if (maxrb == 1)
-    MOE_INT4_LAUNCH(1);
-  else if (maxrb == 2)
-    MOE_INT4_LAUNCH(2);
-  else
-    MOE_INT4_LAUNCH(4);
-#undef MOE_INT4_LAUNCH
+hipError_t launch_gemm(Int4Args a, bool few, int64_t mtiles, hipStream_t s) {
+  if (few) {
+    MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_few<true>" : "grouped_gemm_int4_few<false>",
+      hipLaunchKernelGGL((grouped_gemm_int4_few<kGateUp, kGroup>), dim3(xcd_grid(mtiles * a.ntn)),
+                         dim3(kThreads4), 0, s, a));
+  } else {
+    a.ntn = (a.ntn + 1) / 2;
+    MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_many<true>" : "grouped_gemm_int4_many<false>",
+      hipLaunchKernelGGL((grouped_gemm_int4_many<kGateUp, kGroup>), dim3(xcd_grid(mtiles * a.ntn)),
+                         dim3(kThreads4), 0, s, a));
+  }
   return hipGetLastError();
 }
 
-// 16-row blocks of the tallest tile: a batch of T tokens gives no expert
-// more rows than that unless a caller's routing repeats one, and then the
-// list cuts them.
-int row_blocks(int64_t T) { return T <= 16 ? 1 : T <= 32 ? 2 : 4; }
+// The few-row kernel up to kFewAverage rows per expert on average.
+constexpr int kFewAverage = 4;
+bool use_few(const FfnDims& d) {
+  return d.T <= kFewRows || d.N <= (int64_t)kFewAverage * d.E;
+}
+int tile_rows(const FfnDims& d) { return use_few(d) ? kFewRows : kManyRows; }
 
 }  // namespace
 
 size_t int4_tiles_bytes(const FfnDims& d) {
-  return (size_t)(8 + 8 * ffn_max_mtiles(d.N, d.T, d.E, 16 * row_blocks(d.T))) * sizeof(int32_t);
+  return (size_t)(8 + 8 * ffn_max_mtiles(d.N, d.T, d.E, tile_rows(d))) * sizeof(int32_t);
 }
 
 size_t packed4_bytes(bool gate_up, int64_t experts, int n, int kd, int group) {
@@ -354,7 +526,8 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
                            const int32_t* offsets, const void* w13p, const void* w2p,
                            const void* ws13p, const void* ws2p, uint16_t* h, int32_t* tiles,
                            uint16_t* y, uint16_t* ys, hipStream_t s) {
-  const int maxrb = row_blocks(d.T), bm = 16 * maxrb;
+  const bool few = use_few(d);
+  const int bm = tile_rows(d);
   hipError_t e = ffn_build_tiles(d, offsets, bm, tiles, s, true);
   if (e != hipSuccess) return e;
   const int64_t mt = ffn_grid_mtiles(d, bm);
@@ -376,8 +549,8 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
   a.c_s = h + d.N * d.I;
   a.ldc_r = d.I;
   a.ldc_s = d.Is;
-  e = group == 32 ? launch_gemm<true, 32>(a, maxrb, mt * a.ntn, s)
-                  : launch_gemm<true, 128>(a, maxrb, mt * a.ntn, s);
+  e = group == 32 ? launch_gemm<true, 32>(a, few, mt, s)
+                  : launch_gemm<true, 128>(a, few, mt, s);
   if (e != hipSuccess) return e;
 
   a.nt_r = a.nt_s = a.ntn = d.H / 128;
@@ -390,8 +563,8 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
   a.c_r = y;
   a.c_s = ys;
   a.ldc_r = a.ldc_s = d.H;
-  return group == 32 ? launch_gemm<false, 32>(a, maxrb, mt * a.ntn, s)
-                     : launch_gemm<false, 128>(a, maxrb, mt * a.ntn, s);
+  return group == 32 ? launch_gemm<false, 32>(a, few, mt, s)
+                     : launch_gemm<false, 128>(a, few, mt, s);
 }
 
 }  // namespace moe

@@ -24,6 +24,27 @@ __device__ __forceinline__ uint32_t e4m3_code(float v) {
   return v != v ? 0x7Fu : f32_to_e4m3(v);
 }
 
+// The tile scales of fp8_device.hpp without 64-bit arithmetic, which is most
+// of a decode batch's time here: a / 448 and 448 / a in fp32 are the rounded
+// 64-bit quotients (a quotient of two 24-bit numbers rounds the same through
+// 53 bits), and the smallest power of two >= a / 448 = a / (1.75 2^8) follows
+// from a's exponent and from whether its mantissa exceeds 1.75.
+__device__ __forceinline__ void row_tile_scale(float amax, bool pow2, float& scale, float& inv) {
+  if (!(amax > 0.0f)) {
+    scale = 1.0f;
+    inv = 0.0f;
+  } else if (pow2) {
+    const uint32_t u = __float_as_uint(amax);
+    const int x = (int)(u >> 23);   // 255: infinity
+    const int e = x == 255 ? 127 : max(x - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);
+    scale = __uint_as_float((uint32_t)(e + 127) << 23);
+    inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  } else {
+    scale = amax / 448.0f;
+    inv = 448.0f / amax;
+  }
+}
+
 // e4m3 codes of the 8 values v (one chunk; 16 consecutive lanes hold a tile)
 // and the tile's scale.  All 16 lanes of the tile call this.
 __device__ __forceinline__ uint2 quant_chunk(const float (&v)[8], bool pow2, float& scale) {
@@ -33,10 +54,7 @@ __device__ __forceinline__ uint2 quant_chunk(const float (&v)[8], bool pow2, flo
 #pragma unroll
   for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   float inv;
-  if (pow2)
-    tile_scale_pow2(m, scale, inv);
-  else
-    tile_scale(m, scale, inv);
+  row_tile_scale(m, pow2, scale, inv);
   uint32_t lo = 0, hi = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) lo |= e4m3_code(v[j] * inv) << (8 * j);
@@ -92,9 +110,7 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
   __shared__ float red[32];
   const int64_t row = (int64_t)blockIdx.x * H;
   const int nc = H / kChunk;
-  auto finish = [&](int c, float (&r)[8], float rstd) {
-    float w[8];
-    load_chunk(weight + c * 8, w);
+  auto finish = [&](int c, float (&r)[8], const float (&w)[8], float rstd) {
     if (sum) store_chunk(sum + row + c * 8, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) r[j] = r[j] * rstd * w[j];
@@ -114,7 +130,7 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
   float ss = 0.0f, none = 0.0f;
   if constexpr (NC > 0) {
     RawChunk<IO> a[NC], b[NC];
-    float r[NC][8];
+    float r[NC][8], w[NC][8];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
@@ -130,6 +146,11 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
+      if (c < nc) load_chunk(weight + c * 8, w[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
       if (c >= nc) break;
       add_chunk(a[i], residual != nullptr, b[i], r[i]);
 #pragma unroll
@@ -140,7 +161,7 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nc) finish(c, r[i], rstd);
+      if (c < nc) finish(c, r[i], w[i], rstd);
     }
   } else {
     float r[8];
@@ -152,8 +173,10 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
     workgroup_sums(ss, none, red);
     const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
     for (int c = threadIdx.x; c < nc; c += blockDim.x) {
+      float w[8];
       load(c, r);
-      finish(c, r, rstd);
+      load_chunk(weight + c * 8, w);
+      finish(c, r, w, rstd);
     }
   }
 }

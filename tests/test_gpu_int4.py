@@ -104,6 +104,15 @@ def test_large_widths():
     Layer("int4g128", H=7168, E=2, K=1, I=2048, Is=2048).check(5, random_routing(5, 1, 2, seed=3))
 
 
+@pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
+def test_few_rows_on_average_many_in_one_expert(wd):
+    """The few-row kernel with an expert cut into several 16-row tiles."""
+    L = Layer(wd, 384, E=32, K=1, I=256, Is=128)
+    idx = random_routing(100, 1, 32, seed=8)
+    idx[20:] = 5
+    L.check(100, idx)
+
+
 def test_more_rows_than_tokens():
     """A caller's routing may name one expert twice for a token: more rows than the tile of a small batch."""
     L = Layer("int4g128", 256, E=4, K=4, I=128, Is=0)
