@@ -9,19 +9,21 @@
 // Backward, with g = dy * w and n = r * rstd:
 //   dr = rstd * (g - n * mean(g * n)) + dsum,   dw = sum over rows of dy * n.
 // Sums are fp32 in a fixed order.
-#include "fp8_device.hpp"
 #include "rows_device.hpp"
 
 #include <algorithm>
-#include <type_traits>
 
 namespace moe {
 
 namespace {
 
-// fp32 -> e4m3fn bits as f32_to_e4m3, with NaN kept NaN.
-__device__ __forceinline__ uint32_t e4m3_code(float v) {
-  return v != v ? 0x7Fu : f32_to_e4m3(v);
+// e4m3fn codes of four values: round to nearest even, saturated at 448, NaN
+// kept NaN (the conversion itself would make a value past 448 NaN).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  auto sat = [](float v) { return v != v ? v : __builtin_amdgcn_fmed3f(v, -448.0f, 448.0f); };
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(sat(c), sat(d), r, true);
+  return (uint32_t)r;
 }
 
 // The tile scales of fp8_device.hpp without 64-bit arithmetic, which is most
@@ -55,12 +57,8 @@ __device__ __forceinline__ uint2 quant_chunk(const float (&v)[8], bool pow2, flo
   for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   float inv;
   row_tile_scale(m, pow2, scale, inv);
-  uint32_t lo = 0, hi = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) lo |= e4m3_code(v[j] * inv) << (8 * j);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) hi |= e4m3_code(v[4 + j] * inv) << (8 * j);
-  return make_uint2(lo, hi);
+  return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
 
 // r = x + residual of one chunk, rounded as the stream stores it.
@@ -102,7 +100,8 @@ __device__ __forceinline__ void workgroup_sums(float& a, float& b, float* red) {
 // (NC = 0) are read twice.
 // sum may be x or residual itself: a thread rewrites only chunks that it
 // alone reads, after reading them.
-template <typename IO, int NC>
+// kNt: x, residual and sum pass the caches by (see kStreamBytes).
+template <typename IO, int NC, bool kNt>
 __global__ void __launch_bounds__(1024)
 add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ weight, float eps,
                    int H, IO* sum, IO* y, uint8_t* __restrict__ yq, float* __restrict__ ys,
@@ -111,7 +110,7 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
   const int64_t row = (int64_t)blockIdx.x * H;
   const int nc = H / kChunk;
   auto finish = [&](int c, float (&r)[8], const float (&w)[8], float rstd) {
-    if (sum) store_chunk(sum + row + c * 8, r);
+    if (sum) store_chunk<kNt>(sum + row + c * 8, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) r[j] = r[j] * rstd * w[j];
     if (y) store_chunk(y + row + c * 8, r);
@@ -134,13 +133,13 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nc) a[i].load(x + row + c * 8);
+      if (c < nc) a[i].template load<kNt>(x + row + c * 8);
     }
     if (residual) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
-        if (c < nc) b[i].load(residual + row + c * 8);
+        if (c < nc) b[i].template load<kNt>(residual + row + c * 8);
       }
     }
 #pragma unroll
@@ -186,7 +185,8 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
 // (NC > 0): each thread keeps its columns' weight and dw in registers, reads
 // every value once, and has the next row's loads in flight during the sums.
 // Longer rows (NC = 0) are read twice and dw is kept in `part`.
-template <typename IO, int NC>
+// kNt: the rows read pass the caches by (see kStreamBytes).
+template <typename IO, int NC, bool kNt>
 __global__ void __launch_bounds__(1024)
 add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict__ weight,
                             float eps, const IO* dy, const IO* dsum, int64_t rows, int H, IO* dx,
@@ -203,8 +203,8 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
       for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         if (c >= nc) break;
-        nr[i].load(sum + t * H + c * 8);
-        ng[i].load(dy + t * H + c * 8);
+        nr[i].template load<kNt>(sum + t * H + c * 8);
+        ng[i].template load<kNt>(dy + t * H + c * 8);
       }
     };
     fetch(blockIdx.x);   // the grid has at most `rows` workgroups
@@ -227,7 +227,7 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
           const int c = threadIdx.x + i * blockDim.x;
-          if (c < nc) d[i].load(dsum + t * H + c * 8);
+          if (c < nc) d[i].template load<kNt>(dsum + t * H + c * 8);
         }
       }
       if (t + gridDim.x < rows) fetch(t + gridDim.x);
@@ -351,7 +351,18 @@ int norm_threads(int H, int nc) {
   return std::min(1024, (H / kChunk + 64 * nc - 1) / (64 * nc) * 64);
 }
 
-constexpr int64_t kNormParts = 512;   // row sums of dw kept apart at most
+// Row sums of dw kept apart at most: two workgroups per CU (256 instead of 512
+// take 61 us instead of 55 at T = 4096, H = 7168).
+constexpr int64_t kNormParts = 512;
+
+// Arrays of rows past this size are read (and the sum written)
+// non-temporally.  Measured at H = 7168, bf16, cached -> non-temporal: forward
+// 12.7 -> 13.4 us at 15 MB an array, 26.4 -> 25.0 at 29 MB, 46.5 -> 42.7 at
+// 59 MB; backward 20.2 -> 23.1, 32.2 -> 30.7, 53.9 -> 48.7 us.  With a kernel
+// before that writes x or dy and one after that reads y or dx the three stay
+// within 1% of each other from 29 MB on (95.0 -> 94.3 and 100.3 -> 100.7 us at
+// 59 MB).
+constexpr int64_t kStreamBytes = 24000000;
 
 }  // namespace
 
@@ -359,25 +370,27 @@ size_t rmsnorm_backward_ws_bytes(int64_t rows, int H) {
   return ((size_t)std::min(rows, kNormParts) * H * sizeof(float) + 255) / 256 * 256;
 }
 
+template <typename IO, int NC, bool kNt>
+static void add_rmsnorm(const void* x, const void* residual, const float* weight, float eps,
+                        int64_t rows, int H, void* sum, void* y, uint8_t* yq, float* ys,
+                        bool pow2, hipStream_t s) {
+  MOE_TIMED_LAUNCH(s, "add_rmsnorm_kernel",
+    hipLaunchKernelGGL((add_rmsnorm_kernel<IO, NC, kNt>), dim3((unsigned)rows),
+                       dim3(norm_threads(H, NC ? NC : 4)), 0, s, (const IO*)x,
+                       (const IO*)residual, weight, eps, H, (IO*)sum, (IO*)y, yq, ys, pow2));
+}
+
 // Chunks of a row that a thread holds in registers: two, four from H = 16384
 // on, none (the row is read twice) past 32768.
-#define MOE_NORM_BY_WIDTH(H, call) \
-  ((H) <= 16384 ? call(2) : (H) <= 32768 ? call(4) : call(0))
-
 template <typename IO>
 static hipError_t add_rmsnorm(const void* x, const void* residual, const float* weight, float eps,
                               int64_t rows, int H, void* sum, void* y, uint8_t* yq, float* ys,
                               bool pow2, hipStream_t s) {
-  auto run = [&](auto nc) {
-    constexpr int NC = decltype(nc)::value;
-    MOE_TIMED_LAUNCH(s, "add_rmsnorm_kernel",
-      hipLaunchKernelGGL((add_rmsnorm_kernel<IO, NC>), dim3((unsigned)rows),
-                         dim3(norm_threads(H, NC ? NC : 4)), 0, s, (const IO*)x,
-                         (const IO*)residual, weight, eps, H, (IO*)sum, (IO*)y, yq, ys, pow2));
-  };
-#define MOE_CALL(nc) run(std::integral_constant<int, nc>{})
-  MOE_NORM_BY_WIDTH(H, MOE_CALL);
-#undef MOE_CALL
+  auto* run = H > 32768   ? add_rmsnorm<IO, 0, false>
+              : H > 16384 ? add_rmsnorm<IO, 4, false>
+              : rows * H * (int64_t)sizeof(IO) > kStreamBytes ? add_rmsnorm<IO, 2, true>
+                                                              : add_rmsnorm<IO, 2, false>;
+  run(x, residual, weight, eps, rows, H, sum, y, yq, ys, pow2, s);
   return hipGetLastError();
 }
 
@@ -394,19 +407,18 @@ static hipError_t add_rmsnorm_backward(const void* sum, const float* weight, flo
                                        void* dx, float* dweight, float* part, hipStream_t s) {
   const int64_t parts = std::min(rows, kNormParts);
   if (parts) {
-    auto run = [&](auto nc) {
-      constexpr int NC = decltype(nc)::value;
-      MOE_TIMED_LAUNCH(s, "add_rmsnorm_backward_kernel",
-        hipLaunchKernelGGL((add_rmsnorm_backward_kernel<IO, NC>), dim3((unsigned)parts),
-                           dim3(norm_threads(H, NC ? NC : 4)), 0, s, (const IO*)sum, weight, eps,
-                           (const IO*)dy, (const IO*)dsum, rows, H, (IO*)dx, part));
-    };
-    // wider rows leave no registers for a thread's share of dw
+    // Two chunks a thread in bf16, one in fp32; wider rows leave no registers
+    // for a thread's share of dw.
     constexpr int NC = sizeof(IO) == 2 ? 2 : 1;
-    if (H <= 1024 * NC * kChunk)
-      run(std::integral_constant<int, NC>{});
-    else
-      run(std::integral_constant<int, 0>{});
+    const bool wide = H > 1024 * NC * kChunk;
+    auto* kernel = wide ? add_rmsnorm_backward_kernel<IO, 0, false>
+                   : rows * H * (int64_t)sizeof(IO) > kStreamBytes
+                       ? add_rmsnorm_backward_kernel<IO, NC, true>
+                       : add_rmsnorm_backward_kernel<IO, NC, false>;
+    MOE_TIMED_LAUNCH(s, "add_rmsnorm_backward_kernel",
+      hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(norm_threads(H, wide ? 4 : NC)), 0, s,
+                         (const IO*)sum, weight, eps, (const IO*)dy, (const IO*)dsum, rows, H,
+                         (IO*)dx, part));
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -22,23 +22,38 @@ __device__ __forceinline__ u32x4 pack_bf16x8(const float (&f)[8]) {
                  pack_bf16x2(f[6], f[7])};
 }
 
+// 16 bytes; kNt: non-temporal, for data that is not used again soon.
+template <bool kNt, typename V>
+__device__ __forceinline__ V load16(const V* p) {
+  return kNt ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool kNt, typename V>
+__device__ __forceinline__ void store16(V* p, V v) {
+  if (kNt)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
 // A chunk as it lies in memory.
 template <typename IO>
 struct RawChunk;
 template <>
 struct RawChunk<uint16_t> {
   u32x4 v;
+  template <bool kNt = false>
   __device__ __forceinline__ void load(const uint16_t* p) {
-    v = *reinterpret_cast<const u32x4*>(p);
+    v = load16<kNt>(reinterpret_cast<const u32x4*>(p));
   }
   __device__ __forceinline__ void to(float (&f)[8]) const { unpack_bf16x8(v, f); }
 };
 template <>
 struct RawChunk<float> {
   f32x4 a, b;
+  template <bool kNt = false>
   __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const f32x4*>(p);
-    b = *reinterpret_cast<const f32x4*>(p + 4);
+    a = load16<kNt>(reinterpret_cast<const f32x4*>(p));
+    b = load16<kNt>(reinterpret_cast<const f32x4*>(p + 4));
   }
   __device__ __forceinline__ void to(float (&f)[8]) const {
 #pragma unroll
@@ -56,12 +71,14 @@ __device__ __forceinline__ void load_chunk(const IO* p, float (&f)[8]) {
   r.to(f);
 }
 
+template <bool kNt = false>
 __device__ __forceinline__ void store_chunk(uint16_t* p, const float (&f)[8]) {
-  *reinterpret_cast<u32x4*>(p) = pack_bf16x8(f);
+  store16<kNt>(reinterpret_cast<u32x4*>(p), pack_bf16x8(f));
 }
+template <bool kNt = false>
 __device__ __forceinline__ void store_chunk(float* p, const float (&f)[8]) {
-  *reinterpret_cast<f32x4*>(p) = (f32x4){f[0], f[1], f[2], f[3]};
-  *reinterpret_cast<f32x4*>(p + 4) = (f32x4){f[4], f[5], f[6], f[7]};
+  store16<kNt>(reinterpret_cast<f32x4*>(p), (f32x4){f[0], f[1], f[2], f[3]});
+  store16<kNt>(reinterpret_cast<f32x4*>(p + 4), (f32x4){f[4], f[5], f[6], f[7]});
 }
 
 // v as a row of type IO holds it.
@@ -74,23 +91,6 @@ __device__ __forceinline__ float as_stored<uint16_t>(float v) {
 template <>
 __device__ __forceinline__ float as_stored<float>(float v) {
   return v;
-}
-
-// Sum of v over the NT threads of a workgroup in a fixed order (wave
-// shuffles, then the waves in order); every thread gets the result.  red
-// holds NT / 64 floats; every thread calls this.
-template <int NT>
-__device__ __forceinline__ float workgroup_sum(float v, float* red) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  if (NT == 64) return v;
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int w = 0; w < NT / 64; ++w) s += red[w];
-  __syncthreads();
-  return s;
 }
 
 }  // namespace moe
