@@ -32,8 +32,9 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 # result) to the fp32 accumulator with vector FMAs; with the MFMA results
 # kept in VGPRs the compiler no longer copies every partial out of the
 # accumulation registers first (about half of that kernel's vector
-# instructions, 5-7% of its time).
-FILE_FLAGS = {"ffn_fp8_packed.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# instructions, 5-7% of its time).  The 4-bit GEMMs do the same per scale group.
+FILE_FLAGS = {"ffn_fp8_packed.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "ffn_int4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 RESOURCE_REMARKS = "-Rpass-analysis=kernel-resource-usage"
 

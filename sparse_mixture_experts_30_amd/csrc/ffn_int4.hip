@@ -41,8 +41,11 @@ constexpr int kFrags = 8;            // 16-row fragments per tile
 constexpr __host__ __device__ int step_units(int group) { return kCodes16 + 16 * (kStepK / group); }
 
 struct Int4Args {
-  const int32_t* tiles;
-  int ntn;                      // output tiles per M-tile (max over groups)
+  const int32_t* offsets;
+  int routed;                   // whether the routed experts are computed
+  int per;                      // experts per lane in find_item, ceil(E / 64)
+  int shared_rows;              // T, or 0 without the shared expert
+  int ntn;                      // items per M-tile (max over groups)
   int E, K;
   const uint16_t* a_r;
   const uint16_t* a_s;
@@ -66,13 +69,14 @@ __device__ __forceinline__ bf16x8 codes_bf16(uint32_t d) {
   return as_bf16x8(r);
 }
 
-// The eight scales of a vector as fp32.
-__device__ __forceinline__ void scales_f32(u32x4 v, float (&s)[kFrags]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s[2 * i] = __uint_as_float(v[i] << 16);
-    s[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-  }
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Four bf16 scales as fp32.
+__device__ __forceinline__ void scales_f32(uint2 v, float* s) {
+  s[0] = __uint_as_float(v.x << 16);
+  s[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  s[2] = __uint_as_float(v.y << 16);
+  s[3] = __uint_as_float(v.y & 0xFFFF0000u);
 }
 
 __device__ __forceinline__ bf16x8 minus_136() {
@@ -83,14 +87,100 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// This workgroup's output tile and rows.  Group g < E is routed expert g with
+// rows [offsets[g], offsets[g + 1]), group E the shared expert with all T
+// tokens; a group of n rows is cut into mt = ceil(n / kRows) M-tiles of equal
+// height (+-1 row).  Items are numbered group by group, in a group N-tile by
+// N-tile, so the M-tiles that share a weight tile run together, and dealt to
+// the XCDs in chunks (as xcd_chunked).  Every wave finds its item itself from
+// the offsets, a few experts a lane and a scan over the lanes: a list made by
+// a kernel of its own costs that kernel's 4 us in every call.
+__device__ __forceinline__ uint32_t wave_inclusive_scan(uint32_t v) {
+  // Data-parallel moves: within each row of 16 lanes by 1, 2, 4, 8 (lanes
+  // without a source add 0), then the last lane of row 0 / 2 to row 1 / 3 and
+  // of row 1 to rows 2 and 3.
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x111, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x142, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xc, 0xf, false);
+  return v;
+}
+
+struct Item {
+  int g, row0, nrows, ntile;
+  bool alone;   // the only M-tile of its group
+};
+template <int kRows>
+__device__ __forceinline__ bool find_item(const Int4Args& p, Item& it) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t b = blockIdx.x, q = b / kNumXcd;
+  const uint32_t w = ((q / kXcdChunk) * kNumXcd + b % kNumXcd) * kXcdChunk + q % kXcdChunk;
+  const uint32_t i0 = w / (uint32_t)p.ntn;   // M-tile the item would be if each had ntn items
+  auto tiles_of = [](int32_t n) { return (uint32_t)(n + kRows - 1) / kRows; };
+  // M-tiles of this lane's experts, and the end of its range of M-tiles
+  uint32_t mine = 0;
+  int32_t from = 0;
+  if (p.routed) {
+    from = p.offsets[min(lane * p.per, p.E)];
+    int32_t o = from;
+    for (int j = 1; j <= p.per; ++j) {
+      const int32_t next = p.offsets[min(lane * p.per + j, p.E)];
+      mine += tiles_of(next - o);
+      o = next;
+    }
+  }
+  const uint32_t end = wave_inclusive_scan(mine);
+  const uint32_t routed = __builtin_amdgcn_readlane(end, 63);
+  int32_t g, n, r0;
+  uint32_t L;
+  if (i0 < routed) {
+    const int src = __builtin_ctzll(__ballot(end > i0));
+    // that lane's experts one by one, on the scalar unit
+    g = src * p.per;
+    L = __builtin_amdgcn_readlane(end - mine, src);
+    r0 = __builtin_amdgcn_readlane(from, src);
+    for (;; ++g) {
+      const int32_t next = p.offsets[g + 1];
+      n = next - r0;
+      if (i0 < L + tiles_of(n) || g + 1 >= p.E) break;
+      L += tiles_of(n);
+      r0 = next;
+    }
+  } else {
+    g = p.E;
+    n = p.shared_rows;
+    r0 = 0;
+    L = routed;
+    if (i0 >= routed + tiles_of(n)) return false;
+  }
+  const uint32_t mt = tiles_of(n), local = w - L * (uint32_t)p.ntn;
+  if (mt == 1) {
+    it = {g, r0, n, (int)local, true};
+    return true;
+  }
+  const uint32_t m = local % mt;
+  const int32_t first = (int32_t)((uint64_t)m * n / mt),
+                last = (int32_t)((uint64_t)(m + 1) * n / mt);
+  it = {g, r0 + first, last - first, (int)(local / mt), false};
+  return true;
+}
+
 // ---------------------------------------------------------------- few rows
 // A tile of at most 16 rows: wave w takes a quarter of the k steps, D of them
 // in flight, and the four waves' sums are joined through LDS in wave order.
 constexpr int kFewRows = 16;
+constexpr int kFewFrags = 8;    // weight fragments of a workgroup
+constexpr int kFewDepth = 1;    // k steps in flight
+constexpr int kFewWaves = 4;    // waves that share the k steps
+constexpr int kFewThreads = 64 * kFewWaves;
 
-template <bool kGateUp, int kGroup, int D, bool kStream>
+template <bool kGateUp, int kGroup, bool kStream>
 __device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int g, int row0,
-                                              int nrows, int ntile) {
+                                              int nrows, int part_tile) {
+  constexpr int D = kFewDepth, FR = kFewFrags, kParts = kFrags / FR;
+  const int ntile = part_tile / kParts, f0 = part_tile % kParts * FR;   // packed tile, first fragment
   constexpr int kUnits = step_units(kGroup);
   constexpr int kScales = kStepK / kGroup;   // scale vectors per step
   constexpr int kF = 4 / kScales;            // k fragments per group
@@ -98,19 +188,25 @@ __device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
   const int nsteps = (sh ? p.kdim_s : p.kdim_r) / kStepK;
-  const int s0 = nsteps * wave / 4, s1 = nsteps * (wave + 1) / 4;
+  const int s0 = nsteps * wave / kFewWaves, s1 = nsteps * (wave + 1) / kFewWaves;
   const u32x4* bw = (sh ? p.b_s : p.b_r + (int64_t)g * p.nt_r * nsteps * kUnits) +
                     (int64_t)ntile * nsteps * kUnits;
 
-  u32x4 rb[D][kFrags], sc[D][kScales], ra[D][4];
+  u32x4 rb[D][FR], ra[D][4];
+  uint2 sc[D][kScales][FR / 4];
   // Steps past the wave's last one load its last one again.
   auto load_w = [&](int slot, int step) {
     const u32x4* src = bw + (int64_t)min(step, nsteps - 1) * kUnits;
 #pragma unroll
-    for (int b = 0; b < kFrags; ++b)
-      rb[slot][b] = kStream ? __builtin_nontemporal_load(src + b * 64 + lane) : src[b * 64 + lane];
+    for (int b = 0; b < FR; ++b)
+      rb[slot][b] = kStream ? __builtin_nontemporal_load(src + (f0 + b) * 64 + lane)
+                            : src[(f0 + b) * 64 + lane];
 #pragma unroll
-    for (int q = 0; q < kScales; ++q) sc[slot][q] = src[kCodes16 + q * 16 + lr];
+    for (int q = 0; q < kScales; ++q)
+#pragma unroll
+      for (int j = 0; j < FR / 4; ++j)
+        sc[slot][q][j] =
+            reinterpret_cast<const uint2*>(src + kCodes16 + q * 16 + lr)[f0 / 4 + j];
   };
 #pragma unroll
   for (int d = 0; d < D; ++d) load_w(d, s0 + d);
@@ -127,23 +223,24 @@ __device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int
 #pragma unroll
   for (int d = 0; d < D; ++d) load_a(d, s0 + d);
 
-  f32x4 acc[kFrags];
+  f32x4 acc[FR];
 #pragma unroll
-  for (int b = 0; b < kFrags; ++b) acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < FR; ++b) acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
   for (int s = s0; s < s1; s += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       if (s + d < s1) {
 #pragma unroll
         for (int q = 0; q < kScales; ++q) {
-          float sv[kFrags];
-          scales_f32(sc[d][q], sv);
+          float sv[FR];
+#pragma unroll
+          for (int j = 0; j < FR / 4; ++j) scales_f32(sc[d][q][j], sv + 4 * j);
           f32x4 corr = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int f = q * kF; f < (q + 1) * kF; ++f)
             corr = mfma16(as_bf16x8(ra[d][f]), minus_136(), corr);
 #pragma unroll
-          for (int b = 0; b < kFrags; ++b) {
+          for (int b = 0; b < FR; ++b) {
             f32x4 part = corr;
 #pragma unroll
             for (int f = q * kF; f < (q + 1) * kF; ++f)
@@ -160,54 +257,55 @@ __device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int
 
   // [wave][frag][row 16][col 16]
 #pragma unroll
-  for (int b = 0; b < kFrags; ++b)
+  for (int b = 0; b < FR; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      lds[((wave * kFrags + b) * 16 + 4 * lq + i) * 16 + lr] = acc[b][i];
+      lds[((wave * FR + b) * 16 + 4 * lq + i) * 16 + lr] = acc[b][i];
   __syncthreads();
   const int row = tid >> 4;
-  if (row >= nrows) return;
+  if (row >= min(nrows, kFewRows)) return;   // 16 threads a row
   uint16_t* crow = (sh ? p.c_s : p.c_r) + (int64_t)(row0 + row) * (sh ? p.ldc_s : p.ldc_r);
   auto joined = [&](int b, int col) {
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    f32x2 v = {0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
-      v += *reinterpret_cast<const f32x4*>(lds + ((w * kFrags + b) * 16 + row) * 16 + col);
+    for (int w = 0; w < kFewWaves; ++w)
+      v += *reinterpret_cast<const f32x2*>(lds + ((w * FR + b) * 16 + row) * 16 + col);
     return v;
   };
+  // two h columns, or four outputs, per four fragments
   if (kGateUp) {
-    const int col = (tid & 15) * 4, b = (col >> 5) * 4 + (col >> 4 & 1);
-    const f32x4 gv = joined(b, col & 15), uv = joined(b + 2, col & 15);
-    float h[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = gv[j] / (1.0f + __expf(-gv[j])) * uv[j];
-    *reinterpret_cast<uint2*>(crow + ntile * 64 + col) =
-        make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+    for (int j = 0; j < FR / 4; ++j) {
+      const int col = (tid & 15) * 2, b = 4 * j + (col >> 4);
+      const f32x2 gv = joined(b, col & 15), uv = joined(b + 2, col & 15);
+      float h[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) h[i] = gv[i] / (1.0f + __expf(-gv[i])) * uv[i];
+      *reinterpret_cast<uint32_t*>(crow + ntile * 64 + f0 * 8 + 32 * j + col) =
+          pack_bf16x2(h[0], h[1]);
+    }
   } else {
-    const int col = (tid & 15) * 8, b = col >> 4;
-    const f32x4 v = joined(b, col & 15), w = joined(b, (col & 15) + 4);
-    *reinterpret_cast<u32x4*>(crow + ntile * 128 + col) =
-        (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(w[0], w[1]),
-                pack_bf16x2(w[2], w[3])};
+#pragma unroll
+    for (int j = 0; j < FR / 4; ++j) {
+      const int col = (tid & 15) * 4, b = 4 * j + (col >> 4);
+      const f32x2 v = joined(b, col & 15), w = joined(b, (col & 15) + 2);
+      *reinterpret_cast<uint2*>(crow + ntile * 128 + f0 * 16 + 64 * j + col) =
+          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(w[0], w[1]));
+    }
   }
 }
 
 template <bool kGateUp, int kGroup>
-__global__ void __launch_bounds__(kThreads4) grouped_gemm_int4_few(Int4Args p) {
-  __shared__ __align__(16) float lds[4 * kFrags * 256];
-  constexpr int D = 2;
-  const int64_t work = (int64_t)p.tiles[0] * p.ntn;
-  const int64_t w = xcd_chunked(blockIdx.x, work);
-  if (w < 0) return;
-  int ntile;
-  const int32_t* ent = decode_work(p.tiles, w, p.ntn, ntile);
-  const int g = ent[0], row0 = ent[1], nrows = ent[2];
-  if (ntile >= (g == p.E ? p.nt_s : p.nt_r)) return;
+__global__ void __launch_bounds__(kFewThreads) grouped_gemm_int4_few(Int4Args p) {
+  __shared__ __align__(16) float lds[kFewWaves * kFewFrags * 256];
+  Item it;
+  if (!find_item<kFewRows>(p, it)) return;
+  if (it.ntile >= (kFrags / kFewFrags) * (it.g == p.E ? p.nt_s : p.nt_r)) return;
   // A weight tile that only this row tile reads is not kept in cache.
-  if (ent[4] == 1)
-    int4_few_tile<kGateUp, kGroup, D, true>(p, lds, g, row0, nrows, ntile);
+  if (it.alone)
+    int4_few_tile<kGateUp, kGroup, true>(p, lds, it.g, it.row0, it.nrows, it.ntile);
   else
-    int4_few_tile<kGateUp, kGroup, D, false>(p, lds, g, row0, nrows, ntile);
+    int4_few_tile<kGateUp, kGroup, false>(p, lds, it.g, it.row0, it.nrows, it.ntile);
 }
 
 // --------------------------------------------------------------- many rows
@@ -215,6 +313,8 @@ __global__ void __launch_bounds__(kThreads4) grouped_gemm_int4_few(Int4Args p) {
 // fragments over the whole k range, the rows' activations pass through two
 // LDS buffers in fragment order (lane-linear 16-byte reads and writes).
 constexpr int kManyRows = 64;
+constexpr int kManyDepth = 2;    // weight steps in flight
+constexpr int kManyWaves = 2;    // waves per SIMD
 
 template <bool kGateUp, int kGroup, int NRB, bool kStream>
 __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, int g, int row0,
@@ -222,7 +322,7 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   constexpr int kUnits = step_units(kGroup);
   constexpr int kScales = kStepK / kGroup;
   constexpr int kF = 4 / kScales;
-  constexpr int D = 2;                       // weight steps in flight
+  constexpr int D = kManyDepth;
   const bool sh = (g == p.E);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
@@ -278,9 +378,9 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   load_a(1);
   __syncthreads();
 
-  for (int s = 0; s < nsteps; s += D) {
+  for (int s = 0; s < nsteps; s += 2) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
+    for (int d = 0; d < 2; ++d) {   // d: the LDS buffer
       if (s + d < nsteps) {   // the same for the whole workgroup
 #pragma unroll
         for (int q = 0; q < kScales; ++q) {
@@ -290,10 +390,8 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
 #pragma unroll
             for (int f = 0; f < kF; ++f)
               a[r][f] = lds[((d * NRB + r) * 4 + q * kF + f) * 64 + lane];
-          const float sv[4] = {__uint_as_float(sc[d][q].x << 16),
-                               __uint_as_float(sc[d][q].x & 0xFFFF0000u),
-                               __uint_as_float(sc[d][q].y << 16),
-                               __uint_as_float(sc[d][q].y & 0xFFFF0000u)};
+          float sv[4];
+          scales_f32(sc[d % D][q], sv);
           f32x4 corr[NRB];
 #pragma unroll
           for (int r = 0; r < NRB; ++r) {
@@ -307,7 +405,7 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
             f32x4 part[NRB];
 #pragma unroll
             for (int f = 0; f < kF; ++f) {
-              const bf16x8 w = codes_bf16(rb[d][b][q * kF + f]);
+              const bf16x8 w = codes_bf16(rb[d % D][b][q * kF + f]);
 #pragma unroll
               for (int r = 0; r < NRB; ++r)
                 part[r] = mfma16(as_bf16x8(a[r][f]), w, f == 0 ? corr[r] : part[r]);
@@ -318,7 +416,7 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
               for (int i = 0; i < 4; ++i) acc[r][b][i] = fmaf(sv[b], part[r][i], acc[r][b][i]);
           }
         }
-        load_w(d, s + d + D);
+        load_w(d % D, s + d + D);
         store_a(d ^ 1);      // read again after the barrier; last read before the previous one
         load_a(s + d + 2);
         __syncthreads();
@@ -361,16 +459,13 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
 }
 
 template <bool kGateUp, int kGroup>
-__global__ void __launch_bounds__(kThreads4, 2) grouped_gemm_int4_many(Int4Args p) {
+__global__ void __launch_bounds__(kThreads4, kManyWaves) grouped_gemm_int4_many(Int4Args p) {
   __shared__ u32x4 lds[2 * (kManyRows / 16) * 4 * 64];   // 32 KiB
-  const int64_t work = (int64_t)p.tiles[0] * p.ntn;
-  const int64_t w = xcd_chunked(blockIdx.x, work);
-  if (w < 0) return;
-  int npair;
-  const int32_t* ent = decode_work(p.tiles, w, p.ntn, npair);
-  const int g = ent[0], row0 = ent[1], nrows = ent[2];
+  Item it;
+  if (!find_item<kManyRows>(p, it)) return;
+  const int g = it.g, row0 = it.row0, nrows = it.nrows, npair = it.ntile;
   if (2 * npair >= (g == p.E ? p.nt_s : p.nt_r)) return;
-  switch (((nrows + 15) >> 4) * 2 + (ent[4] == 1 ? 1 : 0)) {
+  switch (((nrows + 15) >> 4) * 2 + (it.alone ? 1 : 0)) {
 #define MOE_INT4_CASE(n)                                                               \
     case 2 * n:                                                                        \
       int4_many_tile<kGateUp, kGroup, n, false>(p, lds, g, row0, nrows, npair);        \
@@ -470,33 +565,34 @@ quantize_int4_kernel(int group, const uint16_t* __restrict__ src, int64_t chunks
   if (c % (group / 8) == 0) scales[c * 8 / group] = (uint16_t)sb;
 }
 
+// nt: packed tiles of the group with the most of them.
 template <bool kGateUp, int kGroup>
-hipError_t launch_gemm(Int4Args a, bool few, int64_t mtiles, hipStream_t s) {
-  if (few) {
+hipError_t launch_gemm(Int4Args a, bool few, int64_t mtiles, int nt, hipStream_t s) {
+  a.ntn = few ? nt * (kFrags / kFewFrags) : (nt + 1) / 2;
+  const int64_t work = mtiles * a.ntn;
+  if (work > 0x7fffffff - kXcdGrid) return hipErrorInvalidValue;
+  if (few)
     MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_few<true>" : "grouped_gemm_int4_few<false>",
-      hipLaunchKernelGGL((grouped_gemm_int4_few<kGateUp, kGroup>), dim3(xcd_grid(mtiles * a.ntn)),
-                         dim3(kThreads4), 0, s, a));
-  } else {
-    a.ntn = (a.ntn + 1) / 2;
+      hipLaunchKernelGGL((grouped_gemm_int4_few<kGateUp, kGroup>), dim3(xcd_grid(work)),
+                         dim3(kFewThreads), 0, s, a));
+  else
     MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_many<true>" : "grouped_gemm_int4_many<false>",
-      hipLaunchKernelGGL((grouped_gemm_int4_many<kGateUp, kGroup>), dim3(xcd_grid(mtiles * a.ntn)),
+      hipLaunchKernelGGL((grouped_gemm_int4_many<kGateUp, kGroup>), dim3(xcd_grid(work)),
                          dim3(kThreads4), 0, s, a));
-  }
   return hipGetLastError();
 }
 
-// The few-row kernel up to kFewAverage rows per expert on average.
-constexpr int kFewAverage = 4;
+// The few-row kernel takes batches of up to kFewAverage rows per expert on
+// average, and those whose work would leave CUs idle in the other one (its
+// waves split the k steps, so it makes more and shorter workgroups).
+constexpr int kFewAverage = 8;
+constexpr int64_t kManyGrid = 512;
 bool use_few(const FfnDims& d) {
-  return d.T <= kFewRows || d.N <= (int64_t)kFewAverage * d.E;
+  return d.T <= kFewRows || d.N <= (int64_t)kFewAverage * d.E ||
+         ffn_grid_mtiles(d, kManyRows) * (d.I / 128) < kManyGrid;
 }
-int tile_rows(const FfnDims& d) { return use_few(d) ? kFewRows : kManyRows; }
 
 }  // namespace
-
-size_t int4_tiles_bytes(const FfnDims& d) {
-  return (size_t)(8 + 8 * ffn_max_mtiles(d.N, d.T, d.E, tile_rows(d))) * sizeof(int32_t);
-}
 
 size_t packed4_bytes(bool gate_up, int64_t experts, int n, int kd, int group) {
   const int64_t nt = gate_up ? n / 64 : n / 128;
@@ -524,19 +620,18 @@ hipError_t launch_quantize_int4(int group, const uint16_t* src, int64_t rows, in
 
 hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const int32_t* perm,
                            const int32_t* offsets, const void* w13p, const void* w2p,
-                           const void* ws13p, const void* ws2p, uint16_t* h, int32_t* tiles,
-                           uint16_t* y, uint16_t* ys, hipStream_t s) {
+                           const void* ws13p, const void* ws2p, uint16_t* h, uint16_t* y,
+                           uint16_t* ys, hipStream_t s) {
   const bool few = use_few(d);
-  const int bm = tile_rows(d);
-  hipError_t e = ffn_build_tiles(d, offsets, bm, tiles, s, true);
-  if (e != hipSuccess) return e;
-  const int64_t mt = ffn_grid_mtiles(d, bm);
+  const int64_t mt = ffn_grid_mtiles(d, few ? kFewRows : kManyRows);
 
   Int4Args a{};
-  a.tiles = tiles;
+  a.offsets = offsets;
+  a.routed = d.groups & kGroupRouted;
+  a.per = (d.E + kWave - 1) / kWave;
+  a.shared_rows = (d.groups & kGroupShared) && d.Is > 0 ? (int)d.T : 0;
   a.nt_r = d.I / 64;
   a.nt_s = d.Is / 64;
-  a.ntn = std::max(a.nt_r, a.nt_s);
   a.E = d.E;
   a.K = d.K;
   a.a_r = a.a_s = x;
@@ -549,11 +644,12 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
   a.c_s = h + d.N * d.I;
   a.ldc_r = d.I;
   a.ldc_s = d.Is;
-  e = group == 32 ? launch_gemm<true, 32>(a, few, mt, s)
-                  : launch_gemm<true, 128>(a, few, mt, s);
+  const int nt1 = std::max(a.nt_r, a.nt_s);
+  hipError_t e = group == 32 ? launch_gemm<true, 32>(a, few, mt, nt1, s)
+                             : launch_gemm<true, 128>(a, few, mt, nt1, s);
   if (e != hipSuccess) return e;
 
-  a.nt_r = a.nt_s = a.ntn = d.H / 128;
+  a.nt_r = a.nt_s = d.H / 128;
   a.a_s = h + d.N * d.I;
   a.a_r = h;
   a.lda_r = a.kdim_r = d.I;
@@ -563,8 +659,8 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
   a.c_r = y;
   a.c_s = ys;
   a.ldc_r = a.ldc_s = d.H;
-  return group == 32 ? launch_gemm<false, 32>(a, few, mt, s)
-                     : launch_gemm<false, 128>(a, few, mt, s);
+  return group == 32 ? launch_gemm<false, 32>(a, few, mt, a.nt_r, s)
+                     : launch_gemm<false, 128>(a, few, mt, a.nt_r, s);
 }
 
 }  // namespace moe

@@ -123,7 +123,7 @@ Layout layout(const moe_config* c, int64_t T) {
   L.pos = take((size_t)N * 4);
   L.hist = take((size_t)moe::permute_nblk(N) * (E + 1) * 4);
   moe::FfnDims d{T, N, (int)H, (int)I, (int)Is, (int)E, (int)K};
-  const size_t tiles = is_int4(c->weight_dtype) ? moe::int4_tiles_bytes(d) : moe::ffn_tiles_bytes(d);
+  const size_t tiles = moe::ffn_tiles_bytes(d);
   L.tiles = take(tiles);
   L.tiles2 = take(tiles);   // the shared expert's list on a second stream
   const size_t hel = (size_t)(N * I + T * Is);
@@ -253,7 +253,7 @@ moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t*
     case MOE_INT4_G32:
       HIPCALL(moe::launch_ffn_int4(d, int4_group(c->weight_dtype), (const uint16_t*)x, perm,
                                    offsets, wt->w13, wt->w2, wt->ws13, wt->ws2,
-                                   at<uint16_t>(ws, L.h), tiles, (uint16_t*)y, (uint16_t*)ys, s),
+                                   at<uint16_t>(ws, L.h), (uint16_t*)y, (uint16_t*)ys, s),
               "ffn int4");
       break;
     case MOE_FP8_E4M3_E8M0: {

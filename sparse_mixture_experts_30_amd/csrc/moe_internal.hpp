@@ -272,8 +272,7 @@ hipError_t launch_ffn_backward_fp8(const FfnDims& d, bool pow2, const uint16_t* 
                                    uint16_t* dws2, void* ws, hipStream_t s);
 
 // Expert FFNs on packed 4-bit weights with group scales (ffn_int4.hip);
-// group is 128 or 32.  The tile list needs int4_tiles_bytes.
-size_t int4_tiles_bytes(const FfnDims& d);
+// group is 128 or 32.  No tile list.
 size_t packed4_bytes(bool gate_up, int64_t experts, int n, int kd, int group);
 hipError_t launch_pack_int4(bool gate_up, int group, const uint8_t* codes, const uint16_t* scales,
                             void* dst, int64_t experts, int n, int kd, hipStream_t s);
@@ -281,8 +280,8 @@ hipError_t launch_quantize_int4(int group, const uint16_t* src, int64_t rows, in
                                 uint8_t* codes, uint16_t* scales, hipStream_t s);
 hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const int32_t* perm,
                            const int32_t* offsets, const void* w13p, const void* w2p,
-                           const void* ws13p, const void* ws2p, uint16_t* h, int32_t* tiles,
-                           uint16_t* y, uint16_t* ys, hipStream_t s);
+                           const void* ws13p, const void* ws2p, uint16_t* h, uint16_t* y,
+                           uint16_t* ys, hipStream_t s);
 
 // Residual add + RMS norm and its backward (norm.hip).
 hipError_t launch_add_rmsnorm(const void* x, const void* residual, const float* weight, float eps,
