@@ -61,11 +61,23 @@ struct Int4Args {
   int64_t ldc_r, ldc_s;
 };
 
-// Codes of dword d as bf16 operands 128 + u.
-__device__ __forceinline__ bf16x8 codes_bf16(uint32_t d) {
+// Codes of dword d as bf16 operands 128 + u.  The constants come from
+// registers that the compiler cannot see through (code_constants): with
+// literals it splits every AND-OR into two instructions, and unpacking is
+// most of these kernels' vector work (11 instead of 7 instructions a dword).
+struct CodeConstants {
+  uint32_t mask, one28;
+};
+__device__ __forceinline__ CodeConstants code_constants() {
+  CodeConstants c;
+  asm("s_mov_b32 %0, 0x000f000f" : "=s"(c.mask));
+  asm("v_mov_b32 %0, 0x43004300" : "=v"(c.one28));
+  return c;
+}
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t d, const CodeConstants& c) {
   u32x4 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = ((d >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  for (int i = 0; i < 4; ++i) r[i] = ((d >> (4 * i)) & c.mask) | c.one28;
   return as_bf16x8(r);
 }
 
@@ -223,6 +235,7 @@ __device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int
 #pragma unroll
   for (int d = 0; d < D; ++d) load_a(d, s0 + d);
 
+  const CodeConstants cc = code_constants();
   f32x4 acc[FR];
 #pragma unroll
   for (int b = 0; b < FR; ++b) acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -244,7 +257,7 @@ __device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int
             f32x4 part = corr;
 #pragma unroll
             for (int f = q * kF; f < (q + 1) * kF; ++f)
-              part = mfma16(as_bf16x8(ra[d][f]), codes_bf16(rb[d][b][f]), part);
+              part = mfma16(as_bf16x8(ra[d][f]), codes_bf16(rb[d][b][f], cc), part);
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[b][i] = fmaf(sv[b], part[i], acc[b][i]);
           }
@@ -313,7 +326,9 @@ __global__ void __launch_bounds__(kFewThreads) grouped_gemm_int4_few(Int4Args p)
 // fragments over the whole k range, the rows' activations pass through two
 // LDS buffers in fragment order (lane-linear 16-byte reads and writes).
 constexpr int kManyRows = 64;
-constexpr int kManyDepth = 2;    // weight steps in flight
+// Weight steps in flight (three gain 3% with groups of 32, whose steps hold
+// four times the scale arithmetic, and lose 1% with groups of 128).
+constexpr int many_depth(int nrb, int group) { return nrb <= 2 && group == 32 ? 3 : 2; }
 constexpr int kManyWaves = 2;    // waves per SIMD
 
 template <bool kGateUp, int kGroup, int NRB, bool kStream>
@@ -322,7 +337,7 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   constexpr int kUnits = step_units(kGroup);
   constexpr int kScales = kStepK / kGroup;
   constexpr int kF = 4 / kScales;
-  constexpr int D = kManyDepth;
+  constexpr int D = many_depth(NRB, kGroup), U = D % 2 ? 2 * D : D;   // U: steps unrolled
   const bool sh = (g == p.E);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
@@ -369,6 +384,7 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   load_a(0);
 #pragma unroll
   for (int d = 0; d < D; ++d) load_w(d, d);
+  const CodeConstants cc = code_constants();
   f32x4 acc[NRB][4];
 #pragma unroll
   for (int r = 0; r < NRB; ++r)
@@ -378,10 +394,15 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   load_a(1);
   __syncthreads();
 
-  for (int s = 0; s < nsteps; s += 2) {
+  for (int s = 0; s < nsteps; s += U) {
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {   // d: the LDS buffer
+    for (int d = 0; d < U; ++d) {   // LDS buffer d % 2, weight slot d % D
       if (s + d < nsteps) {   // the same for the whole workgroup
+        // The next step's activations go to the buffer that was last read
+        // before the previous barrier.  Loads return in order, so those of
+        // the step after it are issued ahead of this step's weight loads.
+        store_a((d + 1) % 2);
+        load_a(s + d + 2);
 #pragma unroll
         for (int q = 0; q < kScales; ++q) {
           u32x4 a[NRB][kF];
@@ -389,7 +410,7 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
           for (int r = 0; r < NRB; ++r)
 #pragma unroll
             for (int f = 0; f < kF; ++f)
-              a[r][f] = lds[((d * NRB + r) * 4 + q * kF + f) * 64 + lane];
+              a[r][f] = lds[((d % 2 * NRB + r) * 4 + q * kF + f) * 64 + lane];
           float sv[4];
           scales_f32(sc[d % D][q], sv);
           f32x4 corr[NRB];
@@ -405,7 +426,7 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
             f32x4 part[NRB];
 #pragma unroll
             for (int f = 0; f < kF; ++f) {
-              const bf16x8 w = codes_bf16(rb[d % D][b][q * kF + f]);
+              const bf16x8 w = codes_bf16(rb[d % D][b][q * kF + f], cc);
 #pragma unroll
               for (int r = 0; r < NRB; ++r)
                 part[r] = mfma16(as_bf16x8(a[r][f]), w, f == 0 ? corr[r] : part[r]);
@@ -417,8 +438,6 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
           }
         }
         load_w(d % D, s + d + D);
-        store_a(d ^ 1);      // read again after the barrier; last read before the previous one
-        load_a(s + d + 2);
         __syncthreads();
       }
     }
