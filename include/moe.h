@@ -330,6 +330,8 @@ moe_status moe_quantize_act(const moe_config* cfg, int64_t rows, const void* x, 
  *   y [rows, H] act_dtype out; yq [rows, H] uint8 and ys [rows, H/128] fp32 out
  *   (both or neither; bf16 activations, H % 128 == 0; power-of-two scales with
  *   weight_dtype MOE_FP8_E4M3_E8M0).  y or yq may be NULL, not both.
+ * Rows, weight, dweight, codes and packed weights are 16-byte aligned here and
+ * in the calls below on rows and 4-bit weights (MOE_ERR_INVALID_ARG otherwise).
  * A NaN in a row makes the whole row NaN (in e4m3 too); squares are summed in
  * fp32, so values above about 1e19 overflow to rstd = 0.  No workspace. */
 moe_status moe_add_rmsnorm(const moe_config* cfg, int64_t rows, const void* x,
@@ -524,7 +526,8 @@ moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const voi
  * the rows and kd of the matrix as in moe_weights (w13: 2I rows, kd = H).
  *   moe_quantize_weight: codes and scales of a row-major bf16 matrix, per
  *     group scale = bf16(max |w| / 7), code = round(w / scale) + 8, ties to
- *     even, clamped to 0..15 (scale 0 and codes 8 for a group of zeros).
+ *     even, clamped to 0..15 (scale 0 and codes 8 for a group of zeros).  The
+ *     weights are finite.
  *   moe_pack_quantized: the layout that the kernels stream, codes and scales
  *     together, into a device buffer of moe_packed_bytes(cfg, which) bytes.
  *     Per (expert, output tile, 128-k step) one block: eight 1 KiB fragments

@@ -169,6 +169,12 @@ moe_status check_ws(void* ws, size_t ws_bytes, const Layout& L) {
   do {                                                                 \
     if (!(p)) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", #p);      \
   } while (0)
+// Rows and packed weights are read 16 bytes at a time.
+#define ALIGNED16(p)                                                                \
+  do {                                                                              \
+    if ((uintptr_t)(p) % 16)                                                        \
+      return fail(MOE_ERR_INVALID_ARG, "%s must be 16-byte aligned", #p);           \
+  } while (0)
 #define HIPCALL(expr, where)                              \
   do {                                                    \
     hipError_t _e = (expr);                               \
@@ -328,6 +334,14 @@ moe_status check_weights(const moe_config* c, const moe_weights* w, bool need_ga
       NONNULL(w->ws2_scale);
     }
   }
+  if (is_int4(c->weight_dtype)) {
+    ALIGNED16(w->w13);
+    ALIGNED16(w->w2);
+    if (c->shared_intermediate_size > 0) {
+      ALIGNED16(w->ws13);
+      ALIGNED16(w->ws2);
+    }
+  }
   return MOE_OK;
 }
 
@@ -367,6 +381,7 @@ moe_status forward_impl(const moe_config* cfg, int64_t T, const void* x, const m
   NONNULL(x);
   NONNULL(out);
   CHECK(check_weights(cfg, w, true));
+  if (is_int4(cfg->weight_dtype)) ALIGNED16(x);
   const Layout L = layout(cfg, T);
   CHECK(check_ws(ws, ws_bytes, L));
   if (one_launch &&
@@ -558,6 +573,11 @@ moe_status moe_expert_ffn(const moe_config* cfg, int64_t T, const void* x, const
   NONNULL(y);
   CHECK(check_weights(cfg, w, false));
   if (cfg->shared_intermediate_size > 0) NONNULL(y_shared);
+  if (is_int4(cfg->weight_dtype)) {
+    ALIGNED16(x);
+    ALIGNED16(y);
+    if (cfg->shared_intermediate_size > 0) ALIGNED16(y_shared);
+  }
   const Layout L = layout(cfg, T);
   CHECK(check_ws(ws, ws_bytes, L));
   return run_ffn(cfg, T, x, perm, offsets, w, y,
@@ -800,6 +820,7 @@ moe_status moe_expert_ffn_quantized(const moe_config* cfg, int64_t T, const uint
   if (T == 0) return MOE_OK;
   NONNULL(xq);
   NONNULL(xs);
+  ALIGNED16(xq);
   NONNULL(perm);
   NONNULL(offsets);
   NONNULL(y);
@@ -824,6 +845,12 @@ moe_status moe_add_rmsnorm(const moe_config* cfg, int64_t rows, const void* x,
   NONNULL(x);
   NONNULL(weight);
   if (!y && !yq) return fail(MOE_ERR_INVALID_ARG, "y and yq are both NULL");
+  ALIGNED16(x);
+  ALIGNED16(residual);
+  ALIGNED16(weight);
+  ALIGNED16(sum);
+  ALIGNED16(y);
+  ALIGNED16(yq);
   HIPCALL(moe::launch_add_rmsnorm(x, residual, weight, eps, rows, cfg->hidden_size,
                                   cfg->act_dtype == MOE_BF16, sum, y, yq, ys,
                                   cfg->weight_dtype == MOE_FP8_E4M3_E8M0, (hipStream_t)stream),
@@ -842,6 +869,12 @@ moe_status moe_add_rmsnorm_backward(const moe_config* cfg, int64_t rows, const v
                                     size_t ws_bytes, void* stream) {
   CHECK(check_norm(cfg, rows, eps));
   NONNULL(dweight);
+  ALIGNED16(sum);
+  ALIGNED16(weight);
+  ALIGNED16(dy);
+  ALIGNED16(dsum);
+  ALIGNED16(dx);
+  ALIGNED16(dweight);
   if (rows) {
     NONNULL(sum);
     NONNULL(weight);
@@ -866,6 +899,8 @@ moe_status moe_dispatch(const moe_config* cfg, int64_t T, const void* x, const i
   NONNULL(x);
   NONNULL(pos);
   NONNULL(rows);
+  ALIGNED16(x);
+  ALIGNED16(rows);
   HIPCALL(moe::launch_dispatch(x, (int64_t)cfg->hidden_size * act_bytes(cfg), nullptr, 0, pos, T,
                                cfg->num_experts_per_tok, rows, nullptr, (hipStream_t)stream),
           "dispatch");
@@ -886,6 +921,8 @@ moe_status moe_dispatch_quantized(const moe_config* cfg, int64_t T, const uint8_
   NONNULL(pos);
   NONNULL(rows_q);
   NONNULL(rows_s);
+  ALIGNED16(xq);
+  ALIGNED16(rows_q);
   HIPCALL(moe::launch_dispatch(xq, cfg->hidden_size, xs, cfg->hidden_size / 128, pos, T,
                                cfg->num_experts_per_tok, rows_q, rows_s, (hipStream_t)stream),
           "dispatch");
@@ -900,6 +937,9 @@ moe_status moe_dispatch_backward(const moe_config* cfg, int64_t T, const void* d
   NONNULL(drows);
   NONNULL(pos);
   NONNULL(dx);
+  ALIGNED16(drows);
+  ALIGNED16(dx_add);
+  ALIGNED16(dx);
   HIPCALL(moe::launch_dispatch_backward(drows, dx_add, pos, T, cfg->hidden_size,
                                         cfg->num_experts_per_tok, cfg->act_dtype == MOE_BF16, dx,
                                         (hipStream_t)stream),
@@ -919,6 +959,9 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
   NONNULL(topk_w);
   NONNULL(dy);
   NONNULL(dtopk_w);
+  ALIGNED16(dout);
+  ALIGNED16(y);
+  ALIGNED16(dy);
   HIPCALL(moe::launch_combine_backward(dout, y, pos, topk_w, T, cfg->hidden_size,
                                        cfg->num_experts_per_tok, cfg->act_dtype == MOE_BF16, dy,
                                        dtopk_w, (hipStream_t)stream),
@@ -1009,6 +1052,8 @@ moe_status moe_quantize_weight(const moe_config* cfg, moe_weight_id which, const
   NONNULL(src);
   NONNULL(codes);
   NONNULL(scales);
+  ALIGNED16(src);
+  ALIGNED16(codes);
   HIPCALL(moe::launch_quantize_int4(int4_group(cfg->weight_dtype), (const uint16_t*)src,
                                     m.experts * (m.gate_up ? 2 : 1) * m.n, m.kd, codes,
                                     (uint16_t*)scales, (hipStream_t)stream),
@@ -1026,6 +1071,7 @@ moe_status moe_pack_quantized(const moe_config* cfg, moe_weight_id which, const 
   NONNULL(codes);
   NONNULL(scales);
   NONNULL(dst);
+  ALIGNED16(dst);
   HIPCALL(moe::launch_pack_int4(m.gate_up, int4_group(cfg->weight_dtype), codes,
                                 (const uint16_t*)scales, dst, m.experts, m.n, m.kd,
                                 (hipStream_t)stream),

@@ -175,6 +175,39 @@ def test_int4_refusals(wd):
                                       None, FAKE * 256, 1 << 40, None) == UNS
 
 
+def test_misaligned_rows_are_refused():
+    """Rows, norm weights, codes and packed weights are read 16 bytes at a time."""
+    def each(name, cfg, args, where, status=INV):
+        for i in where:
+            a = list(args)
+            a[i] = FAKE + 8
+            assert _call(name, cfg, *a) == status and "aligned" in moe.moe_last_error(), (name, i)
+    each("moe_add_rmsnorm", _cfg(), [4, FAKE, FAKE, FAKE, 1e-6, FAKE, FAKE, FAKE, FAKE], (1, 2, 3, 5, 6, 7))
+    each("moe_add_rmsnorm_backward", _cfg(), [4, FAKE, FAKE, 1e-6, FAKE, FAKE, FAKE, FAKE, FAKE * 256, 1 << 40],
+         (1, 2, 4, 5, 6, 7))
+    each("moe_dispatch", _cfg(), [4, FAKE, FAKE, FAKE], (1, 3))
+    each("moe_dispatch_quantized", _cfg(), [4] + [FAKE] * 5, (1, 4))
+    each("moe_dispatch_backward", _cfg(), [4] + [FAKE] * 4, (1, 2, 4))
+    each("moe_combine_backward", _cfg(), [4] + [FAKE] * 6, (1, 2, 5))
+    c = _cfg(wdtype="int4g128")
+    each("moe_quantize_weight", c, [moe.MOE_W2, FAKE, FAKE, FAKE], (1, 2))
+    each("moe_pack_quantized", c, [moe.MOE_W2, FAKE, FAKE, FAKE], (3,))
+    for k in ("w13", "w2", "ws13", "ws2"):
+        w = moe.weights(packed=True, **{n: FAKE + 8 * (n == k) for n in ("w13", "w2", "ws13", "ws2")})
+        assert moe.lib().moe_expert_ffn(ctypes.byref(c), 4, FAKE, FAKE, FAKE, ctypes.byref(w), FAKE, FAKE, FAKE * 256,
+                                        1 << 40, None) == INV
+        assert "aligned" in moe.moe_last_error()
+    w = moe.weights(gate_w=FAKE, bias=FAKE, w13=FAKE, w2=FAKE, ws13=FAKE, ws2=FAKE, packed=True)
+    for i in range(3):
+        x, y, ys = (FAKE + 8 * (i == j) for j in range(3))
+        assert moe.lib().moe_expert_ffn(ctypes.byref(c), 4, x, FAKE, FAKE, ctypes.byref(w), y, ys, FAKE * 256, 1 << 40,
+                                        None) == INV
+        assert "aligned" in moe.moe_last_error()
+    assert moe.lib().moe_forward(ctypes.byref(c), 4, FAKE + 8, ctypes.byref(w), FAKE, None, None, None, None, None,
+                                 FAKE * 256, 1 << 40, None) == INV
+    assert "aligned" in moe.moe_last_error()
+
+
 def test_quantized_rows_need_e4m3_weights():
     w = moe.weights(w13=FAKE, w2=FAKE, ws13=FAKE, ws2=FAKE, packed=True)
     for wd in ("bf16", "int4g128"):

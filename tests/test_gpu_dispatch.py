@@ -17,6 +17,7 @@ pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 SIZES = [(1, 64, 1), (1, 7168, 8), (5, 192, 3), (33, 1024, 4), (261, 512, 8), (70, 7168, 9), (7, 8256, 16),
          (3, 256, 64), (1025, 128, 2)]
+LARGE = (1200, 7168, 8)   # past the size from which rows are read and written non-temporally
 
 
 def _cfg(H, K, act):
@@ -45,7 +46,7 @@ def _dev(a):
 
 @pytest.mark.parametrize("drop", [False, True])
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-@pytest.mark.parametrize("T,H,K", SIZES)
+@pytest.mark.parametrize("T,H,K", SIZES + [LARGE])
 def test_dispatch(T, H, K, act, drop):
     pos, x = _pos(T, K, drop), _rows(1, T, H, act)
     rows = torch.full((T * K, H), 7.0, dtype=DT[act], device=DEV)
@@ -58,7 +59,7 @@ def test_dispatch(T, H, K, act, drop):
 
 
 @pytest.mark.parametrize("drop", [False, True])
-@pytest.mark.parametrize("T,H,K", [s for s in SIZES if s[1] % 128 == 0] + [(9, 640, 5)])
+@pytest.mark.parametrize("T,H,K", [s for s in SIZES if s[1] % 128 == 0] + [(9, 640, 5), (2400, 7168, 8)])
 def test_dispatch_quantized(T, H, K, drop):
     rng = np.random.default_rng(T + H)
     pos, q = _pos(T, K, drop), rng.integers(0, 256, (T, H), dtype=np.uint8)
@@ -75,7 +76,7 @@ def test_dispatch_quantized(T, H, K, drop):
 
 @pytest.mark.parametrize("drop", [False, True])
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-@pytest.mark.parametrize("T,H,K", SIZES)
+@pytest.mark.parametrize("T,H,K", SIZES + [LARGE])
 def test_dispatch_backward(T, H, K, act, drop):
     pos, d, add = _pos(T, K, drop), _rows(2, T * K, H, act), _rows(3, T, H, act)
     cfg, N = _cfg(H, K, act), T * K
@@ -98,7 +99,7 @@ def test_dispatch_backward(T, H, K, act, drop):
 
 @pytest.mark.parametrize("drop", [False, True])
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-@pytest.mark.parametrize("T,H,K", SIZES)
+@pytest.mark.parametrize("T,H,K", SIZES + [LARGE])
 def test_combine_backward(T, H, K, act, drop):
     pos, dout, y = _pos(T, K, drop), _rows(4, T, H, act), _rows(5, T * K, H, act)
     w = np.random.default_rng(6).random((T, K), dtype=np.float32)
