@@ -42,17 +42,18 @@ hist_kernel(const int32_t* __restrict__ idx, int64_t N, int E, int32_t* __restri
 
 // One block of PMAXE threads.  hist[b][e] (row stride E + 1) becomes the base
 // position of block b's elements of expert e; *err is set to 1 if any id was
-// outside [0, E), else 0 (each call rewrites it).
+// outside [0, E), that is if fewer than N ids were counted for the experts,
+// else 0 (each call rewrites it).
 __global__ void __launch_bounds__(PMAXE)
-scan_kernel(int32_t* __restrict__ hist, int nblk, int E, int32_t* __restrict__ counts,
+scan_kernel(int32_t* __restrict__ hist, int nblk, int64_t N, int E, int32_t* __restrict__ counts,
             int32_t* __restrict__ offsets, int32_t* __restrict__ err) {
   constexpr int B = 16;   // histogram rows read per batch (independent loads)
   __shared__ int32_t s[PMAXE];
   const int e = threadIdx.x;
   const int64_t ld = E + 1;
-  // Per-expert total over the blocks (thread E also totals the invalid ids).
+  // Per-expert total over the blocks.
   int32_t total = 0;
-  if (e <= E) {
+  if (e < E) {
     for (int b0 = 0; b0 < nblk; b0 += B) {
       int32_t v[B];
 #pragma unroll
@@ -61,8 +62,7 @@ scan_kernel(int32_t* __restrict__ hist, int nblk, int E, int32_t* __restrict__ c
       for (int j = 0; j < B; ++j) total += v[j];
     }
   }
-  if (e == E) *err = total ? 1 : 0;
-  const int32_t mine = (e < E) ? total : 0;
+  const int32_t mine = total;
   if (e < E) counts[e] = mine;
   s[e] = mine;
   __syncthreads();
@@ -89,7 +89,10 @@ scan_kernel(int32_t* __restrict__ hist, int nblk, int E, int32_t* __restrict__ c
       }
     }
   }
-  if (e == E - 1) offsets[E] = s[e];
+  if (e == E - 1) {
+    offsets[E] = s[e];
+    *err = s[e] != N ? 1 : 0;
+  }
 }
 
 __global__ void __launch_bounds__(PTHREADS)
@@ -168,7 +171,8 @@ hipError_t launch_permute(const int32_t* idx, int64_t N, int E, int32_t* hist, i
   MOE_TIMED_LAUNCH(s, "hist_kernel",
     hipLaunchKernelGGL(hist_kernel, dim3(nblk), dim3(PTHREADS), 0, s, idx, N, E, hist));
   MOE_TIMED_LAUNCH(s, "scan_kernel",
-    hipLaunchKernelGGL(scan_kernel, dim3(1), dim3(PMAXE), 0, s, hist, nblk, E, counts, offsets, err));
+    hipLaunchKernelGGL(scan_kernel, dim3(1), dim3(PMAXE), 0, s, hist, nblk, N, E, counts, offsets,
+                       err));
   MOE_TIMED_LAUNCH(s, "scatter_kernel",
     hipLaunchKernelGGL(scatter_kernel, dim3(nblk), dim3(PTHREADS), 0, s, idx, N, E,
                        (const int32_t*)hist, perm, pos));
