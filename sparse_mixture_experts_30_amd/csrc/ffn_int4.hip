@@ -183,9 +183,14 @@ __device__ __forceinline__ bool find_item(const Int4Args& p, Item& it) {
 // A tile of at most 16 rows: wave w takes a quarter of the k steps, D of them
 // in flight, and the four waves' sums are joined through LDS in wave order.
 constexpr int kFewRows = 16;
-constexpr int kFewFrags = 8;    // weight fragments of a workgroup
-constexpr int kFewDepth = 1;    // k steps in flight
-constexpr int kFewWaves = 4;    // waves that share the k steps
+// Fragments of a workgroup, k steps in flight and waves that share the k
+// steps: what leaves four waves per SIMD.  T = 32 (H = 7168, I = 2048, top-8 of
+// 256): 8 fragments, 1 step, 4 waves 361 us (5.7 TB/s); 2 steps 398-423; 4
+// fragments 400-443; 8 waves 397; 2 waves 356, but then T = 1 takes 76 instead
+// of 50 us.  Cached instead of non-temporal weight loads: 395 us.
+constexpr int kFewFrags = 8;
+constexpr int kFewDepth = 1;
+constexpr int kFewWaves = 4;
 constexpr int kFewThreads = 64 * kFewWaves;
 
 template <bool kGateUp, int kGroup, bool kStream>
@@ -324,12 +329,9 @@ __global__ void __launch_bounds__(kFewThreads) grouped_gemm_int4_few(Int4Args p)
 // --------------------------------------------------------------- many rows
 // A tile of at most 64 rows and two packed output tiles: each wave takes four
 // fragments over the whole k range, the rows' activations pass through two
-// LDS buffers in fragment order (lane-linear 16-byte reads and writes).
-constexpr int kManyRows = 64;
-// Weight steps in flight (three gain 3% with groups of 32, whose steps hold
-// four times the scale arithmetic, and lose 1% with groups of 128).
-constexpr int many_depth(int nrb, int group) { return nrb <= 2 && group == 32 ? 3 : 2; }
-constexpr int kManyWaves = 2;    // waves per SIMD
+// LDS buffers in fragment order (lane-linear 16-byte reads and writes).  Tiles
+// of at most 32 rows leave registers for three waves per SIMD instead of two.
+constexpr int kMidRows = 32, kManyRows = 64;
 
 template <bool kGateUp, int kGroup, int NRB, bool kStream>
 __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, int g, int row0,
@@ -337,7 +339,6 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   constexpr int kUnits = step_units(kGroup);
   constexpr int kScales = kStepK / kGroup;
   constexpr int kF = 4 / kScales;
-  constexpr int D = many_depth(NRB, kGroup), U = D % 2 ? 2 * D : D;   // U: steps unrolled
   const bool sh = (g == p.E);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
@@ -358,17 +359,17 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
     const int arow = (!sh && kGateUp) ? p.perm[row0 + rr] / p.K : row0 + rr;
     ap[r] = (sh ? p.a_s : p.a_r) + (int64_t)arow * (sh ? p.lda_s : p.lda_r) + wave * 32 + lq * 8;
   }
-  u32x4 rb[D][4], st[NRB];
-  uint2 sc[D][kScales];
-  auto load_w = [&](int slot, int step) {
+  u32x4 rb[4], st[NRB];
+  uint2 sc[kScales];
+  auto load_w = [&](int step) {
     const u32x4* src = bw + (int64_t)min(step, nsteps - 1) * kUnits;
 #pragma unroll
     for (int b = 0; b < 4; ++b)
-      rb[slot][b] = kStream ? __builtin_nontemporal_load(src + (fh * 4 + b) * 64 + lane)
+      rb[b] = kStream ? __builtin_nontemporal_load(src + (fh * 4 + b) * 64 + lane)
                             : src[(fh * 4 + b) * 64 + lane];
 #pragma unroll
     for (int q = 0; q < kScales; ++q)
-      sc[slot][q] = reinterpret_cast<const uint2*>(src + kCodes16 + q * 16 + lr)[fh];
+      sc[q] = reinterpret_cast<const uint2*>(src + kCodes16 + q * 16 + lr)[fh];
   };
   // Wave w stages k fragment w of every row block.
   auto load_a = [&](int step) {
@@ -382,8 +383,7 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   };
 
   load_a(0);
-#pragma unroll
-  for (int d = 0; d < D; ++d) load_w(d, d);
+  load_w(0);
   const CodeConstants cc = code_constants();
   f32x4 acc[NRB][4];
 #pragma unroll
@@ -394,54 +394,64 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   load_a(1);
   __syncthreads();
 
-  for (int s = 0; s < nsteps; s += U) {
+  // One step from LDS buffer d.
+  auto compute = [&](int d) {
 #pragma unroll
-    for (int d = 0; d < U; ++d) {   // LDS buffer d % 2, weight slot d % D
-      if (s + d < nsteps) {   // the same for the whole workgroup
-        // The next step's activations go to the buffer that was last read
-        // before the previous barrier.  Loads return in order, so those of
-        // the step after it are issued ahead of this step's weight loads.
-        store_a((d + 1) % 2);
-        load_a(s + d + 2);
+    for (int q = 0; q < kScales; ++q) {
+      u32x4 a[NRB][kF];
 #pragma unroll
-        for (int q = 0; q < kScales; ++q) {
-          u32x4 a[NRB][kF];
+      for (int r = 0; r < NRB; ++r)
+#pragma unroll
+        for (int f = 0; f < kF; ++f)
+          a[r][f] = lds[((d * NRB + r) * 4 + q * kF + f) * 64 + lane];
+      float sv[4];
+      scales_f32(sc[q], sv);
+      f32x4 corr[NRB];
+#pragma unroll
+      for (int r = 0; r < NRB; ++r) {
+        corr[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int f = 0; f < kF; ++f)
+          corr[r] = mfma16(as_bf16x8(a[r][f]), minus_136(), corr[r]);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        f32x4 part[NRB];
+#pragma unroll
+        for (int f = 0; f < kF; ++f) {
+          const bf16x8 w = codes_bf16(rb[b][q * kF + f], cc);
 #pragma unroll
           for (int r = 0; r < NRB; ++r)
-#pragma unroll
-            for (int f = 0; f < kF; ++f)
-              a[r][f] = lds[((d % 2 * NRB + r) * 4 + q * kF + f) * 64 + lane];
-          float sv[4];
-          scales_f32(sc[d % D][q], sv);
-          f32x4 corr[NRB];
-#pragma unroll
-          for (int r = 0; r < NRB; ++r) {
-            corr[r] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int f = 0; f < kF; ++f)
-              corr[r] = mfma16(as_bf16x8(a[r][f]), minus_136(), corr[r]);
-          }
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            f32x4 part[NRB];
-#pragma unroll
-            for (int f = 0; f < kF; ++f) {
-              const bf16x8 w = codes_bf16(rb[d % D][b][q * kF + f], cc);
-#pragma unroll
-              for (int r = 0; r < NRB; ++r)
-                part[r] = mfma16(as_bf16x8(a[r][f]), w, f == 0 ? corr[r] : part[r]);
-            }
-#pragma unroll
-            for (int r = 0; r < NRB; ++r)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[r][b][i] = fmaf(sv[b], part[r][i], acc[r][b][i]);
-          }
+            part[r] = mfma16(as_bf16x8(a[r][f]), w, f == 0 ? corr[r] : part[r]);
         }
-        load_w(d % D, s + d + D);
-        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < NRB; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][b][i] = fmaf(sv[b], part[r][i], acc[r][b][i]);
       }
     }
+  };
+  // One step: the next step's activations go to the buffer that was last
+  // read before the previous barrier, and the loads of the step after it are
+  // issued before this step's arithmetic (the scheduling barrier keeps them
+  // there).  The next weights are loaded into the registers that this step
+  // frees: a second set costs more in waves per SIMD than it hides (T = 1024,
+  // H = 7168, I = 2048: one set 1.47 ms, two 1.50, three 1.49).
+  auto one_step = [&](int d, int step) {
+    store_a(d ^ 1);
+    load_a(step + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(d);
+    load_w(step + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+  };
+  int s = 0;
+  for (; s + 2 <= nsteps; s += 2) {
+    one_step(0, s);
+    one_step(1, s + 1);
   }
+  if (s < nsteps) one_step(0, s);   // the same for the whole workgroup
 
   // Results through LDS (the buffers are free after the last barrier), each
   // wave its own part: [row][its 64 output or 32 h columns] bf16.
@@ -477,29 +487,29 @@ __device__ __forceinline__ void int4_many_tile(const Int4Args& p, u32x4* lds, in
   }
 }
 
-template <bool kGateUp, int kGroup>
-__global__ void __launch_bounds__(kThreads4, kManyWaves) grouped_gemm_int4_many(Int4Args p) {
-  __shared__ u32x4 lds[2 * (kManyRows / 16) * 4 * 64];   // 32 KiB
+template <bool kGateUp, int kGroup, int kRows>
+__global__ void __launch_bounds__(kThreads4, kRows == kMidRows ? 3 : 2)
+grouped_gemm_int4_many(Int4Args p) {
+  __shared__ u32x4 lds[2 * (kRows / 16) * 4 * 64];   // 16 or 32 KiB
   Item it;
-  if (!find_item<kManyRows>(p, it)) return;
+  if (!find_item<kRows>(p, it)) return;
   const int g = it.g, row0 = it.row0, nrows = it.nrows, npair = it.ntile;
   if (2 * npair >= (g == p.E ? p.nt_s : p.nt_r)) return;
-  switch (((nrows + 15) >> 4) * 2 + (it.alone ? 1 : 0)) {
-#define MOE_INT4_CASE(n)                                                               \
-    case 2 * n:                                                                        \
-      int4_many_tile<kGateUp, kGroup, n, false>(p, lds, g, row0, nrows, npair);        \
-      break;                                                                           \
-    case 2 * n + 1:                                                                    \
-      int4_many_tile<kGateUp, kGroup, n, true>(p, lds, g, row0, nrows, npair);         \
-      break;
-    MOE_INT4_CASE(1)
-    MOE_INT4_CASE(2)
+  const int blocks = (nrows + 15) >> 4;
+#define MOE_INT4_CASE(n)                                                          \
+  if (blocks == n) {                                                              \
+    if (it.alone)                                                                 \
+      int4_many_tile<kGateUp, kGroup, n, true>(p, lds, g, row0, nrows, npair);    \
+    else                                                                          \
+      int4_many_tile<kGateUp, kGroup, n, false>(p, lds, g, row0, nrows, npair);   \
+  }
+  MOE_INT4_CASE(1)
+  MOE_INT4_CASE(2)
+  if constexpr (kRows > kMidRows) {
     MOE_INT4_CASE(3)
     MOE_INT4_CASE(4)
-#undef MOE_INT4_CASE
-    default:
-      break;
   }
+#undef MOE_INT4_CASE
 }
 
 // One thread per 16-byte fragment piece, then per scale vector.
@@ -584,31 +594,41 @@ quantize_int4_kernel(int group, const uint16_t* __restrict__ src, int64_t chunks
   if (c % (group / 8) == 0) scales[c * 8 / group] = (uint16_t)sb;
 }
 
-// nt: packed tiles of the group with the most of them.
-template <bool kGateUp, int kGroup>
-hipError_t launch_gemm(Int4Args a, bool few, int64_t mtiles, int nt, hipStream_t s) {
-  a.ntn = few ? nt * (kFrags / kFewFrags) : (nt + 1) / 2;
-  const int64_t work = mtiles * a.ntn;
-  if (work > 0x7fffffff - kXcdGrid) return hipErrorInvalidValue;
-  if (few)
-    MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_few<true>" : "grouped_gemm_int4_few<false>",
-      hipLaunchKernelGGL((grouped_gemm_int4_few<kGateUp, kGroup>), dim3(xcd_grid(work)),
-                         dim3(kFewThreads), 0, s, a));
-  else
-    MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_many<true>" : "grouped_gemm_int4_many<false>",
-      hipLaunchKernelGGL((grouped_gemm_int4_many<kGateUp, kGroup>), dim3(xcd_grid(work)),
-                         dim3(kThreads4), 0, s, a));
-  return hipGetLastError();
+// Rows of an M-tile, which name the kernel: the few-row kernel up to
+// kFewAverage rows per expert on average, then tiles of 32 and of 64 rows.
+// Measured at H = 7168, I = 2048, E = 256, K = 8, groups of 128, few / 32 / 64:
+// T = 256 (8 rows an expert) 1.01 / - / 1.13 ms, T = 320 1.04 / 1.01 / 1.07,
+// T = 512 1.25 / 1.12 / 1.17, T = 768 - / 1.29 / 1.32, T = 1024 (32 rows) 2.6 /
+// 1.52 / 1.48; E = 64, groups of 32, T = 200 (25 rows) - / 0.41 / 0.46.
+// A batch whose work would leave CUs idle in the tall-tile kernels takes the
+// few-row kernel too, which splits k over its waves and so makes more and
+// shorter workgroups (T = 201, H = 1024, I = 256, E = 32, K = 4: 18 against 35 us).
+constexpr int kFewAverage = 8, kMidAverage = 28;
+constexpr int64_t kManyGrid = 512;
+int tile_rows(const FfnDims& d) {
+  if (d.T <= kFewRows || d.N <= (int64_t)kFewAverage * d.E ||
+      ffn_grid_mtiles(d, kManyRows) * (d.I / 128) < kManyGrid)
+    return kFewRows;
+  return d.N <= (int64_t)kMidAverage * d.E ? kMidRows : kManyRows;
 }
 
-// The few-row kernel takes batches of up to kFewAverage rows per expert on
-// average, and those whose work would leave CUs idle in the other one (its
-// waves split the k steps, so it makes more and shorter workgroups).
-constexpr int kFewAverage = 8;
-constexpr int64_t kManyGrid = 512;
-bool use_few(const FfnDims& d) {
-  return d.T <= kFewRows || d.N <= (int64_t)kFewAverage * d.E ||
-         ffn_grid_mtiles(d, kManyRows) * (d.I / 128) < kManyGrid;
+// nt: packed tiles of the group with the most of them.
+template <bool kGateUp, int kGroup>
+hipError_t launch_gemm(Int4Args a, int rows, int64_t mtiles, int nt, hipStream_t s) {
+  a.ntn = rows == kFewRows ? nt * (kFrags / kFewFrags) : (nt + 1) / 2;
+  const int64_t work = mtiles * a.ntn;
+  if (work > 0x7fffffff - kXcdGrid) return hipErrorInvalidValue;
+  const dim3 grid(xcd_grid(work));
+  if (rows == kFewRows)
+    MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_few<true>" : "grouped_gemm_int4_few<false>",
+      hipLaunchKernelGGL((grouped_gemm_int4_few<kGateUp, kGroup>), grid, dim3(kFewThreads), 0, s,
+                         a));
+  else
+    MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_many<true>" : "grouped_gemm_int4_many<false>",
+      hipLaunchKernelGGL((rows == kMidRows ? grouped_gemm_int4_many<kGateUp, kGroup, kMidRows>
+                                           : grouped_gemm_int4_many<kGateUp, kGroup, kManyRows>),
+                         grid, dim3(kThreads4), 0, s, a));
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -641,8 +661,8 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
                            const int32_t* offsets, const void* w13p, const void* w2p,
                            const void* ws13p, const void* ws2p, uint16_t* h, uint16_t* y,
                            uint16_t* ys, hipStream_t s) {
-  const bool few = use_few(d);
-  const int64_t mt = ffn_grid_mtiles(d, few ? kFewRows : kManyRows);
+  const int rows = tile_rows(d);
+  const int64_t mt = ffn_grid_mtiles(d, rows);
 
   Int4Args a{};
   a.offsets = offsets;
@@ -664,8 +684,8 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
   a.ldc_r = d.I;
   a.ldc_s = d.Is;
   const int nt1 = std::max(a.nt_r, a.nt_s);
-  hipError_t e = group == 32 ? launch_gemm<true, 32>(a, few, mt, nt1, s)
-                             : launch_gemm<true, 128>(a, few, mt, nt1, s);
+  hipError_t e = group == 32 ? launch_gemm<true, 32>(a, rows, mt, nt1, s)
+                             : launch_gemm<true, 128>(a, rows, mt, nt1, s);
   if (e != hipSuccess) return e;
 
   a.nt_r = a.nt_s = d.H / 128;
@@ -678,8 +698,8 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
   a.c_r = y;
   a.c_s = ys;
   a.ldc_r = a.ldc_s = d.H;
-  return group == 32 ? launch_gemm<false, 32>(a, few, mt, a.nt_r, s)
-                     : launch_gemm<false, 128>(a, few, mt, a.nt_r, s);
+  return group == 32 ? launch_gemm<false, 32>(a, rows, mt, a.nt_r, s)
+                     : launch_gemm<false, 128>(a, rows, mt, a.nt_r, s);
 }
 
 }  // namespace moe

@@ -85,12 +85,22 @@ class Layer:
         assert torch.equal(y, y2) and (ys is None or torch.equal(ys, ys2))
 
 
-# Tokens around the 16-row blocks and the tile heights; K steps that do not divide by four.
+# Tokens around the 16-row blocks of the few-row kernel; K steps that do not divide by four.
 @pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
 @pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 31, 32, 33, 64, 65, 150])
 def test_rows(wd, T):
     L = Layer(wd, H=640, E=8, K=2, I=256, Is=384)
     L.check(T, random_routing(T, 2, 8, seed=T, skew=True))     # expert 0 has all T rows
+
+
+# More than 8 rows per expert on average and enough output tiles to fill the GPU: the kernels with
+# tiles of 32 (up to 28 rows on average) and of 64 rows, with an odd number of k steps and of output tiles.
+# Expert 0 has all T rows, so tiles of every height up to the full one occur, alone and side by side.
+@pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
+@pytest.mark.parametrize("T", [150, 400, 700])
+def test_tall_tiles(wd, T):
+    L = Layer(wd, H=384, E=32, K=2, I=2048, Is=128)
+    L.check(T, random_routing(T, 2, 32, seed=T, skew=True))
 
 
 @pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
