@@ -9,6 +9,7 @@
 // A position outside [0, T*K) is a slot without a row (a dropped token): it
 // is neither read nor written, and its dw is 0.  One workgroup per token, so
 // a token's row is read once and its K rows are whole rows.
+#include "block.hpp"
 #include "rows_device.hpp"
 
 #include <algorithm>

@@ -22,9 +22,9 @@
 // Two kernels.  Batches with few rows per expert (decode) read their
 // activations straight from L2, 16 rows per tile, and split the k steps over
 // the four waves of a workgroup.  Batches with more rows share the
-// activations of up to 64 rows through LDS and split the output columns over
+// activations of 32 or 64 rows through LDS and split the output columns over
 // the waves.
-#include "moe_internal.hpp"
+#include "block.hpp"
 
 #include <algorithm>
 
@@ -80,8 +80,6 @@ __device__ __forceinline__ bf16x8 codes_bf16(uint32_t d, const CodeConstants& c)
   for (int i = 0; i < 4; ++i) r[i] = ((d >> (4 * i)) & c.mask) | c.one28;
   return as_bf16x8(r);
 }
-
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // Four bf16 scales as fp32.
 __device__ __forceinline__ void scales_f32(uint2 v, float* s) {
@@ -180,24 +178,22 @@ __device__ __forceinline__ bool find_item(const Int4Args& p, Item& it) {
 }
 
 // ---------------------------------------------------------------- few rows
-// A tile of at most 16 rows: wave w takes a quarter of the k steps, D of them
-// in flight, and the four waves' sums are joined through LDS in wave order.
+// A tile of at most 16 rows and one packed output tile: the four waves take a
+// quarter of the k steps each and their sums are joined through LDS in wave
+// order.  One step in flight a wave, four waves a SIMD (three with groups of
+// 32).  Bound by the weight stream: T = 32 (H = 7168, I = 2048, top-8 of 256,
+// loads of Zipf 1.2) 340-348 us, 5.9 TB/s; two steps in flight 368 (fewer waves
+// a SIMD), and before the loads past a wave's last step were dropped (358 us):
+// cached instead of non-temporal weight loads 395, half the fragments a
+// workgroup 400-443, k over eight waves 397, over two 356, but then T = 1 takes
+// 76 instead of 50 us.
 constexpr int kFewRows = 16;
-// Fragments of a workgroup, k steps in flight and waves that share the k
-// steps: what leaves four waves per SIMD.  T = 32 (H = 7168, I = 2048, top-8 of
-// 256): 8 fragments, 1 step, 4 waves 361 us (5.7 TB/s); 2 steps 398-423; 4
-// fragments 400-443; 8 waves 397; 2 waves 356, but then T = 1 takes 76 instead
-// of 50 us.  Cached instead of non-temporal weight loads: 395 us.
-constexpr int kFewFrags = 8;
-constexpr int kFewDepth = 1;
 constexpr int kFewWaves = 4;
 constexpr int kFewThreads = 64 * kFewWaves;
 
 template <bool kGateUp, int kGroup, bool kStream>
 __device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int g, int row0,
-                                              int nrows, int part_tile) {
-  constexpr int D = kFewDepth, FR = kFewFrags, kParts = kFrags / FR;
-  const int ntile = part_tile / kParts, f0 = part_tile % kParts * FR;   // packed tile, first fragment
+                                              int nrows, int ntile) {
   constexpr int kUnits = step_units(kGroup);
   constexpr int kScales = kStepK / kGroup;   // scale vectors per step
   constexpr int kF = 4 / kScales;            // k fragments per group
@@ -209,116 +205,103 @@ __device__ __forceinline__ void int4_few_tile(const Int4Args& p, float* lds, int
   const u32x4* bw = (sh ? p.b_s : p.b_r + (int64_t)g * p.nt_r * nsteps * kUnits) +
                     (int64_t)ntile * nsteps * kUnits;
 
-  u32x4 rb[D][FR], ra[D][4];
-  uint2 sc[D][kScales][FR / 4];
-  // Steps past the wave's last one load its last one again.
-  auto load_w = [&](int slot, int step) {
-    const u32x4* src = bw + (int64_t)min(step, nsteps - 1) * kUnits;
+  u32x4 rb[kFrags], sc[kScales], ra[4];
+  auto load_w = [&](int step) {
+    const u32x4* src = bw + (int64_t)step * kUnits;
 #pragma unroll
-    for (int b = 0; b < FR; ++b)
-      rb[slot][b] = kStream ? __builtin_nontemporal_load(src + (f0 + b) * 64 + lane)
-                            : src[(f0 + b) * 64 + lane];
+    for (int b = 0; b < kFrags; ++b)
+      rb[b] = kStream ? __builtin_nontemporal_load(src + b * 64 + lane) : src[b * 64 + lane];
 #pragma unroll
-    for (int q = 0; q < kScales; ++q)
-#pragma unroll
-      for (int j = 0; j < FR / 4; ++j)
-        sc[slot][q][j] =
-            reinterpret_cast<const uint2*>(src + kCodes16 + q * 16 + lr)[f0 / 4 + j];
+    for (int q = 0; q < kScales; ++q) sc[q] = src[kCodes16 + q * 16 + lr];
   };
-#pragma unroll
-  for (int d = 0; d < D; ++d) load_w(d, s0 + d);
+  if (s0 < s1) load_w(s0);
   // This lane's activation row (past the end the first one; those results are
   // never stored).
   const int rr = lr < nrows ? lr : 0;
   const int arow = (!sh && kGateUp) ? p.perm[row0 + rr] / p.K : row0 + rr;
   const uint16_t* ap = (sh ? p.a_s : p.a_r) + (int64_t)arow * (sh ? p.lda_s : p.lda_r) + lq * 8;
-  auto load_a = [&](int slot, int step) {
-    const uint16_t* src = ap + min(step, nsteps - 1) * kStepK;
+  auto load_a = [&](int step) {
+    const uint16_t* src = ap + step * kStepK;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) ra[slot][f] = *reinterpret_cast<const u32x4*>(src + f * 32);
+    for (int f = 0; f < 4; ++f) ra[f] = *reinterpret_cast<const u32x4*>(src + f * 32);
   };
-#pragma unroll
-  for (int d = 0; d < D; ++d) load_a(d, s0 + d);
+  if (s0 < s1) load_a(s0);
 
   const CodeConstants cc = code_constants();
-  f32x4 acc[FR];
+  f32x4 acc[kFrags];
 #pragma unroll
-  for (int b = 0; b < FR; ++b) acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  for (int s = s0; s < s1; s += D) {
+  for (int b = 0; b < kFrags; ++b) acc[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  auto compute = [&]() {
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (s + d < s1) {
+    for (int q = 0; q < kScales; ++q) {
+      float sv[kFrags];
+      scales_f32(make_uint2(sc[q][0], sc[q][1]), sv);
+      scales_f32(make_uint2(sc[q][2], sc[q][3]), sv + 4);
+      f32x4 corr = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < kScales; ++q) {
-          float sv[FR];
+      for (int f = q * kF; f < (q + 1) * kF; ++f)
+        corr = mfma16(as_bf16x8(ra[f]), minus_136(), corr);
 #pragma unroll
-          for (int j = 0; j < FR / 4; ++j) scales_f32(sc[d][q][j], sv + 4 * j);
-          f32x4 corr = {0.f, 0.f, 0.f, 0.f};
+      for (int b = 0; b < kFrags; ++b) {
+        f32x4 part = corr;
 #pragma unroll
-          for (int f = q * kF; f < (q + 1) * kF; ++f)
-            corr = mfma16(as_bf16x8(ra[d][f]), minus_136(), corr);
+        for (int f = q * kF; f < (q + 1) * kF; ++f)
+          part = mfma16(as_bf16x8(ra[f]), codes_bf16(rb[b][f], cc), part);
 #pragma unroll
-          for (int b = 0; b < FR; ++b) {
-            f32x4 part = corr;
-#pragma unroll
-            for (int f = q * kF; f < (q + 1) * kF; ++f)
-              part = mfma16(as_bf16x8(ra[d][f]), codes_bf16(rb[d][b][f], cc), part);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[b][i] = fmaf(sv[b], part[i], acc[b][i]);
-          }
-        }
+        for (int i = 0; i < 4; ++i) acc[b][i] = fmaf(sv[b], part[i], acc[b][i]);
       }
-      load_w(d, s + d + D);
-      load_a(d, s + d + D);
     }
+  };
+  // Only the wave's own steps are loaded: at a few steps a wave, one read
+  // ahead in vain is up to a fifth of the traffic.
+  int s = s0;
+  for (; s + 1 < s1; ++s) {
+    compute();
+    load_w(s + 1);
+    load_a(s + 1);
   }
+  if (s < s1) compute();
 
   // [wave][frag][row 16][col 16]
 #pragma unroll
-  for (int b = 0; b < FR; ++b)
+  for (int b = 0; b < kFrags; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      lds[((wave * FR + b) * 16 + 4 * lq + i) * 16 + lr] = acc[b][i];
+      lds[((wave * kFrags + b) * 16 + 4 * lq + i) * 16 + lr] = acc[b][i];
   __syncthreads();
-  const int row = tid >> 4;
-  if (row >= min(nrows, kFewRows)) return;   // 16 threads a row
+  const int row = tid >> 4;   // 16 threads a row
+  if (row >= nrows) return;
   uint16_t* crow = (sh ? p.c_s : p.c_r) + (int64_t)(row0 + row) * (sh ? p.ldc_s : p.ldc_r);
   auto joined = [&](int b, int col) {
-    f32x2 v = {0.f, 0.f};
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w)
-      v += *reinterpret_cast<const f32x2*>(lds + ((w * FR + b) * 16 + row) * 16 + col);
+      v += *reinterpret_cast<const f32x4*>(lds + ((w * kFrags + b) * 16 + row) * 16 + col);
     return v;
   };
-  // two h columns, or four outputs, per four fragments
   if (kGateUp) {
+    const int col = (tid & 15) * 4, b = (col >> 5) * 4 + (col >> 4 & 1);
+    const f32x4 gv = joined(b, col & 15), uv = joined(b + 2, col & 15);
+    float h[4];
 #pragma unroll
-    for (int j = 0; j < FR / 4; ++j) {
-      const int col = (tid & 15) * 2, b = 4 * j + (col >> 4);
-      const f32x2 gv = joined(b, col & 15), uv = joined(b + 2, col & 15);
-      float h[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) h[i] = gv[i] / (1.0f + __expf(-gv[i])) * uv[i];
-      *reinterpret_cast<uint32_t*>(crow + ntile * 64 + f0 * 8 + 32 * j + col) =
-          pack_bf16x2(h[0], h[1]);
-    }
+    for (int j = 0; j < 4; ++j) h[j] = gv[j] / (1.0f + __expf(-gv[j])) * uv[j];
+    *reinterpret_cast<uint2*>(crow + ntile * 64 + col) =
+        make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
   } else {
-#pragma unroll
-    for (int j = 0; j < FR / 4; ++j) {
-      const int col = (tid & 15) * 4, b = 4 * j + (col >> 4);
-      const f32x2 v = joined(b, col & 15), w = joined(b, (col & 15) + 2);
-      *reinterpret_cast<uint2*>(crow + ntile * 128 + f0 * 16 + 64 * j + col) =
-          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(w[0], w[1]));
-    }
+    const int col = (tid & 15) * 8, b = col >> 4;
+    const f32x4 v = joined(b, col & 15), w = joined(b, (col & 15) + 4);
+    *reinterpret_cast<u32x4*>(crow + ntile * 128 + col) =
+        (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(w[0], w[1]),
+                pack_bf16x2(w[2], w[3])};
   }
 }
 
 template <bool kGateUp, int kGroup>
 __global__ void __launch_bounds__(kFewThreads) grouped_gemm_int4_few(Int4Args p) {
-  __shared__ __align__(16) float lds[kFewWaves * kFewFrags * 256];
+  __shared__ __align__(16) float lds[kFewWaves * kFrags * 256];
   Item it;
   if (!find_item<kFewRows>(p, it)) return;
-  if (it.ntile >= (kFrags / kFewFrags) * (it.g == p.E ? p.nt_s : p.nt_r)) return;
+  if (it.ntile >= (it.g == p.E ? p.nt_s : p.nt_r)) return;
   // A weight tile that only this row tile reads is not kept in cache.
   if (it.alone)
     int4_few_tile<kGateUp, kGroup, true>(p, lds, it.g, it.row0, it.nrows, it.ntile);
@@ -331,6 +314,9 @@ __global__ void __launch_bounds__(kFewThreads) grouped_gemm_int4_few(Int4Args p)
 // fragments over the whole k range, the rows' activations pass through two
 // LDS buffers in fragment order (lane-linear 16-byte reads and writes).  Tiles
 // of at most 32 rows leave registers for three waves per SIMD instead of two.
+// T = 512 (H = 7168, I = 2048, top-8 of 256) 1.12 ms, 5.3 TB/s of weights and
+// rows; T = 1024 1.48 ms, 4.1 TB/s, the matrix cores busy 42% and the vector
+// issue 49% of the time: the two and the weight stream overlap only in part.
 constexpr int kMidRows = 32, kManyRows = 64;
 
 template <bool kGateUp, int kGroup, int NRB, bool kStream>
@@ -615,7 +601,7 @@ int tile_rows(const FfnDims& d) {
 // nt: packed tiles of the group with the most of them.
 template <bool kGateUp, int kGroup>
 hipError_t launch_gemm(Int4Args a, int rows, int64_t mtiles, int nt, hipStream_t s) {
-  a.ntn = rows == kFewRows ? nt * (kFrags / kFewFrags) : (nt + 1) / 2;
+  a.ntn = rows == kFewRows ? nt : (nt + 1) / 2;
   const int64_t work = mtiles * a.ntn;
   if (work > 0x7fffffff - kXcdGrid) return hipErrorInvalidValue;
   const dim3 grid(xcd_grid(work));

@@ -12,6 +12,7 @@
 
 #include "moe_internal.hpp"
 #include "backward.hpp"
+#include "block.hpp"
 
 namespace {
 

@@ -9,6 +9,7 @@
 // Backward, with g = dy * w and n = r * rstd:
 //   dr = rstd * (g - n * mean(g * n)) + dsum,   dw = sum over rows of dy * n.
 // Sums are fp32 in a fixed order.
+#include "block.hpp"
 #include "rows_device.hpp"
 
 #include <algorithm>
