@@ -536,7 +536,7 @@ moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const voi
  *     are its gate rows, 2, 3, 6, 7 the up rows), [lane 64] x 16 bytes, lane l holding row
  *     l % 16 and in its dword f the codes of k = 128 step + 32 f + 8 (l / 16)
  *     + 0..7; then the scales [group][row of 16][fragment 8] bf16.
- * The products x (code + 120) and a group's 136 sum x are formed apart in fp32:
+ * The products x (code + 128) and a group's 136 sum x are formed apart in fp32:
  * activations above about 1e34 overflow there, and a non-finite activation
  * makes its row's outputs NaN.
  * moe_forward and its variants (but moe_forward_decode_fused) and

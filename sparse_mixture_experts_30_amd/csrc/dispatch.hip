@@ -116,22 +116,24 @@ combine_backward_kernel(const IO* __restrict__ dout, const IO* y, const int32_t*
         store_chunk<kNt>(dy + (int64_t)sp[k0 + b] * H + c, g);
       }
     }
-    // The wave's sums: at each of three steps a lane keeps half of its values
-    // and hands the other half over, then three steps on the one left (10
-    // shuffles for eight sums; the order is fixed).
+    // The wave's sums: in each of two steps a lane keeps half of its values
+    // and hands the other half over; the two left are summed over the rows of
+    // 16 lanes.  The order is fixed.
     const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int n = kBatch / 2, off = 32; n >= 1; n >>= 1, off >>= 1)
+    for (int n = kBatch / 2, off = 32; n >= 2; n >>= 1, off >>= 1)
 #pragma unroll
       for (int b = 0; b < n; ++b) {
         const bool high = lane & off;
         const float keep = high ? part[b + n] : part[b], give = high ? part[b] : part[b + n];
         part[b] = keep + __shfl_xor(give, off, 64);
       }
+    const int k = k0 + (lane >> 4 & 1) * 2 + (lane >> 5) * 4;
 #pragma unroll
-    for (int off = 4; off >= 1; off >>= 1) part[0] += __shfl_xor(part[0], off, 64);
-    const int k = k0 + (lane >> 3 & 1) + (lane >> 4 & 1) * 2 + (lane >> 5) * 4;
-    if ((lane & 7) == 0 && k < K) red[k][threadIdx.x >> 6] = part[0];
+    for (int b = 0; b < 2; ++b) {
+      part[b] = row_sum(part[b]);
+      if ((lane & 15) == 0 && k + b < K) red[k + b][threadIdx.x >> 6] = part[b];
+    }
   }
   __syncthreads();
   if (threadIdx.x < K) {

@@ -54,8 +54,7 @@ __device__ __forceinline__ uint2 quant_chunk(const float (&v)[8], bool pow2, flo
   float m = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  m = row_max(m);   // the tile's 16 lanes are a row
   float inv;
   row_tile_scale(m, pow2, scale, inv);
   return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
@@ -74,26 +73,23 @@ __device__ __forceinline__ void add_chunk(const RawChunk<IO>& x, bool has_residu
   for (int j = 0; j < 8; ++j) r[j] = as_stored<IO>(r[j] + b[j]);
 }
 
-// Sums of a and b over the workgroup in a fixed order, one barrier; red holds
-// 2 * 16 floats that the previous call does not use (calls alternate halves).
-__device__ __forceinline__ void workgroup_sums(float& a, float& b, float* red) {
+// Sums over the workgroup of N values per thread in a fixed order, one
+// barrier; every thread gets them.  red holds N * 16 floats that the previous
+// call does not use (calls alternate halves).
+template <int N>
+__device__ __forceinline__ void workgroup_sums(float (&v)[N], float* red) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    a += __shfl_xor(a, off, 64);
-    b += __shfl_xor(b, off, 64);
-  }
-  const int waves = blockDim.x >> 6;
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
   if (waves == 1) return;
-  if ((threadIdx.x & 63) == 0) {
-    red[threadIdx.x >> 6] = a;
-    red[16 + (threadIdx.x >> 6)] = b;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[16 * i + (threadIdx.x >> 6)] = v[i];
   }
   __syncthreads();
-  a = b = 0.0f;
-  for (int w = 0; w < waves; ++w) {
-    a += red[w];
-    b += red[16 + w];
-  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    v[i] = lane_value(row_sum(lane < waves ? red[16 * i + lane] : 0.0f), 0);   // waves <= 16
 }
 
 // One workgroup per row.  A row of up to NC * blockDim.x chunks stays in
@@ -107,7 +103,7 @@ __global__ void __launch_bounds__(1024)
 add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ weight, float eps,
                    int H, IO* sum, IO* y, uint8_t* __restrict__ yq, float* __restrict__ ys,
                    bool pow2) {
-  __shared__ float red[32];
+  __shared__ float red[16];
   const int64_t row = (int64_t)blockIdx.x * H;
   const int nc = H / kChunk;
   auto finish = [&](int c, float (&r)[8], const float (&w)[8], float rstd) {
@@ -127,7 +123,7 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
     if (residual) b.load(residual + row + c * 8);
     add_chunk(a, residual != nullptr, b, r);
   };
-  float ss = 0.0f, none = 0.0f;
+  float ss[1] = {0.0f};
   if constexpr (NC > 0) {
     RawChunk<IO> a[NC], b[NC];
     float r[NC][8], w[NC][8];
@@ -154,10 +150,10 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
       if (c >= nc) break;
       add_chunk(a[i], residual != nullptr, b[i], r[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
+      for (int j = 0; j < 8; ++j) ss[0] = fmaf(r[i][j], r[i][j], ss[0]);
     }
-    workgroup_sums(ss, none, red);
-    const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
+    workgroup_sums(ss, red);
+    const float rstd = 1.0f / sqrtf(ss[0] / (float)H + eps);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
@@ -168,10 +164,10 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
     for (int c = threadIdx.x; c < nc; c += blockDim.x) {
       load(c, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(r[j], r[j], ss);
+      for (int j = 0; j < 8; ++j) ss[0] = fmaf(r[j], r[j], ss[0]);
     }
-    workgroup_sums(ss, none, red);
-    const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
+    workgroup_sums(ss, red);
+    const float rstd = 1.0f / sqrtf(ss[0] / (float)H + eps);
     for (int c = threadIdx.x; c < nc; c += blockDim.x) {
       float w[8];
       load(c, r);
@@ -217,7 +213,7 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
       for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     }
     for (int64_t t = blockIdx.x; t < rows; t += gridDim.x, turn ^= 1) {
-      float ss = 0.0f, dot = 0.0f;
+      float sums[2] = {0.0f, 0.0f};   // r^2, g w r
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         r[i] = nr[i];
@@ -241,13 +237,13 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
         g[i].to(gv);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          ss = fmaf(rv[j], rv[j], ss);
-          dot = fmaf(gv[j] * w[i][j], rv[j], dot);
+          sums[0] = fmaf(rv[j], rv[j], sums[0]);
+          sums[1] = fmaf(gv[j] * w[i][j], rv[j], sums[1]);
         }
       }
-      workgroup_sums(ss, dot, red[turn]);
-      const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
-      const float mean = dot * rstd / (float)H;   // mean(g * n)
+      workgroup_sums(sums, red[turn]);
+      const float rstd = 1.0f / sqrtf(sums[0] / (float)H + eps);
+      const float mean = sums[1] * rstd / (float)H;   // mean(g * n)
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
@@ -273,7 +269,7 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
   } else {
     for (int64_t t = blockIdx.x; t < rows; t += gridDim.x, turn ^= 1) {
       const int64_t row = t * H;
-      float ss = 0.0f, dot = 0.0f;
+      float sums[2] = {0.0f, 0.0f};   // r^2, g w r
       for (int c = threadIdx.x; c < nc; c += blockDim.x) {
         float r[8], g[8], w[8];
         load_chunk(sum + row + c * 8, r);
@@ -281,13 +277,13 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
         load_chunk(weight + c * 8, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          ss = fmaf(r[j], r[j], ss);
-          dot = fmaf(g[j] * w[j], r[j], dot);
+          sums[0] = fmaf(r[j], r[j], sums[0]);
+          sums[1] = fmaf(g[j] * w[j], r[j], sums[1]);
         }
       }
-      workgroup_sums(ss, dot, red[turn]);
-      const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
-      const float mean = dot * rstd / (float)H;
+      workgroup_sums(sums, red[turn]);
+      const float rstd = 1.0f / sqrtf(sums[0] / (float)H + eps);
+      const float mean = sums[1] * rstd / (float)H;
       for (int c = threadIdx.x; c < nc; c += blockDim.x) {
         float r[8], g[8], w[8], a[8], d[8];
         load_chunk(sum + row + c * 8, r);

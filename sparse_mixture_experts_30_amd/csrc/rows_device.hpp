@@ -93,4 +93,40 @@ __device__ __forceinline__ float as_stored<float>(float v) {
   return v;
 }
 
+// v of the lane n places on in the same row of 16 lanes (data-parallel move:
+// no trip through LDS as a shuffle takes).
+template <int n>
+__device__ __forceinline__ float row_rotate(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + n, 0xf, 0xf, true));
+}
+
+// Sum of v over each row of 16 lanes; every lane gets its row's, lanes of one
+// row in different orders of addition.
+__device__ __forceinline__ float row_sum(float v) {
+  v += row_rotate<8>(v);
+  v += row_rotate<4>(v);
+  v += row_rotate<2>(v);
+  v += row_rotate<1>(v);
+  return v;
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// Sum of v over the wave, the same bits in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row_sum(v);
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+// Largest v over each row of 16 lanes (NaN ignored).
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, row_rotate<8>(v));
+  v = fmaxf(v, row_rotate<4>(v));
+  v = fmaxf(v, row_rotate<2>(v));
+  return fmaxf(v, row_rotate<1>(v));
+}
+
 }  // namespace moe
