@@ -588,12 +588,18 @@ quantize_int4_kernel(int group, const uint16_t* __restrict__ src, int64_t chunks
 // 1.52 / 1.48; E = 64, groups of 32, T = 200 (25 rows) - / 0.41 / 0.46.
 // A batch whose work would leave CUs idle in the tall-tile kernels takes the
 // few-row kernel too, which splits k over its waves and so makes more and
-// shorter workgroups (T = 201, H = 1024, I = 256, E = 32, K = 4: 18 against 35 us).
+// shorter workgroups; the more rows an expert has, the fewer tall workgroups
+// are enough, as they re-read the weights less often.  Few against tall, by
+// tall workgroups x rows per expert: 104 x 32 16 / 27 us, 224 x 32 36 / 46, 272
+// x 50 94 / 110, 112 x 128 31 / 37, 388 x 22 40 / 45; 640 x 9 141 / 145; 704 x 16
+// 122 / 103, 832 x 25 208 / 179, 416 x 128 193 / 175, 352 x 512 118 / 103, 152 x
+// 1024 166 / 135.
 constexpr int kFewAverage = 8, kMidAverage = 28;
-constexpr int64_t kManyGrid = 512;
+constexpr int64_t kTallGrid = 512, kTallWork = 32768;
 int tile_rows(const FfnDims& d) {
+  const int64_t tall = ffn_grid_mtiles(d, kManyRows) * (d.I / 128);
   if (d.T <= kFewRows || d.N <= (int64_t)kFewAverage * d.E ||
-      ffn_grid_mtiles(d, kManyRows) * (d.I / 128) < kManyGrid)
+      (tall < kTallGrid && tall * d.N < kTallWork * d.E))
     return kFewRows;
   return d.N <= (int64_t)kMidAverage * d.E ? kMidRows : kManyRows;
 }

@@ -103,6 +103,12 @@ def test_tall_tiles(wd, T):
     L.check(T, random_routing(T, 2, 32, seed=T, skew=True))
 
 
+def test_tall_tiles_with_few_workgroups():
+    """1024 rows an expert: the tall-tile kernel although its grid is small."""
+    L = Layer("int4g128", H=256, E=4, K=4, I=256, Is=128)
+    L.check(1024, random_routing(1024, 4, 4, seed=11))
+
+
 @pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
 @pytest.mark.parametrize("H,I,Is", [(128, 128, 0), (128, 128, 128), (256, 384, 128), (1024, 128, 640), (384, 512, 0)])
 def test_widths(wd, H, I, Is):
