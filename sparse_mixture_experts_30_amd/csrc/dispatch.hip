@@ -60,8 +60,11 @@ dispatch_backward_kernel(const IO* __restrict__ drows, const IO* dx_add,
   __shared__ int32_t sp[kMaxK];
   const int64_t t = blockIdx.x;
   load_slots(pos, t, K, N, sp);
-  for (int c = threadIdx.x * kChunk; c < H; c += blockDim.x * kChunk) {
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int W = kWidth<IO>;
+  for (int c = threadIdx.x * W; c < H; c += blockDim.x * W) {
+    float acc[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc[j] = 0.0f;
     if (dx_add) load_chunk(dx_add + t * H + c, acc);
     for (int k0 = 0; k0 < K; k0 += kBatch) {
       RawChunk<IO> v[kBatch];
@@ -71,10 +74,10 @@ dispatch_backward_kernel(const IO* __restrict__ drows, const IO* dx_add,
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         if (k0 + b >= K || sp[k0 + b] < 0) continue;
-        float r[8];
+        float r[W];
         v[b].to(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += r[j];
+        for (int j = 0; j < W; ++j) acc[j] += r[j];
       }
     }
     store_chunk(dx + t * H + c, acc);
@@ -89,15 +92,16 @@ combine_backward_kernel(const IO* __restrict__ dout, const IO* y, const int32_t*
   __shared__ int32_t sp[kMaxK];
   __shared__ float sw[kMaxK], red[kMaxK][kMaxThreads / 64];
   const int64_t t = blockIdx.x;
+  constexpr int W = kWidth<IO>;
   if (threadIdx.x < K) sw[threadIdx.x] = w[t * K + threadIdx.x];
   load_slots(pos, t, K, N, sp);
   for (int k0 = 0; k0 < K; k0 += kBatch) {
     float part[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) part[b] = 0.0f;
-    for (int c = threadIdx.x * kChunk; c < H; c += blockDim.x * kChunk) {
+    for (int c = threadIdx.x * W; c < H; c += blockDim.x * W) {
       RawChunk<IO> v[kBatch];
-      float d[8];
+      float d[W];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b)
         if (k0 + b < K && sp[k0 + b] >= 0) v[b].template load<kNt>(y + (int64_t)sp[k0 + b] * H + c);
@@ -105,11 +109,11 @@ combine_backward_kernel(const IO* __restrict__ dout, const IO* y, const int32_t*
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         if (k0 + b >= K || sp[k0 + b] < 0) continue;
-        float yv[8], g[8];
+        float yv[W], g[W];
         v[b].to(yv);
         const float wk = sw[k0 + b];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < W; ++j) {
           part[b] = fmaf(d[j], yv[j], part[b]);
           g[j] = d[j] * wk;
         }
@@ -180,7 +184,7 @@ static hipError_t dispatch_backward(const void* drows, const void* dx_add, const
   auto* kernel = T * K * H * (int64_t)sizeof(IO) > kStreamBytes ? dispatch_backward_kernel<IO, true>
                                                                 : dispatch_backward_kernel<IO, false>;
   MOE_TIMED_LAUNCH(s, "dispatch_backward_kernel",
-    hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(row_threads(T, H / kChunk)), 0, s, (const IO*)drows,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(row_threads(T, H / kWidth<IO>)), 0, s, (const IO*)drows,
                        (const IO*)dx_add, pos, H, K, T * K, (IO*)dx));
   return hipGetLastError();
 }
@@ -198,7 +202,7 @@ static hipError_t combine_backward(const void* dout, const void* y, const int32_
   auto* kernel = T * K * H * (int64_t)sizeof(IO) > kStreamBytes ? combine_backward_kernel<IO, true>
                                                                 : combine_backward_kernel<IO, false>;
   MOE_TIMED_LAUNCH(s, "combine_backward_kernel",
-    hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(row_threads(T, H / kChunk)), 0, s, (const IO*)dout,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(row_threads(T, H / kWidth<IO>)), 0, s, (const IO*)dout,
                        (const IO*)y, pos, w, H, K, T * K, (IO*)dy, dw));
   return hipGetLastError();
 }

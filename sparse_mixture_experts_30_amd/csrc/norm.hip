@@ -64,13 +64,13 @@ __device__ __forceinline__ uint2 quant_chunk(const float (&v)[8], bool pow2, flo
 // r = x + residual of one chunk, rounded as the stream stores it.
 template <typename IO>
 __device__ __forceinline__ void add_chunk(const RawChunk<IO>& x, bool has_residual,
-                                          const RawChunk<IO>& residual, float (&r)[8]) {
+                                          const RawChunk<IO>& residual, float (&r)[kWidth<IO>]) {
   x.to(r);
   if (!has_residual) return;
-  float b[8];
+  float b[kWidth<IO>];
   residual.to(b);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = as_stored<IO>(r[j] + b[j]);
+  for (int j = 0; j < kWidth<IO>; ++j) r[j] = as_stored<IO>(r[j] + b[j]);
 }
 
 // Sums over the workgroup of N values per thread in a fixed order, one
@@ -105,44 +105,47 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
                    bool pow2) {
   __shared__ float red[16];
   const int64_t row = (int64_t)blockIdx.x * H;
-  const int nc = H / kChunk;
-  auto finish = [&](int c, float (&r)[8], const float (&w)[8], float rstd) {
-    if (sum) store_chunk<kNt>(sum + row + c * 8, r);
+  constexpr int W = kWidth<IO>;
+  const int nc = H / W;
+  auto finish = [&](int c, float (&r)[W], const float (&w)[W], float rstd) {
+    if (sum) store_chunk<kNt>(sum + row + c * W, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = r[j] * rstd * w[j];
-    if (y) store_chunk(y + row + c * 8, r);
-    if (yq) {
-      float scale;
-      *reinterpret_cast<uint2*>(yq + row + c * 8) = quant_chunk(r, pow2, scale);
-      if ((c & 15) == 0) ys[(row >> 7) + (c >> 4)] = scale;
+    for (int j = 0; j < W; ++j) r[j] = r[j] * rstd * w[j];
+    if (y) store_chunk(y + row + c * W, r);
+    if constexpr (W == 8) {   // bf16
+      if (yq) {
+        float scale;
+        *reinterpret_cast<uint2*>(yq + row + c * 8) = quant_chunk(r, pow2, scale);
+        if ((c & 15) == 0) ys[(row >> 7) + (c >> 4)] = scale;
+      }
     }
   };
-  auto load = [&](int c, float (&r)[8]) {
+  auto load = [&](int c, float (&r)[W]) {
     RawChunk<IO> a, b{};
-    a.load(x + row + c * 8);
-    if (residual) b.load(residual + row + c * 8);
+    a.load(x + row + c * W);
+    if (residual) b.load(residual + row + c * W);
     add_chunk(a, residual != nullptr, b, r);
   };
   float ss[1] = {0.0f};
   if constexpr (NC > 0) {
     RawChunk<IO> a[NC], b[NC];
-    float r[NC][8], w[NC][8];
+    float r[NC][W], w[NC][W];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nc) a[i].template load<kNt>(x + row + c * 8);
+      if (c < nc) a[i].template load<kNt>(x + row + c * W);
     }
     if (residual) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
-        if (c < nc) b[i].template load<kNt>(residual + row + c * 8);
+        if (c < nc) b[i].template load<kNt>(residual + row + c * W);
       }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nc) load_chunk(weight + c * 8, w[i]);
+      if (c < nc) load_f32(weight + c * W, w[i]);
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -150,7 +153,7 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
       if (c >= nc) break;
       add_chunk(a[i], residual != nullptr, b[i], r[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] = fmaf(r[i][j], r[i][j], ss[0]);
+      for (int j = 0; j < W; ++j) ss[0] = fmaf(r[i][j], r[i][j], ss[0]);
     }
     workgroup_sums(ss, red);
     const float rstd = 1.0f / sqrtf(ss[0] / (float)H + eps);
@@ -160,18 +163,18 @@ add_rmsnorm_kernel(const IO* x, const IO* residual, const float* __restrict__ we
       if (c < nc) finish(c, r[i], w[i], rstd);
     }
   } else {
-    float r[8];
+    float r[W];
     for (int c = threadIdx.x; c < nc; c += blockDim.x) {
       load(c, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] = fmaf(r[j], r[j], ss[0]);
+      for (int j = 0; j < W; ++j) ss[0] = fmaf(r[j], r[j], ss[0]);
     }
     workgroup_sums(ss, red);
     const float rstd = 1.0f / sqrtf(ss[0] / (float)H + eps);
     for (int c = threadIdx.x; c < nc; c += blockDim.x) {
-      float w[8];
+      float w[W];
       load(c, r);
-      load_chunk(weight + c * 8, w);
+      load_f32(weight + c * W, w);
       finish(c, r, w, rstd);
     }
   }
@@ -189,28 +192,29 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
                             float eps, const IO* dy, const IO* dsum, int64_t rows, int H, IO* dx,
                             float* __restrict__ part) {
   __shared__ float red[2][32];
-  const int nc = H / kChunk;
+  constexpr int W = kWidth<IO>;
+  const int nc = H / W;
   float* mine = part + (int64_t)blockIdx.x * H;
   int turn = 0;
   if constexpr (NC > 0) {
-    float w[NC][8], dw[NC][8];
+    float w[NC][W], dw[NC][W];
     RawChunk<IO> r[NC], g[NC], nr[NC], ng[NC];
     auto fetch = [&](int64_t t) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         if (c >= nc) break;
-        nr[i].template load<kNt>(sum + t * H + c * 8);
-        ng[i].template load<kNt>(dy + t * H + c * 8);
+        nr[i].template load<kNt>(sum + t * H + c * W);
+        ng[i].template load<kNt>(dy + t * H + c * W);
       }
     };
     fetch(blockIdx.x);   // the grid has at most `rows` workgroups
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nc) load_chunk(weight + c * 8, w[i]);
+      if (c < nc) load_f32(weight + c * W, w[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+      for (int j = 0; j < W; ++j) dw[i][j] = 0.0f;
     }
     for (int64_t t = blockIdx.x; t < rows; t += gridDim.x, turn ^= 1) {
       float sums[2] = {0.0f, 0.0f};   // r^2, g w r
@@ -224,7 +228,7 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
           const int c = threadIdx.x + i * blockDim.x;
-          if (c < nc) d[i].template load<kNt>(dsum + t * H + c * 8);
+          if (c < nc) d[i].template load<kNt>(dsum + t * H + c * W);
         }
       }
       if (t + gridDim.x < rows) fetch(t + gridDim.x);
@@ -232,11 +236,11 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
       for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         if (c >= nc) break;
-        float rv[8], gv[8];
+        float rv[W], gv[W];
         r[i].to(rv);
         g[i].to(gv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < W; ++j) {
           sums[0] = fmaf(rv[j], rv[j], sums[0]);
           sums[1] = fmaf(gv[j] * w[i][j], rv[j], sums[1]);
         }
@@ -248,35 +252,35 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
       for (int i = 0; i < NC; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         if (c >= nc) break;
-        float rv[8], gv[8], dv[8];
+        float rv[W], gv[W], dv[W];
         r[i].to(rv);
         g[i].to(gv);
         if (dsum) d[i].to(dv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < W; ++j) {
           const float n = rv[j] * rstd;
           dw[i][j] = fmaf(gv[j], n, dw[i][j]);
           rv[j] = rstd * (gv[j] * w[i][j] - n * mean) + (dsum ? dv[j] : 0.0f);
         }
-        store_chunk(dx + t * H + c * 8, rv);
+        store_chunk(dx + t * H + c * W, rv);
       }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < nc) store_chunk(mine + c * 8, dw[i]);
+      if (c < nc) store_f32(mine + c * W, dw[i]);
     }
   } else {
     for (int64_t t = blockIdx.x; t < rows; t += gridDim.x, turn ^= 1) {
       const int64_t row = t * H;
       float sums[2] = {0.0f, 0.0f};   // r^2, g w r
       for (int c = threadIdx.x; c < nc; c += blockDim.x) {
-        float r[8], g[8], w[8];
-        load_chunk(sum + row + c * 8, r);
-        load_chunk(dy + row + c * 8, g);
-        load_chunk(weight + c * 8, w);
+        float r[W], g[W], w[W];
+        load_chunk(sum + row + c * W, r);
+        load_chunk(dy + row + c * W, g);
+        load_f32(weight + c * W, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < W; ++j) {
           sums[0] = fmaf(r[j], r[j], sums[0]);
           sums[1] = fmaf(g[j] * w[j], r[j], sums[1]);
         }
@@ -285,20 +289,20 @@ add_rmsnorm_backward_kernel(const IO* __restrict__ sum, const float* __restrict_
       const float rstd = 1.0f / sqrtf(sums[0] / (float)H + eps);
       const float mean = sums[1] * rstd / (float)H;
       for (int c = threadIdx.x; c < nc; c += blockDim.x) {
-        float r[8], g[8], w[8], a[8], d[8];
-        load_chunk(sum + row + c * 8, r);
-        load_chunk(dy + row + c * 8, g);
-        load_chunk(weight + c * 8, w);
-        if (dsum) load_chunk(dsum + row + c * 8, d);
-        if (t != blockIdx.x) load_chunk(mine + c * 8, a);
+        float r[W], g[W], w[W], a[W], d[W];
+        load_chunk(sum + row + c * W, r);
+        load_chunk(dy + row + c * W, g);
+        load_f32(weight + c * W, w);
+        if (dsum) load_chunk(dsum + row + c * W, d);
+        if (t != blockIdx.x) load_f32(mine + c * W, a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < W; ++j) {
           const float n = r[j] * rstd;
           a[j] = fmaf(g[j], n, t != blockIdx.x ? a[j] : 0.0f);
           r[j] = rstd * (g[j] * w[j] - n * mean) + (dsum ? d[j] : 0.0f);
         }
-        store_chunk(mine + c * 8, a);
-        store_chunk(dx + row + c * 8, r);
+        store_f32(mine + c * W, a);
+        store_chunk(dx + row + c * W, r);
       }
     }
   }
@@ -343,9 +347,9 @@ rmsnorm_dweight_kernel(const float* __restrict__ part, int nparts, int H,
   if (slice == 0) *reinterpret_cast<f32x4*>(dweight + h) = s;
 }
 
-// Threads of a workgroup for rows held as NC chunks a thread.
-int norm_threads(int H, int nc) {
-  return std::min(1024, (H / kChunk + 64 * nc - 1) / (64 * nc) * 64);
+// Threads of a workgroup for rows of `chunks` held as nc chunks a thread.
+int norm_threads(int chunks, int nc) {
+  return std::min(1024, (chunks + 64 * nc - 1) / (64 * nc) * 64);
 }
 
 // Row sums of dw kept apart at most: two workgroups per CU (256 instead of 512
@@ -373,18 +377,19 @@ static void add_rmsnorm(const void* x, const void* residual, const float* weight
                         bool pow2, hipStream_t s) {
   MOE_TIMED_LAUNCH(s, "add_rmsnorm_kernel",
     hipLaunchKernelGGL((add_rmsnorm_kernel<IO, NC, kNt>), dim3((unsigned)rows),
-                       dim3(norm_threads(H, NC ? NC : 4)), 0, s, (const IO*)x,
+                       dim3(norm_threads(H / kWidth<IO>, NC ? NC : 4)), 0, s, (const IO*)x,
                        (const IO*)residual, weight, eps, H, (IO*)sum, (IO*)y, yq, ys, pow2));
 }
 
-// Chunks of a row that a thread holds in registers: two, four from H = 16384
-// on, none (the row is read twice) past 32768.
+// Chunks of a row that a thread holds in registers: two, four from 2048
+// chunks on, none (the row is read twice) past 4096.
 template <typename IO>
 static hipError_t add_rmsnorm(const void* x, const void* residual, const float* weight, float eps,
                               int64_t rows, int H, void* sum, void* y, uint8_t* yq, float* ys,
                               bool pow2, hipStream_t s) {
-  auto* run = H > 32768   ? add_rmsnorm<IO, 0, false>
-              : H > 16384 ? add_rmsnorm<IO, 4, false>
+  const int chunks = H / kWidth<IO>;
+  auto* run = chunks > 4096   ? add_rmsnorm<IO, 0, false>
+              : chunks > 2048 ? add_rmsnorm<IO, 4, false>
               : rows * H * (int64_t)sizeof(IO) > kStreamBytes ? add_rmsnorm<IO, 2, true>
                                                               : add_rmsnorm<IO, 2, false>;
   run(x, residual, weight, eps, rows, H, sum, y, yq, ys, pow2, s);
@@ -404,17 +409,18 @@ static hipError_t add_rmsnorm_backward(const void* sum, const float* weight, flo
                                        void* dx, float* dweight, float* part, hipStream_t s) {
   const int64_t parts = std::min(rows, kNormParts);
   if (parts) {
-    // Two chunks a thread in bf16, one in fp32; wider rows leave no registers
-    // for a thread's share of dw.
-    constexpr int NC = sizeof(IO) == 2 ? 2 : 1;
-    const bool wide = H > 1024 * NC * kChunk;
+    // Two chunks a thread; wider rows leave no registers for a thread's share
+    // of dw.
+    constexpr int NC = 2;
+    const int chunks = H / kWidth<IO>;
+    const bool wide = chunks > 1024 * NC;
     auto* kernel = wide ? add_rmsnorm_backward_kernel<IO, 0, false>
                    : rows * H * (int64_t)sizeof(IO) > kStreamBytes
                        ? add_rmsnorm_backward_kernel<IO, NC, true>
                        : add_rmsnorm_backward_kernel<IO, NC, false>;
     MOE_TIMED_LAUNCH(s, "add_rmsnorm_backward_kernel",
-      hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(norm_threads(H, wide ? 4 : NC)), 0, s,
-                         (const IO*)sum, weight, eps, (const IO*)dy, (const IO*)dsum, rows, H,
+      hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(norm_threads(chunks, wide ? 4 : NC)),
+                         0, s, (const IO*)sum, weight, eps, (const IO*)dy, (const IO*)dsum, rows, H,
                          (IO*)dx, part));
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

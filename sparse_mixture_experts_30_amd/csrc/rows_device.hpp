@@ -1,13 +1,17 @@
-// Eight consecutive values of a token row, bf16 or fp32 (gfx950 device code),
-// shared by the kernels that work on whole rows.
+// Sixteen bytes of a token row, bf16 or fp32 (gfx950 device code), and sums over
+// lanes, shared by the kernels that work on whole rows.
 #pragma once
 
 #include "moe_internal.hpp"
 
 namespace moe {
 
-// A chunk is eight values: one 16-byte access in bf16, two in fp32.
-constexpr int kChunk = 8;
+// A chunk is one 16-byte access: eight values in bf16, four in fp32.  Eight in
+// fp32 leave every other 16 bytes of the row out of each access: the norm of
+// 3000 x 4096 fp32 rows took 38.7 us instead of 33.3, the gradients of 665
+// tokens of 4352 values (8 slots) 85 instead of 77.
+template <typename IO>
+constexpr int kWidth = 16 / (int)sizeof(IO);
 
 __device__ __forceinline__ void unpack_bf16x8(u32x4 v, float (&f)[8]) {
 #pragma unroll
@@ -49,23 +53,19 @@ struct RawChunk<uint16_t> {
 };
 template <>
 struct RawChunk<float> {
-  f32x4 a, b;
+  f32x4 v;
   template <bool kNt = false>
   __device__ __forceinline__ void load(const float* p) {
-    a = load16<kNt>(reinterpret_cast<const f32x4*>(p));
-    b = load16<kNt>(reinterpret_cast<const f32x4*>(p + 4));
+    v = load16<kNt>(reinterpret_cast<const f32x4*>(p));
   }
-  __device__ __forceinline__ void to(float (&f)[8]) const {
+  __device__ __forceinline__ void to(float (&f)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = a[i];
-      f[4 + i] = b[i];
-    }
+    for (int i = 0; i < 4; ++i) f[i] = v[i];
   }
 };
 
 template <typename IO>
-__device__ __forceinline__ void load_chunk(const IO* p, float (&f)[8]) {
+__device__ __forceinline__ void load_chunk(const IO* p, float (&f)[kWidth<IO>]) {
   RawChunk<IO> r;
   r.load(p);
   r.to(f);
@@ -76,9 +76,25 @@ __device__ __forceinline__ void store_chunk(uint16_t* p, const float (&f)[8]) {
   store16<kNt>(reinterpret_cast<u32x4*>(p), pack_bf16x8(f));
 }
 template <bool kNt = false>
-__device__ __forceinline__ void store_chunk(float* p, const float (&f)[8]) {
+__device__ __forceinline__ void store_chunk(float* p, const float (&f)[4]) {
   store16<kNt>(reinterpret_cast<f32x4*>(p), (f32x4){f[0], f[1], f[2], f[3]});
-  store16<kNt>(reinterpret_cast<f32x4*>(p + 4), (f32x4){f[4], f[5], f[6], f[7]});
+}
+
+// N fp32 values beside a chunk of N values (norm weights and their gradient).
+template <int N>
+__device__ __forceinline__ void load_f32(const float* p, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[i + j] = v[j];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_f32(float* p, const float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<f32x4*>(p + i) = (f32x4){f[i], f[i + 1], f[i + 2], f[i + 3]};
 }
 
 // v as a row of type IO holds it.

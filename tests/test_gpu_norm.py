@@ -62,7 +62,7 @@ def _check_y(y, ref, H, act):
 
 # Every register-held width and the widths past them; rows around a workgroup.
 SIZES = [(1, 64), (1, 7168), (2, 128), (3, 192), (33, 1024), (5, 2048), (4, 2112), (7, 4160), (130, 7168), (3, 8192),
-         (2, 8256), (2, 16384), (2, 32832), (1031, 256),
+         (2, 8256), (2, 16384), (2, 16448), (2, 32768), (2, 32832), (1031, 256),
          (1700, 7168)]   # past the size from which rows are read non-temporally
 
 
