@@ -322,8 +322,10 @@ moe_status moe_quantize_act(const moe_config* cfg, int64_t rows, const void* x, 
  *   sum = x + residual (rounded to act_dtype; sum = x without a residual),
  *   y = sum * rstd * weight,  rstd = 1 / sqrt(mean(sum^2) + eps),
  * and on request y in e4m3 with one fp32 scale per 1x128 tile (the rule of
- * moe_quantize_act, taken from the fp32 y: one rounding).  The norm reads the
- * rounded sum, so that the backward needs nothing but the stored stream.
+ * moe_quantize_act, taken from the fp32 y: one rounding; code = y * 448 / a also
+ * where 448 / a by itself is past fp32, and a tile whose a / 448 rounds to 0 is
+ * one of zeros, scale 1).  The norm reads the rounded sum, so that the backward
+ * needs nothing but the stored stream.
  *   x, residual [rows, H] act_dtype (residual may be NULL); weight [H] fp32;
  *   eps finite and > 0 (a row of zeros gives zeros).
  *   sum [rows, H] act_dtype out, may be NULL, may be x or residual itself;

@@ -49,14 +49,26 @@ __device__ __forceinline__ void row_tile_scale(float amax, bool pow2, float& sca
 }
 
 // e4m3 codes of the 8 values v (one chunk; 16 consecutive lanes hold a tile)
-// and the tile's scale.  All 16 lanes of the tile call this.
-__device__ __forceinline__ uint2 quant_chunk(const float (&v)[8], bool pow2, float& scale) {
+// and the tile's scale.  All 16 lanes of the tile call this; v is scratch.
+__device__ __forceinline__ uint2 quant_chunk(float (&v)[8], bool pow2, float& scale) {
   float m = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
   m = row_max(m);   // the tile's 16 lanes are a row
   float inv;
   row_tile_scale(m, pow2, scale, inv);
+  if (m < 0x1p-119f && m > 0.0f && !pow2) {
+    // 448 / m is past fp32 (its infinity times a zero of the tile is NaN): the
+    // values are lifted by 2^64 first, exactly.  A scale that rounds to 0
+    // makes the tile one of zeros.
+    inv = 448.0f / (m * 0x1p64f);
+    if (scale == 0.0f) {
+      scale = 1.0f;
+      inv = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= 0x1p64f;
+  }
   return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                     e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }

@@ -183,3 +183,26 @@ def test_on_another_stream():
         moe.moe_add_rmsnorm(_cfg(H, "bf16"), T, x, None, w, EPS, y=y)
     s.synchronize()
     assert torch.equal(y, want)
+
+
+# Largest values of a tile around and below those where 448 / a leaves fp32 (1.3e-36), down to its smallest
+# number.  Beside the rounding to e4m3, a scale below 2^-126 is rounded by up to 2^-150 and multiplies codes
+# up to 448, and y itself is rounded by up to 2^-150 for each of two products: 512 x 2^-150 in all.
+@pytest.mark.parametrize("q", ["fp8", "fp8e8m0"])
+@pytest.mark.parametrize("H", [1792, 17920])
+def test_tiles_of_tiny_values(H, q):
+    T, sizes = 3, [1e-34, 1.4e-36, 1.2e-36, 1e-37, 1e-38, 1e-40, 1e-42, 4e-43, 2e-43, 1e-44, 1e-45, 0.0, 1.0, 1e-37]
+    x, g = _rows(18, T, H, "bf16").view(T, -1, 128), np.random.default_rng(19)
+    x[:, :, 1::2] = 0                                          # zeros beside the tiny values
+    x[1, :, 1:] = 0                                            # one value a tile
+    x = x.reshape(T, H)
+    w = (np.repeat(np.resize(np.array(sizes, np.float32), H // 128), 128) * (0.5 + g.random(H))).astype(np.float32)
+    o = _forward(_cfg(H, "bf16", q), x, None, torch.from_numpy(w).to(DEV), ("y", "q"))
+    t = block.rmsnorm(host(x), w, EPS).reshape(T, -1, 128)
+    a, s = np.abs(t).max(axis=2), host(o["ys"]).astype(np.float64)
+    assert np.all(np.isfinite(s)) and np.all(s > 0)
+    v = host(o["yq"].view(torch.float8_e4m3fn).float()).astype(np.float64)
+    assert np.all(np.isfinite(v)) and np.all(v[host(x) == 0] == 0)
+    v = v.reshape(t.shape) * s[:, :, None]
+    scale = a / 448 if q == "fp8" else s
+    assert np.all(np.abs(v - t) <= (2.0 ** -4 * np.abs(t) + 2.0 ** -10 * scale[:, :, None]) * (1 + 1e-4) + 512 * 2.0 ** -150)
