@@ -594,9 +594,13 @@ quantize_int4_kernel(int group, const uint16_t* __restrict__ src, int64_t chunks
 // x 50 94 / 110, 112 x 128 31 / 37, 388 x 22 40 / 45; 640 x 9 141 / 145; 704 x 16
 // 122 / 103, 832 x 25 208 / 179, 416 x 128 193 / 175, 352 x 512 118 / 103, 152 x
 // 1024 166 / 135.
+// The choice is the whole layer's, whichever of its groups the launch computes:
+// the few-row kernel adds k in another order, and a layer gives the same bits
+// with its shared expert in a launch of its own.
 constexpr int kFewAverage = 8, kMidAverage = 28;
 constexpr int64_t kTallGrid = 512, kTallWork = 32768;
-int tile_rows(const FfnDims& d) {
+int tile_rows(FfnDims d) {
+  d.groups = kGroupsAll;
   const int64_t tall = ffn_grid_mtiles(d, kManyRows) * (d.I / 128);
   if (d.T <= kFewRows || d.N <= (int64_t)kFewAverage * d.E ||
       (tall < kTallGrid && tall * d.N < kTallWork * d.E))

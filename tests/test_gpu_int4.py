@@ -260,3 +260,26 @@ def test_experts_on_e4m3_rows(wd):
     moe.moe_expert_ffn_quantized(C, T, xq, xs, _dev(perm), _dev(off), W, *b, ws)
     sync()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# Routed experts and the shared one in one launch and each in its own (moe_forward_overlap): the rows of the whole
+# layer name the kernel, so that the sums have one order.  More than 8 rows an expert and enough tiles of the whole
+# layer for 32 (T = 600) and 64 rows (T = 1000), where the shared expert's tiles alone would be too few.
+@pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
+@pytest.mark.parametrize("T", [600, 1000])
+def test_overlap_has_the_bits_of_forward(wd, T):
+    cfg = synth.C3.replace(name="int4-overlap", T=T, H=512, E=32, G=4, TG=2, K=1, I=2048, Is=2048, rho=2.5, wdtype=wd)
+    C, g, rng = sd.moe_config(cfg), GROUP[wd], np.random.default_rng(T)
+    which = {"w13": (moe.MOE_W13, cfg.E, 2 * cfg.I, cfg.H), "w2": (moe.MOE_W2, cfg.E, cfg.H, cfg.I),
+             "ws13": (moe.MOE_WS13, 1, 2 * cfg.Is, cfg.H), "ws2": (moe.MOE_WS2, 1, cfg.H, cfg.Is)}
+    packed = {k: _pack(C, i, *_matrix(rng, e, n, m, g)) for k, (i, e, n, m) in which.items()}
+    gate = torch.from_numpy(rng.standard_normal((cfg.E, cfg.H)).astype(np.float32) / np.float32(np.sqrt(cfg.H))).to(DEV)
+    bias = torch.zeros(cfg.E, device=DEV)
+    W = moe.weights(gate_w=gate, bias=bias, packed=True, **packed)
+    x = _bf16_dev(rng.standard_normal((T, cfg.H)))
+    out, other, ws, s = torch.empty_like(x), torch.empty_like(x), sd.workspace(cfg, T), torch.cuda.Stream()
+    moe.moe_forward(C, T, x, W, out, ws)
+    sync()
+    moe.moe_forward_overlap(C, T, x, W, other, ws, s)
+    sync()
+    assert torch.equal(out, other)
