@@ -41,6 +41,16 @@ def make_weights(H, E, I, Is, seed=0):
             "ws13": normal(2 * Is, H, std=H ** -0.5).bfloat16(), "ws2": normal(H, Is, std=Is ** -0.5).bfloat16()}
 
 
+def _check_rows(T, H, at_most=None, **rows):
+    """Raises unless every tensor given is [T, H] bf16 without gaps (and T <= at_most): the library takes addresses,
+    and a row more than a buffer holds would be written past its end."""
+    if at_most is not None and T > at_most:
+        raise ValueError(f"{T} tokens, buffers for {at_most}")
+    for name, t in rows.items():
+        if t is not None and (tuple(t.shape) != (T, H) or t.dtype != torch.bfloat16 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous [{T}, {H}] bfloat16 tensor, not {tuple(t.shape)} {t.dtype}")
+
+
 class Serving:
     """One decode or prompt step on 4-bit experts: (x, residual) -> (out, residual)."""
 
@@ -63,6 +73,7 @@ class Serving:
     def step(self, x, residual, out):
         """residual += x in place; out = the layer's output on the normed residual."""
         T = x.shape[0]
+        _check_rows(T, self.H, at_most=self.n.shape[0], x=x, residual=residual, out=out)
         moe.moe_add_rmsnorm(self.cfg, T, x, residual, self.norm, EPS, sum=residual, y=self.n[:T])
         moe.moe_forward(self.cfg, T, self.n[:T], self.weights, out, self.ws)
         return out
@@ -91,6 +102,7 @@ class ServingFp8:
 
     def step(self, x, residual, out):
         T, C = x.shape[0], self.cfg
+        _check_rows(T, self.H, at_most=self.n.shape[0], x=x, residual=residual, out=out)
         moe.moe_add_rmsnorm(C, T, x, residual, self.norm, EPS, sum=residual, y=self.n, yq=self.xq, ys=self.xs)
         moe.moe_gate(C, T, self.n, *self.gate, None, self.idx, self.w, self.ws)
         moe.moe_permute(C, T, self.idx, self.counts, self.off, self.perm, self.pos, self.ws)
@@ -125,6 +137,7 @@ class Training:
     def forward(self, x, residual):
         """(out, sum): the layer's output and the new residual stream."""
         C, T, w = self.cfg, self.T, self.w
+        _check_rows(T, self.n.shape[1], x=x, residual=residual)
         moe.moe_add_rmsnorm(C, T, x, residual, w["norm"], EPS, sum=self.sum, y=self.n)
         moe.moe_gate(C, T, self.n, w["gate_w"], w["bias"], self.logits, self.idx, self.tw, self.ws)
         moe.moe_permute(C, T, self.idx, self.counts, self.off, self.perm, self.pos, self.ws)
@@ -138,6 +151,7 @@ class Training:
         """Gradients of x (and of residual, the same), the norm, the gate, the experts and the adapter, for
         the gradients of forward's two results."""
         C, T, w = self.cfg, self.T, self.w
+        _check_rows(T, self.n.shape[1], dout=dout, dsum=dsum)
         dy, dtw = torch.empty_like(self.y), torch.empty_like(self.tw)
         moe.moe_combine_backward(C, T, dout, self.y, self.pos, self.tw, dy, dtw)
         d = {k: torch.empty_like(w[k]) for k in WHICH}
