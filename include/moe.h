@@ -335,7 +335,10 @@ moe_status moe_quantize_act(const moe_config* cfg, int64_t rows, const void* x, 
  * Rows, weight, dweight, codes and packed weights are 16-byte aligned here and
  * in the calls below on rows and 4-bit weights (MOE_ERR_INVALID_ARG otherwise).
  * A NaN in a row makes the whole row NaN (in e4m3 too); squares are summed in
- * fp32, so values above about 1e19 overflow to rstd = 0.  No workspace. */
+ * fp32, so values above about 1e19 overflow to rstd = 0.  No workspace.
+ * More rows than one launch takes (at least 4 million; 67 million of at most
+ * 1024 bytes) return MOE_ERR_UNSUPPORTED, here and, by tokens, in the row calls
+ * below. */
 moe_status moe_add_rmsnorm(const moe_config* cfg, int64_t rows, const void* x,
                            const void* residual, const float* weight, float eps, void* sum,
                            void* y, uint8_t* yq, float* ys, void* stream);
@@ -529,9 +532,11 @@ moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const voi
  *   moe_quantize_weight: codes and scales of a row-major bf16 matrix, per
  *     group scale = bf16(max |w| / 7), code = round(w / scale) + 8, ties to
  *     even, clamped to 0..15 (scale 0 and codes 8 for a group of zeros).  The
- *     weights are finite.
+ *     weights are finite, at most 2^35 - 2048 of them (MOE_ERR_UNSUPPORTED
+ *     otherwise).
  *   moe_pack_quantized: the layout that the kernels stream, codes and scales
- *     together, into a device buffer of moe_packed_bytes(cfg, which) bytes.
+ *     together, into a device buffer of moe_packed_bytes(cfg, which) bytes
+ *     (below 2^36, MOE_ERR_UNSUPPORTED otherwise).
  *     Per (expert, output tile, 128-k step) one block: eight 1 KiB fragments
  *     of 16 weight rows (tile: 64 h columns of gate and of up for w13 / ws13,
  *     128 output rows for w2 / ws2; fragments 0, 1, 4, 5 of a w13 / ws13 tile

@@ -6,8 +6,13 @@
 
 namespace moe {
 
+// Threads that a launch may have along one grid dimension.
+constexpr int64_t kMaxGridThreads = 0xffffffffLL;
+
 // Expert FFNs on packed 4-bit weights with group scales (ffn_int4.hip);
-// group is 128 or 32.  No tile list.
+// group is 128 or 32.  No tile list.  A matrix is packed by a thread per 16
+// bytes of packed4_bytes and quantised by a thread per 8 values, in one launch
+// each.
 size_t packed4_bytes(bool gate_up, int64_t experts, int n, int kd, int group);
 hipError_t launch_pack_int4(bool gate_up, int group, const uint8_t* codes, const uint16_t* scales,
                             void* dst, int64_t experts, int n, int kd, hipStream_t s);
@@ -18,7 +23,9 @@ hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const
                            const void* ws13p, const void* ws2p, uint16_t* h, uint16_t* y,
                            uint16_t* ys, hipStream_t s);
 
-// Residual add + RMS norm and its backward (norm.hip).
+// Residual add + RMS norm and its backward (norm.hip).  The forward has a
+// workgroup per row, for at most add_rmsnorm_max_rows rows.
+int64_t add_rmsnorm_max_rows(int H, bool bf16);
 hipError_t launch_add_rmsnorm(const void* x, const void* residual, const float* weight, float eps,
                               int64_t rows, int H, bool bf16, void* sum, void* y, uint8_t* yq,
                               float* ys, bool pow2, hipStream_t s);
@@ -28,7 +35,9 @@ hipError_t launch_add_rmsnorm_backward(const void* sum, const float* weight, flo
                                        bool bf16, void* dx, float* dweight, float* part,
                                        hipStream_t s);
 
-// Sorted token rows and the gradients of the two ends (dispatch.hip).
+// Sorted token rows and the gradients of the two ends (dispatch.hip): a
+// workgroup per token, for at most dispatch_max_tokens tokens.
+int64_t dispatch_max_tokens(int64_t row_bytes);
 hipError_t launch_dispatch(const void* x, int64_t row_bytes, const float* xs, int n_scales,
                            const int32_t* pos, int64_t T, int K, void* rows, float* rows_s,
                            hipStream_t s);

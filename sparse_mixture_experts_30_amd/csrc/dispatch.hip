@@ -168,6 +168,11 @@ int row_threads(int64_t T, int64_t pieces) {
   return (int)std::min<int64_t>((pieces + 63) / 64 * 64, T > kCus ? 512 : kMaxThreads);
 }
 
+// From kCus + 1 tokens on the workgroups have one size.
+int64_t dispatch_max_tokens(int64_t row_bytes) {
+  return kMaxGridThreads / row_threads(kCus + 1, row_bytes / 16);
+}
+
 hipError_t launch_dispatch(const void* x, int64_t row_bytes, const float* xs, int n_scales,
                            const int32_t* pos, int64_t T, int K, void* rows, float* rows_s,
                            hipStream_t s) {

@@ -613,7 +613,7 @@ template <bool kGateUp, int kGroup>
 hipError_t launch_gemm(Int4Args a, int rows, int64_t mtiles, int nt, hipStream_t s) {
   a.ntn = rows == kFewRows ? nt : (nt + 1) / 2;
   const int64_t work = mtiles * a.ntn;
-  if (work > 0x7fffffff - kXcdGrid) return hipErrorInvalidValue;
+  if (work > kMaxGridThreads / kThreads4 - kXcdGrid) return hipErrorInvalidValue;
   const dim3 grid(xcd_grid(work));
   if (rows == kFewRows)
     MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int4_few<true>" : "grouped_gemm_int4_few<false>",

@@ -485,6 +485,24 @@ moe_status check_norm(const moe_config* c, int64_t rows, float eps) {
   return MOE_OK;
 }
 
+// The row kernels have a workgroup per token.
+moe_status check_tokens(const moe_config* c, int64_t T, int64_t row_bytes) {
+  CHECK(check_T(T, c));
+  const int64_t most = moe::dispatch_max_tokens(row_bytes);
+  if (T > most)
+    return fail(MOE_ERR_UNSUPPORTED, "%lld tokens: one launch takes %lld rows of %lld bytes",
+                (long long)T, (long long)most, (long long)row_bytes);
+  return MOE_OK;
+}
+
+// The 4-bit quantiser and packer, workgroups of 256 threads.
+moe_status check_matrix_threads(int64_t threads) {
+  if (threads > moe::kMaxGridThreads / 256 * 256)
+    return fail(MOE_ERR_UNSUPPORTED, "the matrix is too large for one launch (take its experts in "
+                "parts, with fewer n_routed_experts)");
+  return MOE_OK;
+}
+
 // ---- the no-allocation forward ----------------------------------------------
 // Workspace of moe_forward_noalloc: one static device array, of which every GPU
 // that runs the library holds its own copy until the process ends.  In host
@@ -842,6 +860,10 @@ moe_status moe_add_rmsnorm(const moe_config* cfg, int64_t rows, const void* x,
   if (yq && cfg->act_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "the e4m3 output takes bf16 activations");
   if (yq && cfg->hidden_size % 128) return fail(MOE_ERR_UNSUPPORTED, "hidden_size %% 128 != 0");
+  const int64_t most = moe::add_rmsnorm_max_rows(cfg->hidden_size, cfg->act_dtype == MOE_BF16);
+  if (rows > most)
+    return fail(MOE_ERR_UNSUPPORTED, "%lld rows: one launch takes %lld of this width",
+                (long long)rows, (long long)most);
   if (rows == 0) return MOE_OK;
   NONNULL(x);
   NONNULL(weight);
@@ -895,7 +917,7 @@ moe_status moe_add_rmsnorm_backward(const moe_config* cfg, int64_t rows, const v
 moe_status moe_dispatch(const moe_config* cfg, int64_t T, const void* x, const int32_t* pos,
                         void* rows, void* stream) {
   CHECK(check_cfg(cfg));
-  CHECK(check_T(T, cfg));
+  CHECK(check_tokens(cfg, T, (int64_t)cfg->hidden_size * act_bytes(cfg)));
   if (T == 0) return MOE_OK;
   NONNULL(x);
   NONNULL(pos);
@@ -912,7 +934,7 @@ moe_status moe_dispatch_quantized(const moe_config* cfg, int64_t T, const uint8_
                                   const float* xs, const int32_t* pos, uint8_t* rows_q,
                                   float* rows_s, void* stream) {
   CHECK(check_cfg(cfg));
-  CHECK(check_T(T, cfg));
+  CHECK(check_tokens(cfg, T, cfg->hidden_size));
   if (cfg->act_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "e4m3 rows belong to bf16 activations");
   if (cfg->hidden_size % 128) return fail(MOE_ERR_UNSUPPORTED, "hidden_size %% 128 != 0");
@@ -933,7 +955,7 @@ moe_status moe_dispatch_quantized(const moe_config* cfg, int64_t T, const uint8_
 moe_status moe_dispatch_backward(const moe_config* cfg, int64_t T, const void* drows,
                                  const void* dx_add, const int32_t* pos, void* dx, void* stream) {
   CHECK(check_cfg(cfg));
-  CHECK(check_T(T, cfg));
+  CHECK(check_tokens(cfg, T, (int64_t)cfg->hidden_size * act_bytes(cfg)));
   if (T == 0) return MOE_OK;
   NONNULL(drows);
   NONNULL(pos);
@@ -952,7 +974,7 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
                                 const int32_t* pos, const float* topk_w, void* dy,
                                 float* dtopk_w, void* stream) {
   CHECK(check_cfg(cfg));
-  CHECK(check_T(T, cfg));
+  CHECK(check_tokens(cfg, T, (int64_t)cfg->hidden_size * act_bytes(cfg)));
   if (T == 0) return MOE_OK;
   NONNULL(dout);
   NONNULL(y);
@@ -1050,6 +1072,7 @@ moe_status moe_quantize_weight(const moe_config* cfg, moe_weight_id which, const
     return fail(MOE_ERR_UNSUPPORTED, "moe_quantize_weight makes 4-bit weights (MOE_INT4_*)");
   Matrix m;
   CHECK(weight_matrix(cfg, which, &m));
+  CHECK(check_matrix_threads(m.experts * (m.gate_up ? 2 : 1) * m.n * (m.kd / 8)));
   NONNULL(src);
   NONNULL(codes);
   NONNULL(scales);
@@ -1069,6 +1092,7 @@ moe_status moe_pack_quantized(const moe_config* cfg, moe_weight_id which, const 
     return fail(MOE_ERR_UNSUPPORTED, "moe_pack_quantized packs 4-bit weights (MOE_INT4_*)");
   Matrix m;
   CHECK(weight_matrix(cfg, which, &m));
+  CHECK(check_matrix_threads((int64_t)(moe_packed_bytes(cfg, which) / 16)));
   NONNULL(codes);
   NONNULL(scales);
   NONNULL(dst);

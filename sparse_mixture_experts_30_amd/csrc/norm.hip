@@ -359,9 +359,15 @@ rmsnorm_dweight_kernel(const float* __restrict__ part, int nparts, int H,
   if (slice == 0) *reinterpret_cast<f32x4*>(dweight + h) = s;
 }
 
-// Threads of a workgroup for rows of `chunks` held as nc chunks a thread.
+// Chunks of a row that a thread of the forward holds in registers: two, four
+// from 2048 chunks on, none (the row is read twice) past 4096.
+int norm_held(int chunks) { return chunks > 4096 ? 0 : chunks > 2048 ? 4 : 2; }
+
+// Threads of a workgroup for rows of `chunks` held as nc chunks a thread (as
+// four if none are held).
 int norm_threads(int chunks, int nc) {
-  return std::min(1024, (chunks + 64 * nc - 1) / (64 * nc) * 64);
+  const int n = nc ? nc : 4;
+  return std::min(1024, (chunks + 64 * n - 1) / (64 * n) * 64);
 }
 
 // Row sums of dw kept apart at most: two workgroups per CU (256 instead of 512
@@ -389,23 +395,26 @@ static void add_rmsnorm(const void* x, const void* residual, const float* weight
                         bool pow2, hipStream_t s) {
   MOE_TIMED_LAUNCH(s, "add_rmsnorm_kernel",
     hipLaunchKernelGGL((add_rmsnorm_kernel<IO, NC, kNt>), dim3((unsigned)rows),
-                       dim3(norm_threads(H / kWidth<IO>, NC ? NC : 4)), 0, s, (const IO*)x,
+                       dim3(norm_threads(H / kWidth<IO>, NC)), 0, s, (const IO*)x,
                        (const IO*)residual, weight, eps, H, (IO*)sum, (IO*)y, yq, ys, pow2));
 }
 
-// Chunks of a row that a thread holds in registers: two, four from 2048
-// chunks on, none (the row is read twice) past 4096.
 template <typename IO>
 static hipError_t add_rmsnorm(const void* x, const void* residual, const float* weight, float eps,
                               int64_t rows, int H, void* sum, void* y, uint8_t* yq, float* ys,
                               bool pow2, hipStream_t s) {
-  const int chunks = H / kWidth<IO>;
-  auto* run = chunks > 4096   ? add_rmsnorm<IO, 0, false>
-              : chunks > 2048 ? add_rmsnorm<IO, 4, false>
+  const int held = norm_held(H / kWidth<IO>);
+  auto* run = held == 0   ? add_rmsnorm<IO, 0, false>
+              : held == 4 ? add_rmsnorm<IO, 4, false>
               : rows * H * (int64_t)sizeof(IO) > kStreamBytes ? add_rmsnorm<IO, 2, true>
                                                               : add_rmsnorm<IO, 2, false>;
   run(x, residual, weight, eps, rows, H, sum, y, yq, ys, pow2, s);
   return hipGetLastError();
+}
+
+int64_t add_rmsnorm_max_rows(int H, bool bf16) {
+  const int chunks = H / (bf16 ? kWidth<uint16_t> : kWidth<float>);
+  return kMaxGridThreads / norm_threads(chunks, norm_held(chunks));
 }
 
 hipError_t launch_add_rmsnorm(const void* x, const void* residual, const float* weight, float eps,
@@ -431,7 +440,7 @@ static hipError_t add_rmsnorm_backward(const void* sum, const float* weight, flo
                        ? add_rmsnorm_backward_kernel<IO, NC, true>
                        : add_rmsnorm_backward_kernel<IO, NC, false>;
     MOE_TIMED_LAUNCH(s, "add_rmsnorm_backward_kernel",
-      hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(norm_threads(chunks, wide ? 4 : NC)),
+      hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(norm_threads(chunks, wide ? 0 : NC)),
                          0, s, (const IO*)sum, weight, eps, (const IO*)dy, (const IO*)dsum, rows, H,
                          (IO*)dx, part));
     hipError_t e = hipGetLastError();

@@ -231,3 +231,45 @@ def test_binding_refuses_gaps():
     t = torch.zeros(8, 512, dtype=torch.bfloat16)[:, :256]
     with pytest.raises(ValueError, match="contiguous"):
         moe.moe_add_rmsnorm(_cfg(), 8, t, None, FAKE, 1e-6, y=FAKE, stream=0)
+
+
+@pytest.mark.parametrize("act,H,rows", [("bf16", 1024, 64), ("bf16", 1088, 128), ("bf16", 7168, 448),
+                                        ("bf16", 16384, 1024), ("bf16", 16448, 576), ("bf16", 32832, 1024),
+                                        ("f32", 512, 64), ("f32", 8192, 1024), ("f32", 8256, 576)])
+def test_norm_of_more_rows_than_a_launch_takes(act, H, rows):
+    """A workgroup of `rows` threads per row; a launch has fewer than 2^32 threads."""
+    most = (2 ** 32 - 1) // rows
+    c = _cfg(H=H, act=act, wdtype=act)
+    for n in (most + 1, 2 ** 31 - 1):
+        assert _call("moe_add_rmsnorm", c, n, FAKE, None, FAKE, 1e-6, None, FAKE, None, None) == UNS, n
+        assert "launch" in moe.moe_last_error()
+    # one fewer passes this check and fails the next
+    assert _call("moe_add_rmsnorm", c, most, None, None, FAKE, 1e-6, None, FAKE, None, None) == INV
+
+
+@pytest.mark.parametrize("name,n", [("moe_dispatch", 3), ("moe_dispatch_quantized", 5), ("moe_dispatch_backward", 4),
+                                    ("moe_combine_backward", 6)])
+def test_more_tokens_than_a_launch_takes(name, n):
+    q = name == "moe_dispatch_quantized"
+    for act, H, threads in (("bf16", 256, 64), ("bf16", 4096, 256 if q else 512), ("bf16", 16384, 512),
+                            ("f32", 1024, 256), ("f32", 64, 64)):
+        if act == "f32" and q:
+            continue
+        c, most = _cfg(H=H, act=act, wdtype=act, K=1), (2 ** 32 - 1) // threads
+        for T in (most + 1, 2 ** 31 - 1):
+            assert _call(name, c, T, *[FAKE] * n) == UNS, (act, H)
+            assert "launch" in moe.moe_last_error()
+        assert _call(name, c, most, *[None] * n) == INV
+
+
+def test_more_4_bit_weights_than_a_launch_takes():
+    def args(I, which, f):
+        return f, _cfg(wdtype="int4g128", E=512, G=1, H=16384, I=I), which
+    # 512 x 2 I x 16384 values: quantised 8 a thread, packed 512 + 16 threads per 128 x 128
+    assert _call(*args(2048, moe.MOE_W13, "moe_quantize_weight"), FAKE, FAKE, FAKE) == UNS
+    assert "launch" in moe.moe_last_error()
+    assert _call(*args(1920, moe.MOE_W13, "moe_quantize_weight"), None, FAKE, FAKE) == INV
+    assert _call(*args(2048, moe.MOE_W13, "moe_pack_quantized"), None, FAKE, FAKE) == INV
+    assert _call(*args(7936, moe.MOE_W13, "moe_pack_quantized"), None, FAKE, FAKE) == INV
+    assert _call(*args(8192, moe.MOE_W13, "moe_pack_quantized"), FAKE, FAKE, FAKE) == UNS
+    assert "launch" in moe.moe_last_error()
