@@ -143,14 +143,19 @@ def _nbytes(t) -> int:
 
 def _current_stream() -> int:
     """Handle of torch's current stream.  Making a Stream object to ask for it
-    costs 2.7 us a call, the handle itself 0.2."""
+    costs 2.7 us a call, the handle itself 0.2; a torch without the functions
+    that give the handle is asked for the Stream."""
     global _current_stream
     import torch
     torch.cuda.current_device()   # initialises torch's GPU state if nothing has
-    handle, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-    def _current_stream():
-        return handle(device())
+    handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if handle and device:
+        def _current_stream():
+            return handle(device())
+    else:
+        def _current_stream():
+            return torch.cuda.current_stream().cuda_stream
     return _current_stream()
 
 
