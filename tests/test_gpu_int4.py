@@ -283,3 +283,34 @@ def test_overlap_has_the_bits_of_forward(wd, T):
     moe.moe_forward_overlap(C, T, x, W, other, ws, s)
     sync()
     assert torch.equal(out, other)
+
+
+@pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
+def test_prompt_rows(wd):
+    """A prompt of 2048 tokens at full width, 2048 rows an expert and more; the first and last rows of every
+    expert and some between against 64 bits."""
+    T, H, E, K, I, Is, g = 2048, 7168, 3, 2, 2048, 2048, GROUP[wd]
+    C, rng = moe.config(H, E, 1, 1, K, I, Is, 1.0, "bf16", wd), np.random.default_rng(12)
+    m = {"w13": _matrix(rng, E, 2 * I, H, g), "w2": _matrix(rng, E, H, I, g),
+         "ws13": _matrix(rng, 1, 2 * Is, H, g), "ws2": _matrix(rng, 1, H, Is, g)}
+    which = {"w13": moe.MOE_W13, "w2": moe.MOE_W2, "ws13": moe.MOE_WS13, "ws2": moe.MOE_WS2}
+    W_keep = {k: _pack(C, which[k], *v) for k, v in m.items()}
+    x = block.bf16(rng.standard_normal((T, H)).astype(np.float32))
+    c = synth.C1.replace(name="int4", T=T, E=E, G=1, TG=1, K=K)
+    _, off, perm, _, _ = run_permute(c, random_routing(T, K, E, seed=13, skew=True))   # expert 0 has every token
+    y = torch.full((T * K, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ys = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((moe.moe_workspace_bytes(C, T),), 0xFF, dtype=torch.uint8, device=DEV)
+    moe.moe_expert_ffn(C, T, _bf16_dev(x), _dev(perm), _dev(off), moe.weights(packed=True, **W_keep), y, ys, ws)
+    sync()
+    y, ys = host(y), host(ys)
+    assert np.all(np.isfinite(y)) and np.all(np.isfinite(ys))
+    for e in range(E + 1):
+        rows = np.arange(off[e], off[e + 1]) if e < E else np.arange(T)
+        rows = np.unique(np.concatenate([rows[:2], rows[rng.integers(0, len(rows), 8)], rows[-2:]]))
+        k13, k2, i = ("w13", "w2", e) if e < E else ("ws13", "ws2", 0)
+        w13, w2 = (block.dequantize_int4(m[k][0][i], m[k][1][i], g) for k in (k13, k2))
+        got, tok = (y[rows], perm[rows] // K) if e < E else (ys[rows], rows)
+        bad = worst_row_rel(got, block.swiglu(x[tok], w13, w2))
+        log(f"int4 prompt {k13} {e} worst row {bad:.2e}")
+        assert bad <= TOL

@@ -206,3 +206,22 @@ def test_tiles_of_tiny_values(H, q):
     v = v.reshape(t.shape) * s[:, :, None]
     scale = a / 448 if q == "fp8" else s
     assert np.all(np.abs(v - t) <= (2.0 ** -4 * np.abs(t) + 2.0 ** -10 * scale[:, :, None]) * (1 + 1e-4) + 512 * 2.0 ** -150)
+
+
+@pytest.mark.parametrize("act,H", [("bf16", 16448), ("f32", 8256)])
+def test_wide_backward_of_many_rows(act, H):
+    """Rows too wide for registers, three to a workgroup: its share of dweight is read back and added to."""
+    T = 1100
+    r, dy, w = _rows(20, T, H, act, 2.0), _rows(21, T, H, act), _weight(22, H)
+    cfg = _cfg(H, act)
+    ws = torch.full((moe.moe_add_rmsnorm_backward_workspace_bytes(cfg, T),), 0xFF, dtype=torch.uint8, device=DEV)
+    dx, dw = torch.full_like(r, float("nan")), torch.full((H,), float("nan"), device=DEV)
+    moe.moe_add_rmsnorm_backward(cfg, T, r, w, EPS, dy, dx, dw, ws)
+    sync()
+    R, G, W = (host(a).astype(np.float64) for a in (r, dy, w))
+    ref, refw = block.rmsnorm_backward(R, W, EPS, G)
+    rstd = 1 / np.sqrt((R * R).mean(axis=1, keepdims=True) + EPS)
+    n, g = R * rstd, G * W
+    mag = rstd * (np.abs(g) + np.abs(n) * np.abs(g * n).mean(axis=1, keepdims=True))
+    assert np.all(np.abs(host(dx) - ref) <= 8 * _c(H) * mag + _u(act) * np.abs(ref))
+    assert np.all(np.abs(host(dw) - refw) <= ((T + 64) * 2.0 ** -24 + 4 * _c(H)) * np.abs(G * n).sum(axis=0))
