@@ -176,7 +176,8 @@ moe_status moe_set_gate_mode(int mode);
  *   offsets [E+1] int32 out: exclusive prefix sum, offsets[E] = T*K
  *   perm    [T*K] int32 out: flat indices f = t*K + k sorted by expert id,
  *           stable (ascending f inside an expert)
- *   pos     [T*K] int32 out: inverse of perm (pos[perm[j]] = j) */
+ *   pos     [T*K] int32 out: inverse of perm (pos[perm[j]] = j); not written
+ *           for a skipped id */
 moe_status moe_permute(const moe_config* cfg, int64_t T, const int32_t* topk_idx,
                        int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* pos,
                        void* ws, size_t ws_bytes, void* stream);

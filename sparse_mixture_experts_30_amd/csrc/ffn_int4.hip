@@ -9,7 +9,11 @@
 // the second sum comes from a matrix instruction against a constant operand
 // of -136 (exact in bf16) that starts the first one's accumulator.  Products
 // are exact in fp32; the group's scale multiplies its fp32 sum, so the codes
-// are never rounded.
+// are never rounded.  (The code under a constant exponent and the offset taken
+// out of the sum are a published way of multiplying 4-bit weights.)  h is
+// rounded to bf16 like the other paths' h, as the second product's operand:
+// outputs are 2.3e-3 from 64 bits instead of 1.7e-3 with the rounding of y
+// alone; an h in fp32 would need three bf16 products for each of these.
 //
 // Layout (pack_int4): per output tile (64 h columns of gate and up together,
 // or 128 output rows of the down projection) and 128-k step one block: eight

@@ -5,7 +5,8 @@
 // and for FP8 experts the same y per 1x128 tile in e4m3: scale a / 448 (or
 // the smallest power of two not below it) with a = max |y| of the tile.  The
 // tile is quantised from the fp32 y, not from its bf16 rounding: one rounding
-// instead of two.
+// instead of two.  Codes are y times 448 / a rather than y over the scale, one
+// multiplication a value: a code at a rounding boundary can differ by a step.
 // Backward, with g = dy * w and n = r * rstd:
 //   dr = rstd * (g - n * mean(g * n)) + dsum,   dw = sum over rows of dy * n.
 // Sums are fp32 in a fixed order.

@@ -287,7 +287,7 @@ def test_overlap_has_the_bits_of_forward(wd, T):
 
 @pytest.mark.parametrize("wd", ["int4g128", "int4g32"])
 def test_prompt_rows(wd):
-    """A prompt of 2048 tokens at full width, 2048 rows an expert and more; the first and last rows of every
+    """A prompt of 2048 tokens at full width, all of them on one expert too; the first and last rows of every
     expert and some between against 64 bits."""
     T, H, E, K, I, Is, g = 2048, 7168, 3, 2, 2048, 2048, GROUP[wd]
     C, rng = moe.config(H, E, 1, 1, K, I, Is, 1.0, "bf16", wd), np.random.default_rng(12)
