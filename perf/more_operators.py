@@ -1,0 +1,384 @@
+"""Cases of the operators of dense layers, of 8-bit serving and of the end of a training step:
+
+  dense        the SwiGLU feed-forward block of the layers without routed experts (bf16)
+  dense_train  its forward and backward, as a training step calls them
+  experts8     the SwiGLU expert products in 8-bit integers, one scale per token and per output channel
+  clip         the global norm over many gradients, and their copies clipped to it
+
+`run` computes them in plain torch (32-bit arithmetic, rounded once) or, with `own` set, through
+the library.  `exact` is the definition in 64 bits."""
+import math
+import random
+
+import torch
+
+own = False
+
+DEV = "cuda"
+CLIP_EPS = 1e-6
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def listed():
+    return [
+        # one new token of one user through a dense layer: the weight stream
+        {"name": "dense-T1", "op": "dense", "T": 1, "H": 7168, "I": 18432},
+        # a ragged chunk of a prompt through a small layer
+        {"name": "dense-T333", "op": "dense", "T": 333, "H": 1024, "I": 2752},
+        # a 4096-token prompt
+        {"name": "dense-T4096", "op": "dense", "T": 4096, "H": 7168, "I": 18432},
+        # training a small layer on an odd number of tokens
+        {"name": "dense-train-T777", "op": "dense_train", "T": 777, "H": 1024, "I": 2752},
+        # a training step of one 4096-token sequence
+        {"name": "dense-train-T4096", "op": "dense_train", "T": 4096, "H": 7168, "I": 18432},
+        # one new token of one user: eight routed experts and the shared one
+        {"name": "experts8-T1", "op": "experts8", "T": 1, "H": 7168, "E": 256, "K": 8, "I": 2048, "Is": 2048, "skew": 0.0},
+        # the 32-token decode batch with skewed expert loads
+        {"name": "experts8-T32", "op": "experts8", "T": 32, "H": 7168, "E": 256, "K": 8, "I": 2048, "Is": 2048, "skew": 1.2},
+        # a smaller layer, odd batch
+        {"name": "experts8-T201", "op": "experts8", "T": 201, "H": 1024, "E": 32, "K": 4, "I": 256, "Is": 384, "skew": 0.5},
+        # a 4096-token prompt: every expert has many rows
+        {"name": "experts8-T4096", "op": "experts8", "T": 4096, "H": 7168, "E": 256, "K": 8, "I": 2048, "Is": 2048, "skew": 0.3},
+        # what is trained of a block whose experts are frozen: the gate's and the norm's gradients (fp32)
+        {"name": "clip-gate-norm", "op": "clip", "E": 64, "H": 1024, "I": 0, "Is": 0, "n": 0, "total": 0},
+        # a whole model's worth of small tensors of odd sizes, both types
+        {"name": "clip-300", "op": "clip", "E": 0, "H": 0, "I": 0, "Is": 0, "n": 300, "total": 30000001},
+        # one layer's gradients: gate and norm (fp32), 32 routed experts and the shared one (bf16)
+        {"name": "clip-layer-E32", "op": "clip", "E": 32, "H": 7168, "I": 2048, "Is": 2048, "n": 0, "total": 0},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _width(rng, lo, hi, step):
+    return max(lo, _log(rng, lo, hi) // step * step)
+
+
+def draw(rng):
+    op = rng.choice(["dense", "dense_train", "experts8", "experts8", "clip"])
+    if op == "experts8":
+        return {"op": op, "T": _log(rng, 1, 4096), "H": _width(rng, 256, 7168, 128), "E": rng.choice([8, 16, 32, 64, 128, 256]),
+                "K": rng.randint(1, 8), "I": _width(rng, 128, 2048, 128), "Is": rng.choice([0, 128, 384, 1024, 2048]),
+                "skew": rng.choice([0.0, 0.5, 1.2])}
+    if op == "clip":
+        c = {"op": op, "E": 0, "H": 0, "I": 0, "Is": 0, "n": 0, "total": 0}
+        if rng.random() < 0.5:
+            c.update(n=_log(rng, 1, 600), total=_log(rng, 1000, 400_000_000))
+        else:
+            c.update(E=rng.choice([2, 8, 16, 32]), H=_width(rng, 128, 7168, 64), I=rng.choice([0, _width(rng, 64, 2048, 64)]))
+            c["Is"] = rng.choice([0, 1024, 2048]) if c["I"] else 0
+        return c
+    return {"op": op, "T": _log(rng, 1, 4096), "H": _width(rng, 128, 7168, 64), "I": _width(rng, 128, 18432, 64)}
+
+
+# ---------------------------------------------------------------- inputs
+
+def _gen(seed, device=DEV):
+    return torch.Generator(device=device).manual_seed(1000003 * (seed % 100003) + 29)
+
+
+def _randn(g, *shape, dtype=torch.bfloat16, std=1.0):
+    """In pieces, so that the fp32 values of a large matrix are never held whole."""
+    out = torch.empty(shape, dtype=dtype, device=DEV)
+    flat = out.view(-1)
+    for i in range(0, flat.numel(), 1 << 28):
+        n = min(1 << 28, flat.numel() - i)
+        flat[i:i + n] = torch.randn(n, generator=g, device=DEV) * std
+    return out
+
+
+def _choose(c, seed, device):
+    """Routing [T, K]: distinct experts from noisy scores, expert loads falling with their rank."""
+    g = _gen(seed + 7, device)
+    s = -torch.log(-torch.log(torch.rand(c["T"], c["E"], generator=g, device=device).clamp_(1e-9, 1 - 1e-7)))
+    rank = torch.randperm(c["E"], generator=g, device=device).float() + 1
+    return torch.topk(s - c["skew"] * torch.log(rank), min(c["K"], c["E"]), dim=1).indices
+
+
+def _sorted(idx, E):
+    """The stable order by expert: offsets and perm (int32)."""
+    flat = idx.reshape(-1)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=flat.device)
+    off[1:] = torch.cumsum(torch.bincount(flat, minlength=E), 0)
+    return off, torch.argsort(flat, stable=True).int()
+
+
+def _codes8(g, experts, rows, cols):
+    """8-bit codes -127..127 and fp32 channel scales of a weight matrix of about N(0, 1/cols)."""
+    q = torch.empty(experts, rows, cols, dtype=torch.int8, device=DEV)
+    for e in range(experts):
+        q[e] = (torch.randn(rows, cols, generator=g, device=DEV) * 32.0).clamp_(-127, 127).round_()
+    s = (0.7 + 0.6 * torch.rand(experts, rows, generator=g, device=DEV)) / (32.0 * math.sqrt(cols))
+    return q, s
+
+
+def _grad_shapes(c):
+    """(numbers, type) of every gradient."""
+    if c["n"]:
+        r = random.Random(c["n"] * 1000003 + c["total"])
+        w = [math.exp(r.uniform(0.0, 7.0)) for _ in range(c["n"])]
+        return [(max(1, int(c["total"] * v / sum(w))), "f32" if r.random() < 0.3 else "bf16") for v in w]
+    E, H, I, Is = c["E"], c["H"], c["I"], c["Is"]
+    out = [(E * H, "f32"), (H, "f32")]
+    if I:
+        out += [(E * 2 * I * H, "bf16"), (E * H * I, "bf16")]
+    if Is:
+        out += [(2 * Is * H, "bf16"), (H * Is, "bf16")]
+    return out
+
+
+def _views(c, flat):
+    """The gradients as pieces of one buffer per type, one after another without gaps."""
+    at, out = dict.fromkeys(flat, 0), []
+    for n, t in _grad_shapes(c):
+        out.append(flat[t][at[t]:at[t] + n])
+        at[t] += n
+    return out
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    if own:
+        _prepare_own(s, case)
+    return s
+
+
+def _inputs(c, seed):
+    g = _gen(seed)
+    s = {"c": c}
+    if c["op"] == "clip":
+        shapes = _grad_shapes(c)
+        s["flat"] = {t: torch.empty(sum(n for n, u in shapes if u == t), dtype=DT[t], device=DEV) for t in DT}
+        s["grads"] = _views(c, s["flat"])
+        for i, t in enumerate(s["grads"]):
+            t.copy_(_randn(g, t.numel(), dtype=t.dtype, std=10.0 ** (0.5 * (i % 5) - 3.0)))
+        # about the usual choice, 1, for the norm of these: the gradients are scaled to a fraction of theirs
+        total = math.sqrt(sum(n * 10.0 ** (2.0 * (0.5 * (i % 5) - 3.0)) for i, (n, _) in enumerate(shapes)))
+        s["max_norm"] = 0.37 * total
+        return s
+    T, H, I = c["T"], c["H"], c["I"]
+    s["T"] = T
+    s["x"] = _randn(g, T, H)
+    if c["op"] == "experts8":
+        s["off"], s["perm"] = _sorted(_choose(c, seed, DEV), c["E"])
+        s["K"] = min(c["K"], c["E"])
+        s["w13"], s["w2"] = _codes8(g, c["E"], 2 * I, H), _codes8(g, c["E"], H, I)
+        if c["Is"]:
+            s["ws13"], s["ws2"] = _codes8(g, 1, 2 * c["Is"], H), _codes8(g, 1, H, c["Is"])
+        return s
+    s["w13"], s["w2"] = _randn(g, 2 * I, H, std=H ** -0.5), _randn(g, H, I, std=I ** -0.5)
+    if c["op"] == "dense_train":
+        s["dy"] = _randn(g, T, H)
+    return s
+
+
+def _prepare_own(s, c):
+    """The library's config, and the output buffers, workspace and packed weights that a program keeps."""
+    import sparse_mixture_experts_30_amd as moe
+
+    def new(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device=DEV)
+
+    if c["op"] == "clip":
+        s["out"] = {t: torch.empty_like(b) for t, b in s["flat"].items()}
+        s["list"] = moe.gradients(s["grads"], _views(c, s["out"]))
+        s["norm"] = new(1, dtype=torch.float32)
+        s["ws"] = new(moe.moe_grad_norm_workspace_bytes(s["list"]), dtype=torch.uint8)
+        return
+    T, H, I = s["T"], c["H"], c["I"]
+    if c["op"] == "experts8":
+        s["cfg"] = C = moe.config(H, c["E"], 1, 1, s["K"], I, c["Is"], 1.0, "bf16", "int8")
+        packed = {}
+        for name, which in (("w13", moe.MOE_W13), ("w2", moe.MOE_W2), ("ws13", moe.MOE_WS13), ("ws2", moe.MOE_WS2)):
+            if name in s:
+                packed[name] = new(moe.moe_packed_bytes(C, which), dtype=torch.uint8)
+                moe.moe_pack_weight(C, which, s[name][0], packed[name])
+                packed[name + "_scale"] = s[name][1]
+        for name in ("w13", "w2", "ws13", "ws2"):
+            if name in s:
+                s[name] = (packed[name], packed[name + "_scale"])
+        s["W"] = moe.weights(packed=True, **packed)
+        s["y"], s["y_shared"] = new(T * s["K"], H), new(T, H) if c["Is"] else None
+        s["ws"] = new(moe.moe_workspace_bytes(C, T), dtype=torch.uint8)
+        return
+    s["cfg"] = C = moe.config(H, 2, 1, 1, 1, 64, I, 1.0, "bf16", "bf16")
+    s["W"] = moe.weights(ws13=s["w13"], ws2=s["w2"])
+    s["y"] = new(T, H)
+    ws = moe.moe_dense_ffn_workspace_bytes(C, T)
+    if c["op"] == "dense_train":
+        s["gu"], s["dx"] = new(T, 2 * I), new(T, H)
+        s["dw13"], s["dw2"] = torch.empty_like(s["w13"]), torch.empty_like(s["w2"])
+        ws = max(ws, moe.moe_dense_ffn_backward_workspace_bytes(C, T))
+    s["ws"] = new(ws, dtype=torch.uint8)
+
+
+# ---------------------------------------------------------------- one pass
+
+def run(state):
+    return (_own if own else _plain)[state["c"]["op"]](state)
+
+
+def _own_dense(s):
+    import sparse_mixture_experts_30_amd as moe
+    moe.moe_dense_ffn(s["cfg"], s["T"], s["x"], s["W"], s["y"], s["ws"])
+    return {"y": s["y"]}
+
+
+def _own_dense_train(s):
+    import sparse_mixture_experts_30_amd as moe
+    moe.moe_dense_ffn(s["cfg"], s["T"], s["x"], s["W"], s["y"], s["ws"], gu=s["gu"])
+    moe.moe_dense_ffn_backward(s["cfg"], s["T"], s["x"], s["W"], s["dy"], s["dx"], s["dw13"], s["dw2"], s["ws"], gu=s["gu"])
+    return {"y": s["y"], "dx": s["dx"], "dw13": s["dw13"], "dw2": s["dw2"]}
+
+
+def _own_experts8(s):
+    import sparse_mixture_experts_30_amd as moe
+    moe.moe_expert_ffn(s["cfg"], s["T"], s["x"], s["perm"], s["off"], s["W"], s["y"], s["y_shared"], s["ws"])
+    return {"y": s["y"], "y_shared": s["y_shared"]}
+
+
+def _own_clip(s):
+    import sparse_mixture_experts_30_amd as moe
+    moe.moe_clip_grads(s["list"], s["max_norm"], s["norm"], s["ws"])
+    return {"norm": s["norm"], **s["out"]}
+
+
+def _gated(s):
+    g, u = (s["x"].float() @ s["w13"].float().t()).chunk(2, dim=1)
+    return g, u, 1.0 / (1.0 + torch.exp(-g))
+
+
+def _plain_dense(s):
+    g, u, sig = _gated(s)
+    return {"y": ((g * sig * u) @ s["w2"].float().t()).to(s["x"].dtype)}
+
+
+def _plain_dense_train(s):
+    g, u, sig = _gated(s)
+    h = g * sig * u
+    w2, dy, x = s["w2"].float(), s["dy"].float(), s["x"].float()
+    y = h @ w2.t()
+    dh = dy @ w2
+    dgu = torch.cat((dh * u * sig * (1.0 + g * (1.0 - sig)), dh * g * sig), dim=1)
+    bf = s["x"].dtype
+    return {"y": y.to(bf), "dx": (dgu @ s["w13"].float()).to(bf), "dw13": (dgu.t() @ x).to(bf), "dw2": (dy.t() @ h).to(bf)}
+
+
+def _quant8(v):
+    """Values -127..127 and scales of rows [.., n, cols]: the nearest multiple of max |v| / 127, ties to even, found in 64
+    bits (a quotient next to a half rounds the wrong way in 32)."""
+    d = v.double()
+    a = d.abs().amax(dim=-1, keepdim=True)
+    q = torch.where(a > 0, d * 127.0 / a, torch.zeros_like(d)).round()
+    return q.float(), torch.where(a > 0, a / 127.0, torch.ones_like(a)).float()
+
+
+def _swiglu8(w13, w2, x):
+    """[experts, n, H] of x [experts, n, H]: both products of 8-bit integers, h quantised per row like x."""
+    q, s = _quant8(x)
+    gu = torch.bmm(q, w13[0].float().transpose(1, 2).contiguous()) * s * w13[1][:, None, :]
+    g, u = gu.chunk(2, dim=2)
+    q, s = _quant8(g / (1.0 + torch.exp(-g)) * u)
+    return torch.bmm(q, w2[0].float().transpose(1, 2).contiguous()) * s * w2[1][:, None, :]
+
+
+def _plain_experts8(s):
+    """Every expert that has rows, on its rows, padded to the longest expert's; some experts at a time."""
+    T, K, x = s["T"], s["K"], s["x"].float()
+    N, H = T * K, x.shape[1]
+    counts = (s["off"][1:] - s["off"][:-1]).long()
+    active = counts.nonzero()[:, 0]
+    n = counts[active]
+    e = torch.repeat_interleave(torch.arange(active.numel(), device=DEV), n, output_size=N)
+    at = torch.arange(N, device=DEV) - s["off"][active].long()[e]
+    xt = torch.zeros(active.numel(), int(n.max()), H, device=DEV)
+    xt[e, at] = x[(s["perm"] // K).long()]
+    y = torch.empty_like(xt)
+    for i in range(0, active.numel(), 64):
+        part = active[i:i + 64]
+        w13, w2 = (tuple(t[part] for t in s[name]) for name in ("w13", "w2"))
+        y[i:i + 64] = _swiglu8(w13, w2, xt[i:i + 64])
+    ys = _swiglu8(s["ws13"], s["ws2"], x[None])[0].to(s["x"].dtype) if s["c"]["Is"] else None
+    return {"y": y[e, at].to(s["x"].dtype), "y_shared": ys}
+
+
+def _plain_clip(s):
+    total = sum((t.float() * t.float()).sum(dtype=torch.float64) for t in s["grads"])
+    norm = total.sqrt().float().reshape(1)
+    factor = torch.where(torch.isfinite(norm), (s["max_norm"] / (norm + CLIP_EPS)).clamp(max=1.0), torch.ones_like(norm))
+    out = {t: torch.empty_like(b) for t, b in s["flat"].items()}
+    for t, o in zip(s["grads"], _views(s["c"], out)):
+        o.copy_(t.float() * factor)
+    return {"norm": norm, **out}
+
+
+_own = {"dense": _own_dense, "dense_train": _own_dense_train, "experts8": _own_experts8, "clip": _own_clip}
+_plain = {"dense": _plain_dense, "dense_train": _plain_dense_train, "experts8": _plain_experts8, "clip": _plain_clip}
+
+
+# ---------------------------------------------------------------- what a pass has to move and compute
+
+def work(case):
+    c = case
+    if c["op"] == "clip":
+        shapes = _grad_shapes(c)
+        return {"bytes": sum(2 * n * (4 if t == "f32" else 2) for n, t in shapes) + 4, "flops": 3 * sum(n for n, _ in shapes)}
+    T, H, I = c["T"], c["H"], c["I"]
+    if c["op"] == "dense":
+        return {"bytes": 6 * H * I + 4 * T * H, "flops": 6 * T * H * I}
+    if c["op"] == "dense_train":
+        return {"bytes": 12 * H * I + 8 * T * H, "flops": 18 * T * H * I}
+    K, Is = min(c["K"], c["E"]), c["Is"]
+    N = T * K
+    active = int(torch.unique(_choose(c, 0, "cpu")).numel())  # experts that a batch of this kind reaches
+    return {"bytes": 3 * H * (active * I + Is) + 4 * (active * (2 * I + H) + (2 * Is + H if Is else 0)) + 2 * T * H
+            + 2 * (N + (T if Is else 0)) * H + 4 * N, "flops": 6 * H * (N * I + T * Is)}
+
+
+# ---------------------------------------------------------------- the definition in 64 bits
+
+def exact(case, seed):
+    s = _inputs(case, seed)
+    c = case
+    d = lambda t: t.to(torch.float64)  # noqa: E731
+    if c["op"] == "clip":
+        norm = math.sqrt(math.fsum(float(torch.linalg.vector_norm(p.double())) ** 2 for t in s["grads"] for p in t.split(1 << 28)))
+        factor = min(1.0, s["max_norm"] / (norm + CLIP_EPS))
+        return {"norm": torch.tensor([norm], dtype=torch.float64, device=DEV), **{t: d(b) * factor for t, b in s["flat"].items()}}
+    if c["op"] in ("dense", "dense_train"):
+        x, I = d(s["x"]), c["I"]
+        g, u = x @ d(s["w13"][:I]).T, x @ d(s["w13"][I:]).T
+        a = torch.sigmoid(g)
+        h = a * g * u
+        out = {"y": h @ d(s["w2"]).T}
+        if c["op"] == "dense_train":
+            dy = d(s["dy"])
+            out["dw2"] = dy.T @ h
+            dh = dy @ d(s["w2"])
+            dg, du = dh * u * (a + g * a * (1 - a)), dh * a * g
+            out["dx"] = dg @ d(s["w13"][:I]) + du @ d(s["w13"][I:])
+            out["dw13"] = torch.cat((dg.T @ x, du.T @ x))
+        return {k: out[k] for k in ("y", "dx", "dw13", "dw2") if k in out}
+
+    def whole(v):
+        """Rows as 8-bit whole numbers times a scale."""
+        m = v.abs().max(dim=1).values
+        m = torch.where(m > 0, m, torch.full_like(m, 127.0))[:, None]
+        return torch.round(v * 127 / m), m / 127
+
+    def ffn(w13, w2, e, x):
+        q, step = whole(x)
+        gu = (q @ d(w13[0][e]).T) * step * d(w13[1][e])
+        n = gu.shape[1] // 2
+        q, step = whole(gu[:, n:] * gu[:, :n] * torch.sigmoid(gu[:, :n]))
+        return (q @ d(w2[0][e]).T) * step * d(w2[1][e])
+
+    x, off, K = d(s["x"]), s["off"].tolist(), s["K"]
+    tok = s["perm"].long() // K
+    y = torch.empty(c["T"] * K, c["H"], dtype=torch.float64, device=DEV)
+    for e in range(c["E"]):
+        if off[e + 1] > off[e]:
+            y[off[e]:off[e + 1]] = ffn(s["w13"], s["w2"], e, x[tok[off[e]:off[e + 1]]])
+    return {"y": y, "y_shared": ffn(s["ws13"], s["ws2"], 0, x) if c["Is"] else None}
