@@ -34,7 +34,8 @@
  *     for the last failing call on the calling thread.
  *   - Layouts are row-major.  Weight matrices are stored "output rows x
  *     input columns" with the input dimension contiguous.
- *   - T == 0 is a no-op returning MOE_OK (but see moe_add_rmsnorm_backward).
+ *   - T == 0 is a no-op returning MOE_OK (but see moe_add_rmsnorm_backward and
+ *     moe_dense_ffn_backward).
  *   - Global state: the kernel timer below (off by default), the gate mode
  *     (moe_set_gate_mode, split by default), kernel attributes set once per
  *     process on first use, the two fork/join events of moe_forward_overlap (per device and host
@@ -74,7 +75,11 @@ typedef enum {
     MOE_INT4_G128 = 4, /* 4-bit weights, one bf16 scale per 128 inputs of each
                           output row (bf16 activations, packed weights only,
                           forward only; see moe_pack_quantized)               */
-    MOE_INT4_G32 = 5   /* the same, one bf16 scale per 32 inputs               */
+    MOE_INT4_G32 = 5,  /* the same, one bf16 scale per 32 inputs               */
+    MOE_INT8 = 6       /* 8-bit integers, one fp32 scale per output channel; the
+                          activations are quantised to 8-bit integers with one
+                          scale per token row (packed weights only, forward
+                          only; sizes up to 131072; see moe_quantize_weight)  */
 } moe_dtype;
 
 /* Layer shape: the MoEGate constructor arguments of the first page's
@@ -91,8 +96,8 @@ typedef struct {
     moe_dtype act_dtype;              /* x, expert outputs and layer output:
                                          MOE_F32 or MOE_BF16                        */
     moe_dtype weight_dtype;           /* expert and shared weights: MOE_F32 (with
-                                         act F32), MOE_BF16, MOE_FP8_E4M3* or
-                                         MOE_INT4_* (with act BF16)                 */
+                                         act F32), MOE_BF16, MOE_FP8_E4M3*,
+                                         MOE_INT4_* or MOE_INT8 (with act BF16)     */
 } moe_config;
 
 /* Layer weights.  The gate weight and the selection bias are always fp32.
@@ -100,9 +105,12 @@ typedef struct {
  * projection (rows I..2I-1).  For MOE_FP8_E4M3 the *_scale arrays hold one
  * fp32 per 128x128 block, row-major over (row block, column block); for
  * MOE_FP8_E4M3_E8M0 every scale must be a power of two (the kernels read its
- * exponent field); the scales are ignored (may be NULL) otherwise.  ws13/ws2 (+scales) may be NULL iff Is == 0.
+ * exponent field); for MOE_INT8 they hold one fp32 per output channel
+ * (w13_scale [E, 2I], w2_scale [E, H], ws13_scale [2Is], ws2_scale [H], 16-byte
+ * aligned); the scales are ignored (may be NULL) otherwise.  ws13/ws2 (+scales) may be NULL iff Is == 0.
  * packed = 0: w13, w2, ws13, ws2 are row-major as shown; packed = 1: all four
- * were rearranged by moe_pack_weight (bf16 or e4m3 weights; scales unchanged).
+ * were rearranged by moe_pack_weight (bf16, e4m3 or 8-bit integer weights; scales
+ * unchanged).  MOE_INT8 weights are always packed.
  * MOE_INT4_* weights are always packed, by moe_pack_quantized, which stores
  * their scales among the codes: the *_scale arrays are ignored. */
 typedef struct {
@@ -197,17 +205,21 @@ moe_status moe_permute(const moe_config* cfg, int64_t T, const int32_t* topk_idx
  * (its accumulation carries about 13 fraction bits per instruction, below
  * the bf16 rounding of the outputs).  4-bit weights: bf16 MFMA on the codes
  * as bf16 numbers (exact), each group's scale applied to its fp32 sum, h kept
- * in bf16.  f32: fp32 arithmetic throughout. */
+ * in bf16.  8-bit integer weights: x and h quantised per row (see
+ * moe_quantize_act; h from its fp32 values), sums in 32-bit integers over the
+ * whole k (exact), scaled by the row's and the channel's scale in fp32.  f32:
+ * fp32 arithmetic throughout. */
 moe_status moe_expert_ffn(const moe_config* cfg, int64_t T, const void* x, const int32_t* perm,
                           const int32_t* offsets, const moe_weights* w, void* y, void* y_shared,
                           void* ws, size_t ws_bytes, void* stream);
 
 /* moe_expert_ffn on token rows that are already e4m3 with one fp32 scale per
- * 1x128 tile, as moe_quantize_act or moe_add_rmsnorm writes them: the same
- * products without quantising x again.
- *   xq [T, H] uint8, xs [T, H/128] fp32 (powers of two for MOE_FP8_E4M3_E8M0);
- *   the rest as moe_expert_ffn.  MOE_ERR_UNSUPPORTED unless the weights are
- *   e4m3. */
+ * 1x128 tile, as moe_quantize_act or moe_add_rmsnorm writes them, or already
+ * 8-bit integers (moe_quantize_act): the same products without quantising x
+ * again.
+ *   xq [T, H] uint8, xs [T, H/128] fp32 (powers of two for MOE_FP8_E4M3_E8M0),
+ *   with MOE_INT8 int8 codes and xs [T]; the rest as moe_expert_ffn.
+ *   MOE_ERR_UNSUPPORTED unless the weights are e4m3 or 8-bit integers. */
 moe_status moe_expert_ffn_quantized(const moe_config* cfg, int64_t T, const uint8_t* xq,
                                     const float* xs, const int32_t* perm, const int32_t* offsets,
                                     const moe_weights* w, void* y, void* y_shared, void* ws,
@@ -315,7 +327,15 @@ moe_status moe_forward_noalloc(const moe_config* cfg, int64_t T, const void* x,
  * saturated at +-448.  With weight_dtype MOE_FP8_E4M3_E8M0 the scale is
  * instead the smallest power of two 2^e >= a / 448 (e in [-126, 127]) and
  * inv = 2^-e, so v * inv is exact.
- *   xq [rows, H] uint8 out, xs [rows, H/128] fp32 out. */
+ *   xq [rows, H] uint8 out, xs [rows, H/128] fp32 out.
+ * With weight_dtype MOE_INT8: 8-bit integers, one scale per row.  a = max |v| of
+ * the row, scale = a / 127 in fp32, code = the integer nearest to 127 v / a, ties
+ * to even (of the exact quotient), in -127..127; scale 1 and codes 0 for a row of
+ * zeros, scale NaN and codes 0 for one with a NaN or an infinity.  Rows whose
+ * maximum is below about 2^-119 have a scale among the subnormals, with fewer
+ * bits.
+ *   xq [rows, H] int8 out, xs [rows] fp32 out; x and xq 16-byte aligned, at
+ *   most 16.7 million rows (MOE_ERR_UNSUPPORTED). */
 moe_status moe_quantize_act(const moe_config* cfg, int64_t rows, const void* x, uint8_t* xq,
                             float* xs, void* stream);
 
@@ -393,6 +413,79 @@ moe_status moe_dispatch_backward(const moe_config* cfg, int64_t T, const void* d
 moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* dout, const void* y,
                                 const int32_t* pos, const float* topk_w, void* dy,
                                 float* dtopk_w, void* stream);
+
+/* The feed-forward block of a layer without routed experts (the first layers of
+ * the model are dense: "从 1024 块 GPU 到 558 万美元：拆解 DeepSeek-V3 的算法-系统
+ * 协同设计", section 2.2): the shared expert of cfg and w by itself,
+ *   y = W2 (silu(W_gate x) * (W_up x)),
+ * with ws13 and ws2 (and their scales) of w, of width shared_intermediate_size;
+ * the routed sizes of cfg take no part and the routed weights may be NULL.
+ *   x [T, H], y [T, H] act_dtype, 16-byte aligned.  Every weight type and layout
+ *   that the shared expert takes.
+ *   gu [T, 2Is] bf16 out, for the backward: the gate's and the up projection's
+ *   outputs side by side (NULL: not kept; row-major bf16 weights only,
+ *   MOE_ERR_UNSUPPORTED otherwise).
+ * bf16 weights: h kept in bf16; fp32 accumulation.
+ * Row-major bf16 weights serve training and prompts; a few tokens at a time
+ * read either layout at the rate of memory.
+ * Workspace: moe_dense_ffn_workspace_bytes(cfg, T) bytes (0 for a configuration
+ * it does not handle, shared_intermediate_size == 0 among them). */
+size_t moe_dense_ffn_workspace_bytes(const moe_config* cfg, int64_t T);
+moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w,
+                         void* gu, void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward, for row-major bf16 weights.  With [g u] = gu and dy the gradient
+ * of y:
+ *   dh = dy W2;  dg = dh u silu'(g);  du = dh silu(g);
+ *   dx = [dg du] W13;  dW2 = dy^T h;  dW13 = [dg du]^T x,  h = silu(g) u.
+ * g, u, h and [dg du] are bf16 operands, every product accumulates in fp32.
+ *   x, dy [T, H] bf16; gu [T, 2Is] as the forward wrote it (NULL: computed again
+ *   from x); dx [T, H] bf16 out (may be dy itself; NULL: not wanted); dws13
+ *   [2Is, H], dws2 [H, Is] bf16 out, written whole, zeros for T == 0 (the outputs
+ *   that a call without tokens writes).
+ * Workspace: moe_dense_ffn_backward_workspace_bytes(cfg, T) bytes, 256-byte
+ * aligned (0 for a configuration it does not handle; not needed for T == 0). */
+size_t moe_dense_ffn_backward_workspace_bytes(const moe_config* cfg, int64_t T);
+moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* x,
+                                  const moe_weights* w, const void* gu, const void* dy, void* dx,
+                                  void* dws13, void* dws2, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* A list of gradients, in host arrays of n that the call reads before it
+ * returns: device addresses, numbers of values (0 is allowed) and types
+ * (MOE_F32 or MOE_BF16, mixed as they come; aligned to their type), and where
+ * moe_clip_grads writes the scaled ones (an entry may be the gradient itself;
+ * out may be NULL for moe_grad_norm). */
+typedef struct {
+    int32_t n;
+    const void* const* grad;
+    void* const* out;
+    const int64_t* count;
+    const int32_t* dtype;     /* moe_dtype */
+} moe_gradients;
+
+/* The global norm of all gradients together: norm = sqrt(sum of squares), the
+ * sum in 64 bits in a fixed order, the result rounded to fp32.
+ *   norm [1] fp32 out (device); a NaN or infinity among the gradients gives
+ *   NaN or infinity; 0 for an empty list.
+ * Workspace: moe_grad_norm_workspace_bytes(g) bytes (it depends on n alone),
+ * 256-byte aligned. */
+size_t moe_grad_norm_workspace_bytes(const moe_gradients* g);
+moe_status moe_grad_norm(const moe_gradients* g, float* norm, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* Clipping by the global norm: out = grad * min(1, max_norm / (norm + 1e-6)), the
+ * product in fp32, rounded once to the gradient's type.  The factor is 1 if the
+ * norm is not finite: the gradients stay what they are, and the caller sees
+ * the norm.
+ *   norm_given = 0: norm [1] is written first, as by moe_grad_norm (ws as there);
+ *   norm_given = 1: norm [1] is read (device), e.g. after the squares of several
+ *   ranks' norms were added; ws may be NULL.
+ *   max_norm >= 0, infinity allowed (MOE_ERR_INVALID_ARG otherwise).
+ * An output must not overlap another entry's gradient or output, nor its own
+ * gradient in part (MOE_ERR_INVALID_ARG). */
+moe_status moe_clip_grads(const moe_gradients* g, float max_norm, float* norm, int norm_given,
+                          void* ws, size_t ws_bytes, void* stream);
 
 /* Backward of the grouped SwiGLU expert FFN, for training.  The experts are
  * SwiGLU FFNs (mqxn.cn/news/19449, section 3.1) over the routed rows and the
@@ -515,10 +608,14 @@ moe_status moe_bias_update(const moe_config* cfg, const int32_t* counts, float g
  *   (cb = 1); w2/ws2 row 256 t + 64 w + 32 cb + l % 32.  Rows past the
  *   matrix are zero.  The fp8 block scales keep their row-major layout.
  * Pack once when the weights are loaded.
+ *   8-bit integers: k steps of 128; tiles and blocks as for 4-bit weights below,
+ *         16 KiB each: eight fragments of 16 rows, [k half 2][lane 64] x 16
+ *         bytes, lane l holding row l % 16, k = 128 step + 64 half +
+ *         16 (l / 16) + 0..15.
  *   moe_packed_bytes: size of the packed copy of matrix `which` (0 for an
  *     invalid or fp32 config, or for MOE_WS13/MOE_WS2 when Is == 0).
  *   moe_pack_weight: src is the row-major matrix (w13 [E,2I,H], w2 [E,H,I],
- *     ws13 [2Is,H] or ws2 [H,Is], bf16 or e4m3), dst a device buffer of
+ *     ws13 [2Is,H] or ws2 [H,Is], bf16, e4m3 or int8), dst a device buffer of
  *     moe_packed_bytes(cfg, which) bytes (tile padding is zero-filled). */
 size_t moe_packed_bytes(const moe_config* cfg, moe_weight_id which);
 moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const void* src,
@@ -535,7 +632,10 @@ moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const voi
  *     even, clamped to 0..15 (scale 0 and codes 8 for a group of zeros).  The
  *     weights are finite, at most 2^35 - 2048 of them (MOE_ERR_UNSUPPORTED
  *     otherwise).
- *   moe_pack_quantized: the layout that the kernels stream, codes and scales
+ *     With MOE_INT8: codes [experts, rows, kd] int8 and scales [experts, rows] fp32
+ *     of every row by the rule of moe_quantize_act (at most 16.7 million rows),
+ *     the codes for moe_pack_weight, the scales for the *_scale arrays.
+ *   moe_pack_quantized: the layout that the kernels stream, 4-bit codes and scales
  *     together, into a device buffer of moe_packed_bytes(cfg, which) bytes
  *     (below 2^36, MOE_ERR_UNSUPPORTED otherwise).
  *     Per (expert, output tile, 128-k step) one block: eight 1 KiB fragments

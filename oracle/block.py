@@ -81,3 +81,44 @@ def swiglu(x, w13, w2) -> np.ndarray:
     gu = x @ w13.T
     g, u = np.split(gu, 2, axis=1)
     return (g / (1.0 + np.exp(-g)) * u) @ w2.T
+
+
+def _sigmoid(g):
+    return 1.0 / (1.0 + np.exp(-g))
+
+
+def swiglu_backward(x, w13, w2, dy):
+    """(dx, dw13, dw2) of swiglu for the output gradient dy."""
+    x, w13, w2, dy = (np.asarray(a, np.float64) for a in (x, w13, w2, dy))
+    g, u = np.split(x @ w13.T, 2, axis=1)
+    s = _sigmoid(g)
+    dh = dy @ w2
+    da = np.concatenate([dh * u * (s + g * s * (1.0 - s)), dh * g * s], axis=1)
+    return da @ w13, da.T @ x, dy.T @ (g * s * u)
+
+
+def quantize_int8(v):
+    """(codes -127..127, scales) of rows v [.., n, cols]: per row max |v| / 127, ties to even; scales in 64 bits."""
+    v = np.asarray(v, np.float64)
+    a = np.abs(v).max(axis=-1, keepdims=True)
+    q = np.where(a > 0, np.rint(v * 127.0 / np.where(a > 0, a, 1.0)), 0.0)
+    return q, np.where(a > 0, a / 127.0, 1.0)[..., 0]
+
+
+def int8_product(q, s, codes, scales) -> np.ndarray:
+    """s[t] scales[n] sum_k q[t, k] codes[n, k]."""
+    return (np.asarray(q, np.float64) @ np.asarray(codes, np.float64).T) * s[:, None] * np.asarray(scales, np.float64)
+
+
+def swiglu_int8(x, w13, w2):
+    """SwiGLU with both products in 8-bit integers; w13, w2 are (codes, channel scales)."""
+    g, u = np.split(int8_product(*quantize_int8(x), *w13), 2, axis=1)
+    return int8_product(*quantize_int8(g * _sigmoid(g) * u), *w2)
+
+
+def clip(grads, max_norm):
+    """(norm, clipped gradients) for the global 2-norm; a norm that is not finite leaves them."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        norm = np.sqrt(sum(float((np.asarray(g, np.float64) ** 2).sum()) for g in grads))
+    f = min(1.0, max_norm / (norm + 1e-6)) if np.isfinite(norm) else 1.0
+    return norm, [np.asarray(g, np.float64) * f for g in grads]

@@ -21,6 +21,9 @@ from ._lib import (EXPORTS, MOE_BF16, MOE_ERR_DEVICE_CHECK, MOE_ERR_HIP, MOE_ERR
                    MOE_INT4_G128, MOE_INT4_G32, moe_quantize_weight, moe_pack_quantized,
                    moe_expert_ffn_quantized, moe_add_rmsnorm, moe_add_rmsnorm_backward,
                    moe_add_rmsnorm_backward_workspace_bytes, moe_dispatch,
-                   moe_dispatch_quantized, moe_dispatch_backward, moe_combine_backward)
+                   moe_dispatch_quantized, moe_dispatch_backward, moe_combine_backward,
+                   MOE_INT8, moe_dense_ffn, moe_dense_ffn_workspace_bytes, moe_dense_ffn_backward,
+                   moe_dense_ffn_backward_workspace_bytes, MoeGradients, gradients, moe_grad_norm,
+                   moe_grad_norm_workspace_bytes, moe_clip_grads)
 
 __all__ = [n for n in dir() if not n.startswith("_")]

@@ -14,6 +14,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP
     MOE_ERR_DEVICE_CHECK = range(6)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_E8M0 = 0, 1, 2, 3
 MOE_INT4_G128, MOE_INT4_G32 = 4, 5
+MOE_INT8 = 6
 
 # Every function declared in include/moe.h.
 EXPORTS = ("moe_workspace_bytes", "moe_gate", "moe_permute", "moe_expert_ffn", "moe_combine",
@@ -26,7 +27,9 @@ EXPORTS = ("moe_workspace_bytes", "moe_gate", "moe_permute", "moe_expert_ffn", "
            "moe_quantize_weight", "moe_pack_quantized", "moe_add_rmsnorm",
            "moe_add_rmsnorm_backward", "moe_add_rmsnorm_backward_workspace_bytes",
            "moe_dispatch", "moe_dispatch_quantized", "moe_dispatch_backward",
-           "moe_combine_backward")
+           "moe_combine_backward", "moe_dense_ffn", "moe_dense_ffn_workspace_bytes",
+           "moe_dense_ffn_backward", "moe_dense_ffn_backward_workspace_bytes", "moe_grad_norm",
+           "moe_grad_norm_workspace_bytes", "moe_clip_grads")
 MOE_W13, MOE_W2, MOE_WS13, MOE_WS2 = 0, 1, 2, 3
 
 
@@ -51,6 +54,12 @@ class MoeWeights(ctypes.Structure):
                                                "ws2_scale")] + [("packed", ctypes.c_int32)]
 
 
+class MoeGradients(ctypes.Structure):
+    """A list of gradients (see `gradients`); keeps its tensors and arrays alive."""
+    _fields_ = [("n", ctypes.c_int32), ("grad", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("count", ctypes.c_void_p), ("dtype", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -65,6 +74,7 @@ def lib():
         vp, i64, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
         cfgp = ctypes.POINTER(MoeConfig)
         wp = ctypes.POINTER(MoeWeights)
+        gp = ctypes.POINTER(MoeGradients)
         sig = {
             "moe_workspace_bytes": (sz, [cfgp, i64]),
             "moe_gate": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -100,6 +110,14 @@ def lib():
             "moe_dispatch_quantized": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, vp, vp]),
             "moe_dispatch_backward": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, vp]),
             "moe_combine_backward": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, vp, vp, vp]),
+            "moe_dense_ffn_workspace_bytes": (sz, [cfgp, i64]),
+            "moe_dense_ffn": (ctypes.c_int, [cfgp, i64, vp, wp, vp, vp, vp, sz, vp]),
+            "moe_dense_ffn_backward_workspace_bytes": (sz, [cfgp, i64]),
+            "moe_dense_ffn_backward": (ctypes.c_int, [cfgp, i64, vp, wp, vp, vp, vp, vp, vp, vp, sz,
+                                                      vp]),
+            "moe_grad_norm_workspace_bytes": (sz, [gp]),
+            "moe_grad_norm": (ctypes.c_int, [gp, vp, vp, sz, vp]),
+            "moe_clip_grads": (ctypes.c_int, [gp, ctypes.c_float, vp, ctypes.c_int, vp, sz, vp]),
             "moe_get_device_error": (ctypes.c_int, [vp, sz, vp]),
             "moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
             "moe_last_error": (ctypes.c_char_p, []),
@@ -174,7 +192,7 @@ def _check(status: int):
 
 def config(H, E, G, TG, K, I, Is, rho, act="bf16", wdtype="bf16") -> MoeConfig:
     dt = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3, "fp8e8m0": MOE_FP8_E4M3_E8M0,
-          "int4g128": MOE_INT4_G128, "int4g32": MOE_INT4_G32}
+          "int4g128": MOE_INT4_G128, "int4g32": MOE_INT4_G32, "int8": MOE_INT8}
     return MoeConfig(H, E, G, TG, K, I, Is, float(rho), dt[act], dt[wdtype])
 
 
@@ -295,7 +313,8 @@ def moe_pack_weight(cfg, which, src, dst, stream=None):
 
 
 def moe_quantize_weight(cfg, which, src, codes, scales, stream=None):
-    """4-bit codes and bf16 group scales of a row-major bf16 weight matrix."""
+    """4-bit codes and bf16 group scales, or 8-bit codes and fp32 channel scales, of a row-major
+    bf16 weight matrix."""
     _check(lib().moe_quantize_weight(ctypes.byref(cfg), which, _flat(src), _flat(codes),
                                      _flat(scales), _stream(stream)))
 
@@ -308,7 +327,8 @@ def moe_pack_quantized(cfg, which, codes, scales, dst, stream=None):
 
 def moe_expert_ffn_quantized(cfg, T, xq, xs, perm, offsets, w: MoeWeights, y, y_shared, ws,
                              stream=None):
-    """moe_expert_ffn on token rows already in e4m3 with 1x128 scales."""
+    """moe_expert_ffn on token rows already in e4m3 with 1x128 scales, or in 8-bit integers with
+    one scale a row."""
     _check(lib().moe_expert_ffn_quantized(ctypes.byref(cfg), T, _flat(xq), _flat(xs), _flat(perm),
                                           _flat(offsets), ctypes.byref(w), _flat(y),
                                           _flat(y_shared), _flat(ws),
@@ -357,6 +377,68 @@ def moe_combine_backward(cfg, T, dout, y, pos, topk_w, dy, dtopk_w, stream=None)
     """dy[pos[t, k]] = topk_w[t, k] dout[t], dtopk_w[t, k] = <dout[t], y[pos[t, k]]>."""
     _check(lib().moe_combine_backward(ctypes.byref(cfg), T, _flat(dout), _flat(y), _flat(pos),
                                       _flat(topk_w), _flat(dy), _flat(dtopk_w), _stream(stream)))
+
+
+def moe_dense_ffn_workspace_bytes(cfg: MoeConfig, T: int) -> int:
+    return lib().moe_dense_ffn_workspace_bytes(ctypes.byref(cfg), T)
+
+
+def moe_dense_ffn(cfg, T, x, w: MoeWeights, y, ws, gu=None, stream=None):
+    """y = W2 (silu(W_gate x) * (W_up x)) with ws13 and ws2 of w; gu keeps both projections."""
+    _check(lib().moe_dense_ffn(ctypes.byref(cfg), T, _flat(x), ctypes.byref(w), _flat(gu), _flat(y),
+                               _flat(ws), _nbytes(ws) if ws is not None else 0, _stream(stream)))
+
+
+def moe_dense_ffn_backward_workspace_bytes(cfg: MoeConfig, T: int) -> int:
+    return lib().moe_dense_ffn_backward_workspace_bytes(ctypes.byref(cfg), T)
+
+
+def moe_dense_ffn_backward(cfg, T, x, w: MoeWeights, dy, dx, dws13, dws2, ws, gu=None,
+                           stream=None):
+    """Gradients of x, ws13 and ws2 for dy; gu as the forward wrote it, or None: computed again."""
+    _check(lib().moe_dense_ffn_backward(ctypes.byref(cfg), T, _flat(x), ctypes.byref(w), _flat(gu),
+                                        _flat(dy), _flat(dx), _flat(dws13), _flat(dws2), _flat(ws),
+                                        _nbytes(ws) if ws is not None else 0, _stream(stream)))
+
+
+def gradients(grads, out=None) -> MoeGradients:
+    """The list that moe_grad_norm and moe_clip_grads take, made once for buffers that stay where
+    they are: fp32 or bf16 tensors without gaps, and where the clipped ones go (None: in place)."""
+    import torch
+    types = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError(f"{len(grads)} gradients, {len(out)} outputs")
+    for g, o in zip(grads, out):
+        if g.dtype not in types:
+            raise ValueError(f"gradient of type {g.dtype}, not float32 or bfloat16")
+        if o.dtype != g.dtype or o.numel() != g.numel():
+            raise ValueError(f"output of {o.numel()} {o.dtype} for a gradient of {g.numel()} {g.dtype}")
+    n = len(grads)
+    arrays = ((ctypes.c_void_p * n)(*[_flat(t) for t in grads]),
+              (ctypes.c_void_p * n)(*[_flat(t) for t in out]),
+              (ctypes.c_int64 * n)(*[t.numel() for t in grads]),
+              (ctypes.c_int32 * n)(*[types[t.dtype] for t in grads]))
+    m = MoeGradients(n, *[ctypes.addressof(a) for a in arrays])
+    m.keep = (arrays, grads, out)
+    return m
+
+
+def moe_grad_norm_workspace_bytes(g: MoeGradients) -> int:
+    return lib().moe_grad_norm_workspace_bytes(ctypes.byref(g))
+
+
+def moe_grad_norm(g: MoeGradients, norm, ws, stream=None):
+    """norm [1] = the 2-norm of all gradients together."""
+    _check(lib().moe_grad_norm(ctypes.byref(g), _flat(norm), _flat(ws),
+                               _nbytes(ws) if ws is not None else 0, _stream(stream)))
+
+
+def moe_clip_grads(g: MoeGradients, max_norm, norm, ws=None, norm_given=False, stream=None):
+    """Gradients times min(1, max_norm / (norm + 1e-6)); norm [1] is written first, or read."""
+    _check(lib().moe_clip_grads(ctypes.byref(g), float(max_norm), _flat(norm), int(bool(norm_given)),
+                                _flat(ws), _nbytes(ws) if ws is not None else 0, _stream(stream)))
 
 
 def moe_get_device_error(ws, stream=None) -> int:

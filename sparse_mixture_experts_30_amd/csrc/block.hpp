@@ -1,5 +1,5 @@
 // Host launchers of the operators around the layer: residual add + RMS norm,
-// sorted token rows, and the expert FFNs on 4-bit weights.
+// sorted token rows, and the expert FFNs on integer weights.
 #pragma once
 
 #include "moe_internal.hpp"
@@ -21,6 +21,23 @@ hipError_t launch_quantize_int4(int group, const uint16_t* src, int64_t rows, in
 hipError_t launch_ffn_int4(const FfnDims& d, int group, const uint16_t* x, const int32_t* perm,
                            const int32_t* offsets, const void* w13p, const void* w2p,
                            const void* ws13p, const void* ws2p, uint16_t* h, uint16_t* y,
+                           uint16_t* ys, hipStream_t s);
+
+// Expert FFNs in 8-bit integers (ffn_int8.hip): per-row activation scales,
+// per-channel weight scales.  h (fp32), hq and hs hold N routed rows, then the
+// shared expert's T.  Rows are quantised a workgroup each, for at most
+// quantize_rows_int8_max rows.
+size_t packed_int8_bytes(bool gate_up, int64_t experts, int n, int kd);
+hipError_t launch_pack_int8(bool gate_up, const int8_t* codes, void* dst, int64_t experts, int n,
+                            int kd, hipStream_t s);
+constexpr int64_t quantize_rows_int8_max() { return kMaxGridThreads / 256; }
+hipError_t launch_quantize_rows_int8(const void* x, bool bf16, int64_t rows, int cols, int8_t* q,
+                                     float* scale, hipStream_t s);
+hipError_t launch_ffn_int8(const FfnDims& d, const int8_t* xq, const float* xs,
+                           const int32_t* perm, const int32_t* offsets, const void* w13p,
+                           const float* w13s, const void* w2p, const float* w2s,
+                           const void* ws13p, const float* ws13s, const void* ws2p,
+                           const float* ws2s, float* h, int8_t* hq, float* hs, uint16_t* y,
                            uint16_t* ys, hipStream_t s);
 
 // Residual add + RMS norm and its backward (norm.hip).  The forward has a

@@ -1,0 +1,368 @@
+// Expert FFNs in 8-bit integers (gfx950), for serving: activations with one
+// scale per token row, weights with one scale per output channel,
+//   q[t][k] = round(127 x[t][k] / max_k |x[t][k]|),  s[t] = max / 127,
+//   y[t][n] = s[t] c[n] sum_k q[t][k] w[n][k],
+// the sums in 32-bit integers over the whole k (exact: |sum| <= 127^2 k, so k
+// up to 131072).  h = silu(g) u is kept in fp32 between the two products and
+// quantised per row like x: rounding it to bf16 first would move a tenth of
+// its codes by a step (five times the error of the bf16 outputs).
+//
+// Layout (pack_int8): per output tile (64 h columns of gate and up together,
+// or 128 output rows of the down projection) and 128-k step one block of 16
+// KiB: eight fragments of 16 rows, each two 1 KiB halves of 64 k, lane l of a
+// half holding row l % 16, k = 64 half + 16 (l / 16) + 0..15.  Fragments 0, 1
+// and 4, 5 of a gate/up tile are gate rows of its first and second 32 columns,
+// 2, 3 and 6, 7 the up rows of the same.
+#include "block.hpp"
+#include "items_device.hpp"
+#include "rows_device.hpp"
+
+#include <algorithm>
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads8 = 256;
+constexpr int kStepK = 128;          // k per packed step
+constexpr int kFrags = 8;            // 16-row fragments per tile
+constexpr int kUnits = kFrags * 128; // 16-byte units of a step block
+
+struct Int8Args : ItemArgs {
+  const int8_t* a_r;            // rows of codes, row length kdim
+  const int8_t* a_s;
+  const float* as_r;            // row scales
+  const float* as_s;
+  const int32_t* perm;          // gate/up: routed A row = perm[j] / K
+  int kdim_r, kdim_s;
+  const u32x4* b_r;             // packed routed weights
+  int nt_r;                     // output tiles per routed expert
+  const u32x4* b_s;
+  int nt_s;
+  const float* bs_r;            // channel scales [E][channels]
+  const float* bs_s;
+  int ncol_r, ncol_s;           // h columns (gate/up) or output columns
+  void* c_r;                    // fp32 h or bf16 y, row length ncol
+  void* c_s;
+};
+
+__device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                               __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+
+// ---------------------------------------------------------------- few rows
+// A tile of at most 16 rows and one packed output tile; the four waves take a
+// quarter of the k steps each, their integer sums are joined through LDS.
+constexpr int kFewRows = 16;
+constexpr int kFewWaves = 4;
+
+template <bool kGateUp, bool kStream>
+__device__ __forceinline__ void int8_few_tile(const Int8Args& p, int* lds, const Item& it) {
+  const bool sh = it.g == p.E;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lr = lane & 15, lq = lane >> 4;
+  const int kdim = sh ? p.kdim_s : p.kdim_r, nsteps = kdim / kStepK;
+  const int s0 = nsteps * wave / kFewWaves, s1 = nsteps * (wave + 1) / kFewWaves;
+  const u32x4* bw = (sh ? p.b_s : p.b_r + (int64_t)it.g * p.nt_r * nsteps * kUnits) +
+                    (int64_t)it.ntile * nsteps * kUnits + lane;
+  u32x4 rb[kFrags][2], ra[2];
+  auto load_w = [&](int step) {
+    const u32x4* src = bw + (int64_t)step * kUnits;
+#pragma unroll
+    for (int b = 0; b < kFrags; ++b)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const u32x4* q = src + (b * 2 + f) * 64;
+        rb[b][f] = kStream ? __builtin_nontemporal_load(q) : *q;
+      }
+  };
+  if (s0 < s1) load_w(s0);
+  // This lane's row (past the end the first one; those results are not stored).
+  const int rr = lr < it.nrows ? lr : 0;
+  const int arow = (!sh && kGateUp) ? p.perm[it.row0 + rr] / p.K : it.row0 + rr;
+  const int8_t* ap = (sh ? p.a_s : p.a_r) + (int64_t)arow * kdim + lq * 16;
+  auto load_a = [&](int step) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      ra[f] = *reinterpret_cast<const u32x4*>(ap + step * kStepK + f * 64);
+  };
+  if (s0 < s1) load_a(s0);
+  i32x4 acc[kFrags];
+#pragma unroll
+  for (int b = 0; b < kFrags; ++b) acc[b] = (i32x4){0, 0, 0, 0};
+  auto compute = [&]() {
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int b = 0; b < kFrags; ++b) acc[b] = mfma_i8(ra[f], rb[b][f], acc[b]);
+  };
+  int s = s0;
+  for (; s + 1 < s1; ++s) {
+    compute();
+    load_w(s + 1);
+    load_a(s + 1);
+  }
+  if (s < s1) compute();
+
+  // [wave][frag][row 16][col 16]
+#pragma unroll
+  for (int b = 0; b < kFrags; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      lds[((wave * kFrags + b) * 16 + 4 * lq + i) * 16 + lr] = acc[b][i];
+  __syncthreads();
+  const int row = tid >> 4;   // 16 threads a row
+  if (row >= it.nrows) return;
+  const int64_t crow = it.row0 + row;
+  const int64_t srow = (!sh && kGateUp) ? p.perm[crow] / p.K : crow;
+  const float as = (sh ? p.as_s : p.as_r)[srow];
+  const int ncol = sh ? p.ncol_s : p.ncol_r;
+  const float* bs = sh ? p.bs_s : p.bs_r + (int64_t)it.g * (kGateUp ? 2 : 1) * ncol;
+  // Four neighbouring sums of fragment b from column col, scaled.
+  auto joined = [&](int b, int col, const float* scale) {
+    i32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w)
+      v += *reinterpret_cast<const i32x4*>(lds + ((w * kFrags + b) * 16 + row) * 16 + col);
+    const f32x4 c = *reinterpret_cast<const f32x4*>(scale);
+    f32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = (float)v[j] * (as * c[j]);
+    return r;
+  };
+  if (kGateUp) {
+    const int col = (tid & 15) * 4, b = (col >> 5) * 4 + (col >> 4 & 1), n = it.ntile * 64 + col;
+    const f32x4 gv = joined(b, col & 15, bs + n), uv = joined(b + 2, col & 15, bs + ncol + n);
+    f32x4 h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = swiglu(gv[j], uv[j]);
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(sh ? p.c_s : p.c_r) + crow * ncol + n) = h;
+  } else {
+    const int col = (tid & 15) * 8, b = col >> 4, n = it.ntile * 128 + col;
+    const f32x4 v = joined(b, col & 15, bs + n), w = joined(b, (col & 15) + 4, bs + n + 4);
+    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(sh ? p.c_s : p.c_r) + crow * ncol + n) =
+        (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(w[0], w[1]),
+                pack_bf16x2(w[2], w[3])};
+  }
+}
+
+template <bool kGateUp>
+__global__ void __launch_bounds__(kThreads8) grouped_gemm_int8_few(Int8Args p) {
+  __shared__ __align__(16) int lds[kFewWaves * kFrags * 256];
+  Item it;
+  if (!find_item<kFewRows>(p, it)) return;
+  if (it.ntile >= (it.g == p.E ? p.nt_s : p.nt_r)) return;
+  // A weight tile that only this row tile reads is not kept in cache.
+  if (it.alone)
+    int8_few_tile<kGateUp, true>(p, lds, it);
+  else
+    int8_few_tile<kGateUp, false>(p, lds, it);
+}
+
+// ---------------------------------------------------------------- quantising
+// Codes and scale of one row of kIn (bf16 or fp32) values: a workgroup a row.
+// 127 x is exact for bf16 and its quotient by the maximum, if not a tie, is
+// at least 2^-9 from one, so the code is that of the exact quotient, ties to
+// even.  A row with a NaN or an infinity gets the scale NaN, a row of zeros
+// codes 0 and the scale 1.  Rows of up to 8192 values stay in registers.
+template <typename IO>
+__global__ void __launch_bounds__(256)
+quantize_rows_int8_kernel(const IO* __restrict__ x, int cols, int8_t* __restrict__ q,
+                          float* __restrict__ scale) {
+  constexpr int kKeep = 4;
+  __shared__ uint32_t red[4];
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const IO* xr = x + row * cols;
+  const int chunks = cols / 8;
+  auto load = [&](int c, float* v) {
+    if constexpr (sizeof(IO) == 2) {
+      const u32x4 p = *reinterpret_cast<const u32x4*>(xr + c * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(p[j] << 16);
+        v[2 * j + 1] = __uint_as_float(p[j] & 0xFFFF0000u);
+      }
+    } else {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(xr + c * 8),
+                  b = *reinterpret_cast<const f32x4*>(xr + c * 8 + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = a[j];
+        v[4 + j] = b[j];
+      }
+    }
+  };
+  float keep[kKeep][8];
+  uint32_t m = 0;   // bits of the largest magnitude: NaN above infinity above the rest
+  auto track = [&](const float* v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (tid + i * 256 < chunks) {
+      load(tid + i * 256, keep[i]);
+      track(keep[i]);
+    }
+  for (int c = tid + kKeep * 256; c < chunks; c += 256) {
+    float v[8];
+    load(c, v);
+    track(v);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+  if ((tid & 63) == 0) red[tid >> 6] = m;
+  __syncthreads();
+  m = max(max(red[0], red[1]), max(red[2], red[3]));
+  const bool bad = m >= 0x7F800000u;
+  const float a = __uint_as_float(m);
+  // 127 x must stay finite
+  const float lift = a > 0x1p120f ? 0x1p-16f : 1.0f, d = a * lift;
+  auto store = [&](int c, const float* v) {
+    uint32_t w[2] = {0, 0};
+    if (!bad && m != 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float r = __builtin_rintf(v[j] * lift * 127.0f / d);
+        w[j >> 2] |= ((uint32_t)(int)fminf(fmaxf(r, -127.0f), 127.0f) & 0xFFu) << (8 * (j & 3));
+      }
+    }
+    *reinterpret_cast<uint2*>(q + row * cols + c * 8) = make_uint2(w[0], w[1]);
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (tid + i * 256 < chunks) store(tid + i * 256, keep[i]);
+  for (int c = tid + kKeep * 256; c < chunks; c += 256) {
+    float v[8];
+    load(c, v);
+    store(c, v);
+  }
+  if (tid == 0) scale[row] = bad ? __uint_as_float(0x7FC00000u) : m == 0 ? 1.0f : a / 127.0f;
+}
+
+// One thread per 16-byte piece of the packed matrix.
+__global__ void __launch_bounds__(256)
+pack_int8_kernel(bool gate_up, const int8_t* __restrict__ codes, u32x4* __restrict__ dst,
+                 int64_t units, int n, int kd, int nt) {
+  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (u >= units) return;
+  const int nsteps = kd / kStepK;
+  const int lane = (int)(u & 63), f = (int)(u >> 6 & 1), b = (int)(u >> 7 & 7);
+  const int64_t blk = u / kUnits;
+  const int step = (int)(blk % nsteps);
+  const int64_t et = blk / nsteps;
+  const int tile = (int)(et % nt);
+  const int64_t e = et / nt, rows = gate_up ? 2 * (int64_t)n : n;
+  const int r = lane & 15;
+  const int64_t row = gate_up ? (b & 2 ? n : 0) + (int64_t)tile * 64 + (b >> 2) * 32 + (b & 1) * 16 + r
+                              : (int64_t)tile * 128 + b * 16 + r;
+  dst[u] = *reinterpret_cast<const u32x4*>(codes + (e * rows + row) * kd + step * kStepK + f * 64 +
+                                           16 * (lane >> 4));
+}
+
+// nt: packed tiles of the group with the most of them.
+template <bool kGateUp>
+hipError_t launch_gemm(Int8Args a, int64_t mtiles, int nt, hipStream_t s) {
+  a.ntn = nt;
+  const int64_t work = mtiles * a.ntn;
+  if (work > kMaxGridThreads / kThreads8 - kXcdGrid) return hipErrorInvalidValue;
+  MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int8_few<true>" : "grouped_gemm_int8_few<false>",
+    hipLaunchKernelGGL((grouped_gemm_int8_few<kGateUp>), dim3(xcd_grid(work)), dim3(kThreads8), 0,
+                       s, a));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t packed_int8_bytes(bool gate_up, int64_t experts, int n, int kd) {
+  const int64_t nt = gate_up ? n / 64 : n / 128;
+  return (size_t)(experts * nt * (kd / kStepK) * kUnits) * sizeof(u32x4);
+}
+
+hipError_t launch_pack_int8(bool gate_up, const int8_t* codes, void* dst, int64_t experts, int n,
+                            int kd, hipStream_t s) {
+  const int64_t units = (int64_t)(packed_int8_bytes(gate_up, experts, n, kd) / sizeof(u32x4));
+  MOE_TIMED_LAUNCH(s, "pack_int8_kernel",
+    hipLaunchKernelGGL(pack_int8_kernel, dim3((unsigned)((units + 255) / 256)), dim3(256), 0, s,
+                       gate_up, codes, (u32x4*)dst, units, n, kd, gate_up ? n / 64 : n / 128));
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_rows_int8(const void* x, bool bf16, int64_t rows, int cols, int8_t* q,
+                                     float* scale, hipStream_t s) {
+  if (rows > quantize_rows_int8_max()) return hipErrorInvalidValue;
+  MOE_TIMED_LAUNCH(s, "quantize_rows_int8_kernel",
+    if (bf16)
+      hipLaunchKernelGGL(quantize_rows_int8_kernel<uint16_t>, dim3((unsigned)rows), dim3(256), 0, s,
+                         (const uint16_t*)x, cols, q, scale);
+    else
+      hipLaunchKernelGGL(quantize_rows_int8_kernel<float>, dim3((unsigned)rows), dim3(256), 0, s,
+                         (const float*)x, cols, q, scale));
+  return hipGetLastError();
+}
+
+hipError_t launch_ffn_int8(const FfnDims& d, const int8_t* xq, const float* xs,
+                           const int32_t* perm, const int32_t* offsets, const void* w13p,
+                           const float* w13s, const void* w2p, const float* w2s,
+                           const void* ws13p, const float* ws13s, const void* ws2p,
+                           const float* ws2s, float* h, int8_t* hq, float* hs, uint16_t* y,
+                           uint16_t* ys, hipStream_t s) {
+  const int64_t mt = ffn_grid_mtiles(d, kFewRows);
+  const bool routed = d.groups & kGroupRouted, shared = (d.groups & kGroupShared) && d.Is > 0;
+  Int8Args a{};
+  a.offsets = offsets;
+  a.routed = routed;
+  a.per = (d.E + kWave - 1) / kWave;
+  a.shared_rows = shared ? (int)d.T : 0;
+  a.E = d.E;
+  a.K = d.K;
+  a.a_r = a.a_s = xq;
+  a.as_r = a.as_s = xs;
+  a.perm = perm;
+  a.kdim_r = a.kdim_s = d.H;
+  a.b_r = (const u32x4*)w13p;
+  a.b_s = (const u32x4*)ws13p;
+  a.nt_r = d.I / 64;
+  a.nt_s = d.Is / 64;
+  a.bs_r = w13s;
+  a.bs_s = ws13s;
+  a.ncol_r = d.I;
+  a.ncol_s = d.Is;
+  a.c_r = h;
+  a.c_s = h + d.N * d.I;
+  hipError_t e = launch_gemm<true>(a, mt, std::max(a.nt_r, a.nt_s), s);
+  if (e != hipSuccess) return e;
+
+  int8_t* hq_s = hq + d.N * d.I;
+  float* hs_s = hs + d.N;
+  if (routed && d.N) {
+    e = launch_quantize_rows_int8(h, false, d.N, d.I, hq, hs, s);
+    if (e != hipSuccess) return e;
+  }
+  if (shared) {
+    e = launch_quantize_rows_int8(h + d.N * d.I, false, d.T, d.Is, hq_s, hs_s, s);
+    if (e != hipSuccess) return e;
+  }
+
+  a.nt_r = a.nt_s = d.H / 128;
+  a.a_r = hq;
+  a.a_s = hq_s;
+  a.as_r = hs;
+  a.as_s = hs_s;
+  a.kdim_r = d.I;
+  a.kdim_s = d.Is;
+  a.b_r = (const u32x4*)w2p;
+  a.b_s = (const u32x4*)ws2p;
+  a.bs_r = w2s;
+  a.bs_s = ws2s;
+  a.ncol_r = a.ncol_s = d.H;
+  a.c_r = y;
+  a.c_s = ys;
+  return launch_gemm<false>(a, mt, a.nt_r, s);
+}
+
+}  // namespace moe

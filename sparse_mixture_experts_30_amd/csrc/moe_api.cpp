@@ -8,11 +8,15 @@
 #include <string.h>
 
 #include <algorithm>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "moe_internal.hpp"
 #include "backward.hpp"
 #include "block.hpp"
+#include "dense.hpp"
+#include "grads.hpp"
 
 namespace {
 
@@ -40,7 +44,14 @@ bool is_fp8(moe_dtype w) { return w == MOE_FP8_E4M3 || w == MOE_FP8_E4M3_E8M0; }
 bool is_int4(moe_dtype w) { return w == MOE_INT4_G128 || w == MOE_INT4_G32; }
 int int4_group(moe_dtype w) { return w == MOE_INT4_G32 ? 32 : 128; }
 
-// Configurations of the expert and layer backward: 4-bit weights are for
+// 8-bit integer weights with an fp32 scale per output channel.
+bool is_int8(moe_dtype w) { return w == MOE_INT8; }
+constexpr int kInt8MaxK = 131072;   // 127^2 k stays below 2^31
+
+// Weight types whose kernels read tokens quantised beforehand.
+bool quantises_act(moe_dtype w) { return is_fp8(w) || is_int8(w); }
+
+// Configurations of the expert and layer backward: integer weights are for
 // serving and have none.
 bool has_backward(const moe_config* c) {
   return c->act_dtype == MOE_BF16 && (c->weight_dtype == MOE_BF16 || is_fp8(c->weight_dtype));
@@ -67,7 +78,7 @@ moe_status check_cfg(const moe_config* c) {
   const moe_dtype a = c->act_dtype, w = c->weight_dtype;
   if (a != MOE_F32 && a != MOE_BF16)
     return fail(MOE_ERR_INVALID_ARG, "act_dtype must be MOE_F32 or MOE_BF16");
-  if (w != MOE_F32 && w != MOE_BF16 && !is_fp8(w) && !is_int4(w))
+  if (w != MOE_F32 && w != MOE_BF16 && !is_fp8(w) && !is_int4(w) && !is_int8(w))
     return fail(MOE_ERR_INVALID_ARG, "unknown weight_dtype");
   // Valid for the method, not handled by these kernels:
   if (E > 512) return fail(MOE_ERR_UNSUPPORTED, "n_routed_experts > 512");
@@ -75,9 +86,11 @@ moe_status check_cfg(const moe_config* c) {
   if (K > 64) return fail(MOE_ERR_UNSUPPORTED, "num_experts_per_tok > 64");
   if ((a == MOE_F32) != (w == MOE_F32))
     return fail(MOE_ERR_UNSUPPORTED, "fp32 activations need fp32 weights and vice versa");
-  const int mult = is_fp8(w) || is_int4(w) ? 128 : 64;
+  const int mult = is_fp8(w) || is_int4(w) || is_int8(w) ? 128 : 64;
   if (H % mult || I % mult || Is % mult)
     return fail(MOE_ERR_UNSUPPORTED, "hidden and FFN sizes must be multiples of %d", mult);
+  if (is_int8(w) && (H > kInt8MaxK || I > kInt8MaxK || Is > kInt8MaxK))
+    return fail(MOE_ERR_UNSUPPORTED, "8-bit integer products take sizes up to %d", kInt8MaxK);
   return MOE_OK;
 }
 
@@ -85,6 +98,9 @@ moe_status check_T(int64_t T, const moe_config* c) {
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T < 0");
   if (T * (int64_t)c->num_experts_per_tok > 0x7fffffffLL || T > 0x7fffffffLL)
     return fail(MOE_ERR_UNSUPPORTED, "T * top_k exceeds int32 indexing");
+  if (is_int8(c->weight_dtype) && T * c->num_experts_per_tok > moe::quantize_rows_int8_max())
+    return fail(MOE_ERR_UNSUPPORTED, "T * top_k: one launch quantises %lld rows",
+                (long long)moe::quantize_rows_int8_max());
   return MOE_OK;
 }
 
@@ -92,18 +108,40 @@ size_t act_bytes(const moe_config* c) { return c->act_dtype == MOE_BF16 ? 2 : 4;
 
 // Workspace segments (byte offsets, 256-aligned).
 struct Layout {
-  size_t err, part, gsplit, idx, w, counts, offsets, perm, pos, hist, tiles, tiles2, h, hs, xq,
-      xs, y, ys, flags, total;
+  size_t err, part, gsplit, idx, w, counts, offsets, perm, pos, hist, tiles, tiles2, h, hq, hs,
+      xq, xs, y, ys, flags, total;
   int ksplit;
   bool decode;   // decode routing (gate, selection, permutation, tile list in three launches)
 };
+
+// The segments of the expert products themselves: h of N routed and T shared
+// rows, its codes and scales, the tokens' codes and scales.
+template <class Take>
+void ffn_segments(Layout& L, const moe_config* c, int64_t N, int64_t T, Take take) {
+  const int64_t H = c->hidden_size, I = c->moe_intermediate_size, Is = c->shared_intermediate_size;
+  const size_t hel = (size_t)(N * I + T * Is);
+  L.hq = L.hs = L.xq = L.xs = 0;
+  if (is_fp8(c->weight_dtype)) {
+    L.h = take(hel);
+    L.hs = take(hel / 128 * 4);
+    L.xq = take((size_t)T * H);
+    L.xs = take((size_t)T * H / 128 * 4);
+  } else if (is_int8(c->weight_dtype)) {
+    L.h = take(hel * 4);   // fp32
+    L.hq = take(hel);
+    L.hs = take((size_t)(N + T) * 4);
+    L.xq = take((size_t)T * H);
+    L.xs = take((size_t)T * 4);
+  } else {
+    L.h = take(hel * act_bytes(c));
+  }
+}
 
 Layout layout(const moe_config* c, int64_t T) {
   Layout L{};
   const int64_t H = c->hidden_size, E = c->n_routed_experts, K = c->num_experts_per_tok,
                 I = c->moe_intermediate_size, Is = c->shared_intermediate_size;
   const int64_t N = T * K;
-  const bool fp8 = is_fp8(c->weight_dtype);
   L.ksplit = c->act_dtype == MOE_BF16 ? moe::gate_ksplit(T, (int)H, (int)E) : 1;
   L.decode = moe::decode_route_ok(T, (int)H, (int)E, (int)K);
   const int64_t nparts = std::max<int64_t>(L.ksplit, L.decode ? moe::decode_ksplit((int)H, (int)E) : 1);
@@ -127,16 +165,7 @@ Layout layout(const moe_config* c, int64_t T) {
   const size_t tiles = moe::ffn_tiles_bytes(d);
   L.tiles = take(tiles);
   L.tiles2 = take(tiles);   // the shared expert's list on a second stream
-  const size_t hel = (size_t)(N * I + T * Is);
-  if (fp8) {
-    L.h = take(hel);
-    L.hs = take(hel / 128 * 4);
-    L.xq = take((size_t)T * H);
-    L.xs = take((size_t)T * H / 128 * 4);
-  } else {
-    L.h = take(hel * act_bytes(c));
-    L.hs = L.xq = L.xs = o;
-  }
+  ffn_segments(L, c, N, T, take);
   L.y = take((size_t)N * H * act_bytes(c));
   L.ys = take((size_t)T * H * act_bytes(c));
   // completion flags of the one-launch decode layer (bf16)
@@ -218,10 +247,24 @@ moe_status run_permute(const moe_config* c, int64_t T, const int32_t* idx, int32
   return MOE_OK;
 }
 
+// Quantises T token rows of x into the workspace, as the weights' kernels read them.
+moe_status quantise_tokens(const moe_config* c, int64_t T, const void* x, void* ws,
+                           const Layout& L, hipStream_t s) {
+  if (is_int8(c->weight_dtype))
+    HIPCALL(moe::launch_quantize_rows_int8(x, true, T, c->hidden_size, at<int8_t>(ws, L.xq),
+                                           at<float>(ws, L.xs), s),
+            "quantise x");
+  else
+    HIPCALL(moe::launch_quant_rows((const uint16_t*)x, T, c->hidden_size, at<uint8_t>(ws, L.xq),
+                                   at<float>(ws, L.xs), c->weight_dtype == MOE_FP8_E4M3_E8M0, s),
+            "quantise x");
+  return MOE_OK;
+}
+
 // groups: which groups to compute (moe::kGroupRouted / kGroupShared);
-// tiles: the tile list to use (built here unless tiles_ready); quantize: fp8
-// weights only, quantise x first (else the workspace's xq / xs already hold
-// it, or given_q / given_s do).
+// tiles: the tile list to use (built here unless tiles_ready); quantize: e4m3
+// and 8-bit integer weights only, quantise x first (else the workspace's xq /
+// xs already hold it, or given_q / given_s do).
 moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t* perm,
                    const int32_t* offsets, const moe_weights* wt, void* y, void* ys, void* ws,
                    const Layout& L, hipStream_t s, int groups = moe::kGroupsAll,
@@ -229,6 +272,7 @@ moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t*
                    const uint8_t* given_q = nullptr, const float* given_s = nullptr) {
   moe::FfnDims d{T, T * c->num_experts_per_tok, c->hidden_size, c->moe_intermediate_size,
                  c->shared_intermediate_size, c->n_routed_experts, c->num_experts_per_tok};
+  if (!(groups & moe::kGroupRouted) && !perm) d.N = 0;   // a dense layer: no routed rows at all
   d.groups = groups;
   d.tiles_ready = tiles_ready;
   if (!tiles) tiles = at<int32_t>(ws, L.tiles);
@@ -263,13 +307,21 @@ moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t*
                                    at<uint16_t>(ws, L.h), (uint16_t*)y, (uint16_t*)ys, s),
               "ffn int4");
       break;
+    case MOE_INT8: {
+      const uint8_t* xq = given_q ? given_q : at<uint8_t>(ws, L.xq);
+      const float* xs = given_q ? given_s : at<float>(ws, L.xs);
+      if (quantize) CHECK(quantise_tokens(c, T, x, ws, L, s));
+      HIPCALL(moe::launch_ffn_int8(d, (const int8_t*)xq, xs, perm, offsets, wt->w13, wt->w13_scale,
+                                   wt->w2, wt->w2_scale, wt->ws13, wt->ws13_scale, wt->ws2,
+                                   wt->ws2_scale, at<float>(ws, L.h), at<int8_t>(ws, L.hq),
+                                   at<float>(ws, L.hs), (uint16_t*)y, (uint16_t*)ys, s),
+              "ffn int8");
+      break;
+    }
     case MOE_FP8_E4M3_E8M0: {
       const uint8_t* xq = given_q ? given_q : at<uint8_t>(ws, L.xq);
       const float* xs = given_q ? given_s : at<float>(ws, L.xs);
-      if (quantize)
-        HIPCALL(moe::launch_quant_rows((const uint16_t*)x, T, c->hidden_size,
-                                       at<uint8_t>(ws, L.xq), at<float>(ws, L.xs), true, s),
-                "quantise x");
+      if (quantize) CHECK(quantise_tokens(c, T, x, ws, L, s));
       HIPCALL(moe::launch_ffn_fp8_mx(d, xq, xs, perm, offsets, wt->w13, wt->w13_scale, wt->w2,
                                      wt->w2_scale, wt->ws13, wt->ws13_scale, wt->ws2,
                                      wt->ws2_scale, at<uint8_t>(ws, L.h), at<float>(ws, L.hs),
@@ -280,10 +332,7 @@ moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t*
     case MOE_FP8_E4M3: {
       const uint8_t* xq = given_q ? given_q : at<uint8_t>(ws, L.xq);
       const float* xs = given_q ? given_s : at<float>(ws, L.xs);
-      if (quantize)
-        HIPCALL(moe::launch_quant_rows((const uint16_t*)x, T, c->hidden_size,
-                                       at<uint8_t>(ws, L.xq), at<float>(ws, L.xs), false, s),
-                "quantise x");
+      if (quantize) CHECK(quantise_tokens(c, T, x, ws, L, s));
       if (wt->packed) {
         HIPCALL(moe::launch_ffn_fp8_packed(d, xq, xs, perm, offsets, wt->w13, wt->w13_scale,
                                            wt->w2, wt->w2_scale, wt->ws13, wt->ws13_scale, wt->ws2,
@@ -305,7 +354,9 @@ moe_status run_ffn(const moe_config* c, int64_t T, const void* x, const int32_t*
   return MOE_OK;
 }
 
-moe_status check_weights(const moe_config* c, const moe_weights* w, bool need_gate) {
+// dense: the shared expert's matrices only.
+moe_status check_weights(const moe_config* c, const moe_weights* w, bool need_gate,
+                         bool dense = false) {
   NONNULL(w);
   if (w->packed != 0 && w->packed != 1)
     return fail(MOE_ERR_INVALID_ARG, "moe_weights.packed must be 0 or 1");
@@ -313,34 +364,50 @@ moe_status check_weights(const moe_config* c, const moe_weights* w, bool need_ga
     return fail(MOE_ERR_UNSUPPORTED, "the packed weight layout is for bf16 and fp8 weights");
   if (!w->packed && is_int4(c->weight_dtype))
     return fail(MOE_ERR_UNSUPPORTED, "4-bit weights must be packed (moe_pack_quantized)");
+  if (!w->packed && is_int8(c->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "8-bit integer weights must be packed (moe_pack_weight)");
   if (need_gate) {
     NONNULL(w->gate_w);
     NONNULL(w->bias);
   }
-  NONNULL(w->w13);
-  NONNULL(w->w2);
-  const bool fp8 = is_fp8(c->weight_dtype);
+  if (!dense) {
+    NONNULL(w->w13);
+    NONNULL(w->w2);
+  }
+  const bool scaled = is_fp8(c->weight_dtype) || is_int8(c->weight_dtype);
   if (c->weight_dtype == MOE_FP8_E4M3_E8M0 && !w->packed)
     return fail(MOE_ERR_UNSUPPORTED, "e4m3 weights with power-of-two scales must be packed "
                 "(moe_pack_weight)");
-  if (fp8) {
+  if (scaled && !dense) {
     NONNULL(w->w13_scale);
     NONNULL(w->w2_scale);
   }
   if (c->shared_intermediate_size > 0) {
     NONNULL(w->ws13);
     NONNULL(w->ws2);
-    if (fp8) {
+    if (scaled) {
       NONNULL(w->ws13_scale);
       NONNULL(w->ws2_scale);
     }
   }
-  if (is_int4(c->weight_dtype)) {
-    ALIGNED16(w->w13);
-    ALIGNED16(w->w2);
+  if (is_int4(c->weight_dtype) || is_int8(c->weight_dtype)) {
+    if (!dense) {
+      ALIGNED16(w->w13);
+      ALIGNED16(w->w2);
+    }
     if (c->shared_intermediate_size > 0) {
       ALIGNED16(w->ws13);
       ALIGNED16(w->ws2);
+    }
+  }
+  if (is_int8(c->weight_dtype)) {   // four channels' scales are read together
+    if (!dense) {
+      ALIGNED16(w->w13_scale);
+      ALIGNED16(w->w2_scale);
+    }
+    if (c->shared_intermediate_size > 0) {
+      ALIGNED16(w->ws13_scale);
+      ALIGNED16(w->ws2_scale);
     }
   }
   return MOE_OK;
@@ -382,7 +449,7 @@ moe_status forward_impl(const moe_config* cfg, int64_t T, const void* x, const m
   NONNULL(x);
   NONNULL(out);
   CHECK(check_weights(cfg, w, true));
-  if (is_int4(cfg->weight_dtype)) ALIGNED16(x);
+  if (is_int4(cfg->weight_dtype) || is_int8(cfg->weight_dtype)) ALIGNED16(x);
   const Layout L = layout(cfg, T);
   CHECK(check_ws(ws, ws_bytes, L));
   if (one_launch &&
@@ -403,18 +470,14 @@ moe_status forward_impl(const moe_config* cfg, int64_t T, const void* x, const m
   void* y = at<void>(ws, L.y);
   const bool sh = cfg->shared_intermediate_size > 0;
   void* ys = sh ? at<void>(ws, L.ys) : nullptr;
-  const bool fp8 = is_fp8(cfg->weight_dtype);
   // The fp32 expert kernels compute every group in one launch.
   const bool split = s2 && sh && cfg->weight_dtype != MOE_F32;
 
   ForkJoin* ev = nullptr;
   if (split) {
     HIPCALL(fork_join_events(&ev), "fork/join events");
-    if (fp8)   // x is quantised once, before the fork, for both streams
-      HIPCALL(moe::launch_quant_rows((const uint16_t*)x, T, cfg->hidden_size, at<uint8_t>(ws, L.xq),
-                                     at<float>(ws, L.xs),
-                                     cfg->weight_dtype == MOE_FP8_E4M3_E8M0, s),
-              "quantise x");
+    if (quantises_act(cfg->weight_dtype))   // once, before the fork, for both streams
+      CHECK(quantise_tokens(cfg, T, x, ws, L, s));
     HIPCALL(hipEventRecord(ev->fork, s), "fork");
     HIPCALL(hipStreamWaitEvent(s2, ev->fork, 0), "fork");
     CHECK(run_ffn(cfg, T, x, pm, offs, w, y, ys, ws, L, s2, moe::kGroupShared,
@@ -500,6 +563,138 @@ moe_status check_matrix_threads(int64_t threads) {
   if (threads > moe::kMaxGridThreads / 256 * 256)
     return fail(MOE_ERR_UNSUPPORTED, "the matrix is too large for one launch (take its experts in "
                 "parts, with fewer n_routed_experts)");
+  return MOE_OK;
+}
+
+// ---- dense layers -----------------------------------------------------------
+// The shared expert's matrices alone.
+moe_status check_dense(const moe_config* c, int64_t T) {
+  CHECK(check_cfg(c));
+  CHECK(check_T(T, c));
+  if (c->shared_intermediate_size <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "a dense layer needs shared_intermediate_size > 0");
+  if (c->weight_dtype == MOE_BF16 &&
+      !moe::dense_fits(T, c->hidden_size, c->shared_intermediate_size))
+    return fail(MOE_ERR_UNSUPPORTED, "T, hidden_size or shared_intermediate_size is too large for "
+                "one launch of the dense layer");
+  return MOE_OK;
+}
+
+// Either form of the weights (row-major, packed) fits.
+Layout dense_layout(const moe_config* c, int64_t T) {
+  Layout L{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    size_t at = o;
+    o += up(bytes);
+    return at;
+  };
+  moe::FfnDims d{T, 0, c->hidden_size, c->moe_intermediate_size, c->shared_intermediate_size,
+                 c->n_routed_experts, c->num_experts_per_tok};
+  L.tiles = take(moe::ffn_tiles_bytes(d));
+  ffn_segments(L, c, 0, T, take);
+  L.total = o;
+  return L;
+}
+
+struct DenseBackwardLayout {
+  size_t gu, da, h, total;
+};
+DenseBackwardLayout dense_backward_layout(const moe_config* c, int64_t T) {
+  const size_t row = up((size_t)T * c->shared_intermediate_size * 2);
+  return {0, 2 * row, 4 * row, 5 * row};
+}
+
+// ---- gradients --------------------------------------------------------------
+struct GradArrays {
+  std::unique_ptr<uint8_t[]> bf16;
+  moe::GradList list(const moe_gradients* g) const {
+    return {g->n, g->grad, g->out, g->count, bf16.get()};
+  }
+};
+
+moe_status check_overlap(const moe_gradients* g) {
+  struct Range {
+    uintptr_t a, b;
+    int i;
+    bool out;
+  };
+  // Outputs that follow one another, on the gradients themselves or all behind
+  // or before them, as the pieces of flat buffers do, need no sorting.
+  uintptr_t end = 0, lo = UINTPTR_MAX, hi = 0, olo = UINTPTR_MAX;
+  bool ordered = true, same = true;
+  for (int i = 0; i < g->n; ++i) {
+    if (!g->count[i]) continue;
+    const uintptr_t bytes = g->count[i] * (g->dtype[i] == MOE_BF16 ? 2 : 4);
+    const uintptr_t in = (uintptr_t)g->grad[i], out = (uintptr_t)g->out[i];
+    ordered = ordered && out >= end;
+    same = same && in == out;
+    end = out + bytes;
+    lo = std::min(lo, in);
+    hi = std::max(hi, in + bytes);
+    olo = std::min(olo, out);
+  }
+  if (ordered && (same || end <= lo || olo >= hi)) return MOE_OK;
+  const std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * (size_t)g->n]);
+  if (!r) return fail(MOE_ERR_INVALID_ARG, "n = %d: no host memory", g->n);
+  size_t m = 0;
+  for (int i = 0; i < g->n; ++i) {
+    if (!g->count[i]) continue;
+    const uintptr_t bytes = g->count[i] * (g->dtype[i] == MOE_BF16 ? 2 : 4);
+    const uintptr_t in = (uintptr_t)g->grad[i], out = (uintptr_t)g->out[i];
+    r[m++] = {out, out + bytes, i, true};
+    if (in != out) r[m++] = {in, in + bytes, i, false};
+  }
+  std::sort(r.get(), r.get() + m, [](const Range& x, const Range& y) { return x.a < y.a; });
+  // Ends of the ranges so far: of the outputs, and of all.
+  uintptr_t out_end = 0, all_end = 0;
+  int out_i = 0, all_i = 0;
+  for (size_t k = 0; k < m; ++k) {
+    const bool bad = r[k].out ? r[k].a < all_end : r[k].a < out_end;
+    if (bad)
+      return fail(MOE_ERR_INVALID_ARG, "output of gradient %d overlaps gradient or output %d",
+                  r[k].out ? r[k].i : out_i, r[k].out ? all_i : r[k].i);
+    if (r[k].out && r[k].b > out_end) out_end = r[k].b, out_i = r[k].i;
+    if (r[k].b > all_end) all_end = r[k].b, all_i = r[k].i;
+  }
+  return MOE_OK;
+}
+
+// With `writes`, no output may overlap another gradient or output; a gradient
+// may be its own output.
+moe_status check_gradients(const moe_gradients* g, bool writes, GradArrays* a) {
+  NONNULL(g);
+  if (g->n < 0) return fail(MOE_ERR_INVALID_ARG, "n < 0");
+  if (g->n == 0) return MOE_OK;
+  NONNULL(g->grad);
+  NONNULL(g->count);
+  NONNULL(g->dtype);
+  if (writes) NONNULL(g->out);
+  a->bf16.reset(new (std::nothrow) uint8_t[g->n]);
+  if (!a->bf16) return fail(MOE_ERR_INVALID_ARG, "n = %d: no host memory", g->n);
+  double bytes = 0;
+  for (int i = 0; i < g->n; ++i) {
+    const int32_t t = g->dtype[i];
+    if (t != MOE_F32 && t != MOE_BF16)
+      return fail(MOE_ERR_UNSUPPORTED, "gradient %d: dtype must be MOE_F32 or MOE_BF16", i);
+    const int size = t == MOE_BF16 ? 2 : 4;
+    a->bf16[i] = t == MOE_BF16;
+    if (g->count[i] < 0) return fail(MOE_ERR_INVALID_ARG, "gradient %d: count < 0", i);
+    if (g->count[i] == 0) continue;
+    bytes += (double)g->count[i] * size;
+    if (!g->grad[i] || (writes && !g->out[i]))
+      return fail(MOE_ERR_INVALID_ARG, "gradient %d is NULL", i);
+    if ((uintptr_t)g->grad[i] % size || (writes && (uintptr_t)g->out[i] % size))
+      return fail(MOE_ERR_INVALID_ARG, "gradient %d is not aligned to its type", i);
+  }
+  if (bytes > 4e12) return fail(MOE_ERR_UNSUPPORTED, "more than 4e12 bytes of gradients");
+  return writes ? check_overlap(g) : MOE_OK;
+}
+
+moe_status check_grad_ws(const moe_gradients* g, void* ws, size_t ws_bytes) {
+  const size_t need = moe::grad_norm_ws_bytes(g->n);
+  if (g->n && (!ws || ws_bytes < need || ((uintptr_t)ws & 255)))
+    return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
   return MOE_OK;
 }
 
@@ -592,7 +787,7 @@ moe_status moe_expert_ffn(const moe_config* cfg, int64_t T, const void* x, const
   NONNULL(y);
   CHECK(check_weights(cfg, w, false));
   if (cfg->shared_intermediate_size > 0) NONNULL(y_shared);
-  if (is_int4(cfg->weight_dtype)) {
+  if (is_int4(cfg->weight_dtype) || is_int8(cfg->weight_dtype)) {
     ALIGNED16(x);
     ALIGNED16(y);
     if (cfg->shared_intermediate_size > 0) ALIGNED16(y_shared);
@@ -834,8 +1029,8 @@ moe_status moe_expert_ffn_quantized(const moe_config* cfg, int64_t T, const uint
                                     size_t ws_bytes, void* stream) {
   CHECK(check_cfg(cfg));
   CHECK(check_T(T, cfg));
-  if (!is_fp8(cfg->weight_dtype))
-    return fail(MOE_ERR_UNSUPPORTED, "e4m3 activation rows need e4m3 weights");
+  if (!quantises_act(cfg->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "quantised rows need e4m3 or 8-bit integer weights");
   if (T == 0) return MOE_OK;
   NONNULL(xq);
   NONNULL(xs);
@@ -845,6 +1040,10 @@ moe_status moe_expert_ffn_quantized(const moe_config* cfg, int64_t T, const uint
   NONNULL(y);
   CHECK(check_weights(cfg, w, false));
   if (cfg->shared_intermediate_size > 0) NONNULL(y_shared);
+  if (is_int8(cfg->weight_dtype)) {
+    ALIGNED16(y);
+    if (cfg->shared_intermediate_size > 0) ALIGNED16(y_shared);
+  }
   const Layout L = layout(cfg, T);
   CHECK(check_ws(ws, ws_bytes, L));
   return run_ffn(cfg, T, nullptr, perm, offsets, w, y,
@@ -859,6 +1058,8 @@ moe_status moe_add_rmsnorm(const moe_config* cfg, int64_t rows, const void* x,
   if (!yq != !ys) return fail(MOE_ERR_INVALID_ARG, "yq and ys go together");
   if (yq && cfg->act_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "the e4m3 output takes bf16 activations");
+  if (yq && is_int8(cfg->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "the norm writes no 8-bit integer rows (moe_quantize_act)");
   if (yq && cfg->hidden_size % 128) return fail(MOE_ERR_UNSUPPORTED, "hidden_size %% 128 != 0");
   const int64_t most = moe::add_rmsnorm_max_rows(cfg->hidden_size, cfg->act_dtype == MOE_BF16);
   if (rows > most)
@@ -937,6 +1138,8 @@ moe_status moe_dispatch_quantized(const moe_config* cfg, int64_t T, const uint8_
   CHECK(check_tokens(cfg, T, cfg->hidden_size));
   if (cfg->act_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "e4m3 rows belong to bf16 activations");
+  if (is_int8(cfg->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED, "rows of e4m3 codes with 1x128 scales, not of 8-bit integers");
   if (cfg->hidden_size % 128) return fail(MOE_ERR_UNSUPPORTED, "hidden_size %% 128 != 0");
   if (T == 0) return MOE_OK;
   NONNULL(xq);
@@ -992,6 +1195,124 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
   return MOE_OK;
 }
 
+size_t moe_dense_ffn_workspace_bytes(const moe_config* cfg, int64_t T) {
+  if (check_dense(cfg, T) != MOE_OK) return 0;
+  return dense_layout(cfg, T).total;
+}
+
+moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w,
+                         void* gu, void* y, void* ws, size_t ws_bytes, void* stream) {
+  CHECK(check_dense(cfg, T));
+  NONNULL(w);
+  const bool rowmajor = cfg->weight_dtype == MOE_BF16 && !w->packed;
+  if (gu && !rowmajor)
+    return fail(MOE_ERR_UNSUPPORTED, "gu is kept by row-major bf16 weights only");
+  if (T == 0) return MOE_OK;
+  NONNULL(x);
+  NONNULL(y);
+  CHECK(check_weights(cfg, w, false, true));
+  ALIGNED16(x);
+  ALIGNED16(y);
+  ALIGNED16(gu);
+  const Layout L = dense_layout(cfg, T);
+  CHECK(check_ws(ws, ws_bytes, L));
+  const hipStream_t s = (hipStream_t)stream;
+  if (!rowmajor)
+    return run_ffn(cfg, T, x, nullptr, nullptr, w, nullptr, y, ws, L, s, moe::kGroupShared);
+  ALIGNED16(w->ws13);
+  ALIGNED16(w->ws2);
+  const int H = cfg->hidden_size, I = cfg->shared_intermediate_size;
+  uint16_t* h = at<uint16_t>(ws, L.h);
+  HIPCALL(moe::launch_dense_gate_up((const uint16_t*)x, (const uint16_t*)w->ws13, T, H, I,
+                                    (uint16_t*)gu, h, s),
+          "dense gate/up");
+  HIPCALL(moe::launch_dense_down(h, (const uint16_t*)w->ws2, T, H, I, (uint16_t*)y, s),
+          "dense down");
+  return MOE_OK;
+}
+
+size_t moe_dense_ffn_backward_workspace_bytes(const moe_config* cfg, int64_t T) {
+  if (check_dense(cfg, T) != MOE_OK || cfg->weight_dtype != MOE_BF16) return 0;
+  return dense_backward_layout(cfg, T).total;
+}
+
+moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* x,
+                                  const moe_weights* w, const void* gu, const void* dy, void* dx,
+                                  void* dws13, void* dws2, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  CHECK(check_dense(cfg, T));
+  if (cfg->weight_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "the dense backward takes bf16 weights");
+  NONNULL(w);
+  if (w->packed)
+    return fail(MOE_ERR_UNSUPPORTED, "the dense backward reads row-major weights (packed = 0)");
+  NONNULL(dws13);
+  NONNULL(dws2);
+  const int H = cfg->hidden_size, I = cfg->shared_intermediate_size;
+  const DenseBackwardLayout L = dense_backward_layout(cfg, T);
+  if (T) {
+    NONNULL(x);
+    NONNULL(dy);
+    NONNULL(w->ws13);
+    NONNULL(w->ws2);
+    if (!ws || ws_bytes < L.total || ((uintptr_t)ws & 255))
+      return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes",
+                  L.total);
+  }
+  ALIGNED16(x);
+  ALIGNED16(w->ws13);
+  ALIGNED16(w->ws2);
+  ALIGNED16(gu);
+  ALIGNED16(dy);
+  ALIGNED16(dx);
+  ALIGNED16(dws13);
+  ALIGNED16(dws2);
+  const hipStream_t s = (hipStream_t)stream;
+  const uint16_t* g = (const uint16_t*)gu;
+  if (T && !g) {   // computed again
+    HIPCALL(moe::launch_dense_gate_up((const uint16_t*)x, (const uint16_t*)w->ws13, T, H, I,
+                                      at<uint16_t>(ws, L.gu), nullptr, s),
+            "dense gate/up");
+    g = at<uint16_t>(ws, L.gu);
+  }
+  HIPCALL(moe::launch_dense_backward((const uint16_t*)x, (const uint16_t*)w->ws13,
+                                     (const uint16_t*)w->ws2, g, (const uint16_t*)dy, T, H, I,
+                                     at<uint16_t>(ws, L.da), at<uint16_t>(ws, L.h), (uint16_t*)dx,
+                                     (uint16_t*)dws13, (uint16_t*)dws2, s),
+          "dense backward");
+  return MOE_OK;
+}
+
+size_t moe_grad_norm_workspace_bytes(const moe_gradients* g) {
+  if (!g || g->n < 0) return 0;
+  return std::max<size_t>(moe::grad_norm_ws_bytes(g->n), kAlign);
+}
+
+moe_status moe_grad_norm(const moe_gradients* g, float* norm, void* ws, size_t ws_bytes,
+                         void* stream) {
+  GradArrays a;
+  CHECK(check_gradients(g, false, &a));
+  NONNULL(norm);
+  CHECK(check_grad_ws(g, ws, ws_bytes));
+  HIPCALL(moe::launch_grad_norm(a.list(g), (double*)ws, norm, (hipStream_t)stream),
+          "gradient norm");
+  return MOE_OK;
+}
+
+moe_status moe_clip_grads(const moe_gradients* g, float max_norm, float* norm, int norm_given,
+                          void* ws, size_t ws_bytes, void* stream) {
+  GradArrays a;
+  CHECK(check_gradients(g, true, &a));
+  if (!(max_norm >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must be >= 0");
+  NONNULL(norm);
+  if (!norm_given) CHECK(check_grad_ws(g, ws, ws_bytes));
+  const hipStream_t s = (hipStream_t)stream;
+  const moe::GradList l = a.list(g);
+  if (!norm_given) HIPCALL(moe::launch_grad_norm(l, (double*)ws, norm, s), "gradient norm");
+  HIPCALL(moe::launch_grad_scale(l, norm, max_norm, s), "gradient clipping");
+  return MOE_OK;
+}
+
 moe_status moe_bias_update(const moe_config* cfg, const int32_t* counts, float gamma,
                            float* bias, void* stream) {
   CHECK(check_cfg(cfg));
@@ -1011,11 +1332,22 @@ moe_status moe_quantize_act(const moe_config* cfg, int64_t rows, const void* x, 
   if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows < 0");
   if (rows == 0) return MOE_OK;
   if (cfg->act_dtype != MOE_BF16)
-    return fail(MOE_ERR_UNSUPPORTED, "the fp8 quantiser takes bf16 activations");
+    return fail(MOE_ERR_UNSUPPORTED, "the quantiser takes bf16 activations");
   if (cfg->hidden_size % 128) return fail(MOE_ERR_UNSUPPORTED, "hidden_size %% 128 != 0");
+  if (is_int8(cfg->weight_dtype) && rows > moe::quantize_rows_int8_max())
+    return fail(MOE_ERR_UNSUPPORTED, "%lld rows: one launch takes %lld", (long long)rows,
+                (long long)moe::quantize_rows_int8_max());
   NONNULL(x);
   NONNULL(xq);
   NONNULL(xs);
+  if (is_int8(cfg->weight_dtype)) {
+    ALIGNED16(x);
+    ALIGNED16(xq);
+    HIPCALL(moe::launch_quantize_rows_int8(x, true, rows, cfg->hidden_size, (int8_t*)xq, xs,
+                                           (hipStream_t)stream),
+            "quantise");
+    return MOE_OK;
+  }
   HIPCALL(moe::launch_quant_rows((const uint16_t*)x, rows, cfg->hidden_size, xq, xs,
                                  cfg->weight_dtype == MOE_FP8_E4M3_E8M0,
                                  (hipStream_t)stream),
@@ -1030,6 +1362,7 @@ size_t moe_packed_bytes(const moe_config* cfg, moe_weight_id which) {
   auto bytes = [cfg](bool gate_up, int64_t experts, int n, int kd) {
     if (is_int4(cfg->weight_dtype))
       return moe::packed4_bytes(gate_up, experts, n, kd, int4_group(cfg->weight_dtype));
+    if (is_int8(cfg->weight_dtype)) return moe::packed_int8_bytes(gate_up, experts, n, kd);
     return is_fp8(cfg->weight_dtype) ? moe::packed8_bytes(gate_up, experts, n, kd)
                                      : moe::packed_bytes(gate_up, experts, n, kd);
   };
@@ -1054,7 +1387,14 @@ moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const voi
   CHECK(weight_matrix(cfg, which, &m));
   NONNULL(src);
   NONNULL(dst);
-  if (is_fp8(cfg->weight_dtype))
+  if (is_int8(cfg->weight_dtype)) {
+    CHECK(check_matrix_threads((int64_t)(moe_packed_bytes(cfg, which) / 16)));
+    ALIGNED16(src);
+    ALIGNED16(dst);
+    HIPCALL(moe::launch_pack_int8(m.gate_up, (const int8_t*)src, dst, m.experts, m.n, m.kd,
+                                  (hipStream_t)stream),
+            "pack weight");
+  } else if (is_fp8(cfg->weight_dtype))
     HIPCALL(moe::launch_pack8(m.gate_up, (const uint8_t*)src, dst, m.experts, m.n, m.kd,
                               (hipStream_t)stream),
             "pack weight");
@@ -1068,10 +1408,24 @@ moe_status moe_pack_weight(const moe_config* cfg, moe_weight_id which, const voi
 moe_status moe_quantize_weight(const moe_config* cfg, moe_weight_id which, const void* src,
                                uint8_t* codes, void* scales, void* stream) {
   CHECK(check_cfg(cfg));
-  if (!is_int4(cfg->weight_dtype))
-    return fail(MOE_ERR_UNSUPPORTED, "moe_quantize_weight makes 4-bit weights (MOE_INT4_*)");
+  if (!is_int4(cfg->weight_dtype) && !is_int8(cfg->weight_dtype))
+    return fail(MOE_ERR_UNSUPPORTED,
+                "moe_quantize_weight makes integer weights (MOE_INT4_*, MOE_INT8)");
   Matrix m;
   CHECK(weight_matrix(cfg, which, &m));
+  if (is_int8(cfg->weight_dtype)) {
+    const int64_t rows = m.experts * (m.gate_up ? 2 : 1) * m.n;
+    CHECK(check_matrix_threads(rows * 256));
+    NONNULL(src);
+    NONNULL(codes);
+    NONNULL(scales);
+    ALIGNED16(src);
+    ALIGNED16(codes);
+    HIPCALL(moe::launch_quantize_rows_int8(src, true, rows, m.kd, (int8_t*)codes, (float*)scales,
+                                           (hipStream_t)stream),
+            "quantise weight");
+    return MOE_OK;
+  }
   CHECK(check_matrix_threads(m.experts * (m.gate_up ? 2 : 1) * m.n * (m.kd / 8)));
   NONNULL(src);
   NONNULL(codes);
