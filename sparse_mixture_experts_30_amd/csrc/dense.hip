@@ -73,14 +73,18 @@ dense_gemm(DenseArgs p) {
   f32x16 acc[Tile::kMI][Tile::kNJ];
   Tile::run(lds0, lds1, A, (int)m0, B, (int)n0, p.K, acc);
 
+  // The operands are read for the last time: the waves share their LDS out.
+  float* l = reinterpret_cast<float*>(lds0) + Tile::wave() * (32 * 32 * Tile::kNJ);
+  const int64_t row0 = m0 + Tile::row0();
+  const int64_t col0 = n0 + (kEpi == EPI_SWIGLU ? Tile::col0() / 2 : Tile::col0());
   if constexpr (kEpi == EPI_STORE) {
-    Tile::template rows<false>(lds0, acc, [&](int r, int c, const float (&v)[8]) {
-      const int64_t row = m0 + r, col = n0 + c;
+    wave_rows<false>(l, acc, [&](int r, int c, const float (&v)[8]) {
+      const int64_t row = row0 + r, col = col0 + c;
       if (row < p.M && col < p.N) *reinterpret_cast<u32x4*>(p.c + row * p.N + col) = pack_bf16x8(v);
     });
   } else if constexpr (kEpi == EPI_SWIGLU) {
-    Tile::template rows<true>(lds0, acc, [&](int r, int c, const float (&g)[8], const float (&u)[8]) {
-      const int64_t row = m0 + r, col = n0 + c;
+    wave_rows<true>(l, acc, [&](int r, int c, const float (&g)[8], const float (&u)[8]) {
+      const int64_t row = row0 + r, col = col0 + c;
       if (row >= p.M || col >= p.N) return;
       if (p.gu) {
         *reinterpret_cast<u32x4*>(p.gu + row * 2 * p.N + col) = pack_bf16x8(g);
@@ -94,8 +98,8 @@ dense_gemm(DenseArgs p) {
       }
     });
   } else {
-    Tile::template rows<false>(lds0, acc, [&](int r, int c, const float (&dh)[8]) {
-      const int64_t row = m0 + r, col = n0 + c;
+    wave_rows<false>(l, acc, [&](int r, int c, const float (&dh)[8]) {
+      const int64_t row = row0 + r, col = col0 + c;
       if (row >= p.M || col >= p.N) return;
       const uint16_t* gp = p.gu + row * 2 * p.N + col;
       float g[8], u[8], dg[8], du[8], h[8];

@@ -14,6 +14,7 @@
 // and 4, 5 of a gate/up tile are gate rows of its first and second 32 columns,
 // 2, 3 and 6, 7 the up rows of the same.
 #include "block.hpp"
+#include "gemm_device.hpp"
 #include "items_device.hpp"
 #include "rows_device.hpp"
 
@@ -22,6 +23,8 @@
 namespace moe {
 
 namespace {
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads8 = 256;
 constexpr int kStepK = 128;          // k per packed step
@@ -162,6 +165,175 @@ __global__ void __launch_bounds__(kThreads8) grouped_gemm_int8_few(Int8Args p) {
     int8_few_tile<kGateUp, false>(p, lds, it);
 }
 
+// --------------------------------------------------------------- many rows
+// A tile of at most kM rows (64 or 128) and two packed output tiles, eight
+// waves of kM / 2 rows x 64 columns.  Rows and weights pass through three LDS
+// stages that loads from memory fill directly, two steps ahead: at 64 and 128
+// rows a weight byte the memory, not the matrix cores, sets the pace, and it
+// wants 64 KiB and more in flight a CU.
+constexpr int kManyThreads = 512;
+
+template <bool kGateUp, int kM, bool kStream>
+__device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u32x4* st1,
+                                               u32x4* st2, const Item& it) {
+  constexpr int kMI = kM / 64;          // 32-row blocks a wave
+  constexpr int kW = 2 * kUnits;        // pieces of a step's weights (two packed tiles)
+  constexpr int kLoadsW = kW / kManyThreads, kLoadsA = kM * 8 / kManyThreads;
+  const bool sh = it.g == p.E;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int kdim = sh ? p.kdim_s : p.kdim_r, nsteps = kdim / kStepK;
+  const int nt = sh ? p.nt_s : p.nt_r;
+  // An odd number of packed tiles leaves the last pair's second half to no
+  // one: it repeats the first, and its waves store nothing.
+  const int tile0 = it.ntile * 2, tile1 = min(tile0 + 1, nt - 1);
+  const u32x4* bw = sh ? p.b_s : p.b_r + (int64_t)it.g * nt * nsteps * kUnits;
+  // Waves 0-3 load the first packed tile's blocks, 4-7 the second's.
+  const u32x4* src_w = bw + (int64_t)(wave < 4 ? tile0 : tile1) * nsteps * kUnits +
+                       (wave & 3) * 64 + lane;
+  // Rows tid / 8 + 64 j; past the end the first row again (not stored).
+  const char* src_a[kLoadsA];
+#pragma unroll
+  for (int j = 0; j < kLoadsA; ++j) {
+    const int r = (tid >> 3) + 64 * j, rr = r < it.nrows ? r : 0;
+    const int arow = (!sh && kGateUp) ? p.perm[it.row0 + rr] / p.K : it.row0 + rr;
+    src_a[j] = reinterpret_cast<const char*>(sh ? p.a_s : p.a_r) + (int64_t)arow * kdim +
+               ((tid & 7) ^ ((r ^ (r >> 3)) & 7)) * 16;
+  }
+  auto load = [&](u32x4* l, int step) {
+    u32x4* lw = l + (wave >> 2) * kUnits + (wave & 3) * 64;
+#pragma unroll
+    for (int j = 0; j < kLoadsW; ++j)
+      load_global_to_lds<kStream>(src_w + (int64_t)step * kUnits + j * 256, lw + j * 256);
+#pragma unroll
+    for (int j = 0; j < kLoadsA; ++j)
+      load_global_to_lds<false>(src_a[j] + step * kStepK, l + kW + j * kManyThreads + wave * 64);
+  };
+
+  i32x16 acc[kMI][2];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+  const int lr = lane & 31, lh = lane >> 5;
+  // Wave wn's four fragments of the 16: two blocks of 32 columns (gate and up).
+  const int frag0 = wn * 4 + (lr >> 4);
+  auto compute = [&](const u32x4* l) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      i32x4 a[kMI], b[2];
+#pragma unroll
+      for (int i = 0; i < kMI; ++i)
+        a[i] = __builtin_bit_cast(
+            i32x4, l[kW + row_chunk(wm * (kM / 2) + i * 32 + lr, 2 * t + lh)]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        b[j] = __builtin_bit_cast(i32x4, l[((frag0 + 2 * j) * 2 + (t >> 1)) * 64 +
+                                           (2 * (t & 1) + lh) * 16 + (lr & 15)]);
+#pragma unroll
+      for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  // Step s: its stage has arrived (only step s + 1's loads may be under way) and
+  // no wave reads the stage of step s - 1 any more, which step s + 2 fills.
+  auto one = [&](u32x4* now, u32x4* next, int s) {
+    wait_and_meet<kLoadsW + kLoadsA>();
+    load(next, s + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(now);
+  };
+  auto last = [&](u32x4* now, u32x4* next, int s) {
+    if (s >= nsteps) return;
+    if (s + 1 < nsteps) wait_and_meet<kLoadsW + kLoadsA>();
+    else wait_and_meet<0>();
+    if (s + 2 < nsteps) load(next, s + 2);
+    compute(now);
+  };
+  load(st0, 0);
+  load(st1, min(1, nsteps - 1));
+  int s = 0;
+  for (; s + 5 <= nsteps; s += 3) {
+    one(st0, st2, s);
+    one(st1, st0, s + 1);
+    one(st2, st1, s + 2);
+  }
+  last(st0, st2, s);
+  last(st1, st0, s + 1);
+  last(st2, st1, s + 2);
+  last(st0, st2, s + 3);
+  wait_and_meet<0>();   // the stages are free
+
+  const int ncol = sh ? p.ncol_s : p.ncol_r;
+  const float* as = sh ? p.as_s : p.as_r;
+  const float* bs = sh ? p.bs_s : p.bs_r + (int64_t)it.g * (kGateUp ? 2 : 1) * ncol;
+  const int tile = tile0 + (wn >> 1);
+  if (tile >= nt) return;   // the whole wave; nothing waits behind this
+  f32x16 v[kMI][2];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[i][j][q] = (float)acc[i][j][q];
+  float* l = reinterpret_cast<float*>(wave < 4 ? st0 : st1) + (wave & 3) * (32 * 64);
+  const int row0 = wm * (kM / 2);
+  auto scaled = [&](float (&x)[8], float s, const float* c) {
+    const f32x4 c0 = *reinterpret_cast<const f32x4*>(c),
+                c1 = *reinterpret_cast<const f32x4*>(c + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] *= s * c0[j];
+      x[4 + j] *= s * c1[j];
+    }
+  };
+  if constexpr (kGateUp) {
+    const int col0 = tile * 64 + (wn & 1) * 32;
+    wave_rows<true>(l, v, [&](int r, int c, float (&g)[8], float (&u)[8]) {
+      const int row = row0 + r, col = col0 + c;
+      if (row >= it.nrows) return;
+      const int64_t crow = it.row0 + row;
+      const float s = as[sh ? crow : p.perm[crow] / p.K];
+      scaled(g, s, bs + col);
+      scaled(u, s, bs + ncol + col);
+      f32x4* o = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(sh ? p.c_s : p.c_r) +
+                                          crow * ncol + col);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        o[j] = (f32x4){swiglu(g[4 * j], u[4 * j]), swiglu(g[4 * j + 1], u[4 * j + 1]),
+                       swiglu(g[4 * j + 2], u[4 * j + 2]), swiglu(g[4 * j + 3], u[4 * j + 3])};
+    });
+  } else {
+    const int col0 = tile * 128 + (wn & 1) * 64;
+    wave_rows<false>(l, v, [&](int r, int c, float (&x)[8]) {
+      const int row = row0 + r, col = col0 + c;
+      if (row >= it.nrows) return;
+      const int64_t crow = it.row0 + row;
+      scaled(x, as[crow], bs + col);
+      *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(sh ? p.c_s : p.c_r) + crow * ncol +
+                                col) = pack_bf16x8(x);
+    });
+  }
+}
+
+template <bool kGateUp, int kM>
+__global__ void __launch_bounds__(kManyThreads, 2) grouped_gemm_int8_many(Int8Args p) {
+  constexpr int kStage = 2 * kUnits + kM * 8;
+  __shared__ u32x4 st0[kStage], st1[kStage], st2[kStage];
+  Item it;
+  if (!find_item<kM>(p, it)) return;
+  if (2 * it.ntile >= (it.g == p.E ? p.nt_s : p.nt_r)) return;
+  if (it.alone)
+    int8_many_tile<kGateUp, kM, true>(p, st0, st1, st2, it);
+  else
+    int8_many_tile<kGateUp, kM, false>(p, st0, st1, st2, it);
+}
+
 // ---------------------------------------------------------------- quantising
 // Codes and scale of one row of kIn (bf16 or fp32) values: a workgroup a row.
 // 127 x is exact for bf16 and its quotient by the maximum, if not a tie, is
@@ -264,15 +436,27 @@ pack_int8_kernel(bool gate_up, const int8_t* __restrict__ codes, u32x4* __restri
                                            16 * (lane >> 4));
 }
 
+// Rows of an M-tile, which name the kernel, for the whole layer.
+int tile_rows(const FfnDims& d) {
+  if (d.T <= kFewRows || d.N <= 8 * (int64_t)d.E) return kFewRows;
+  return d.N <= 64 * (int64_t)d.E ? 64 : 128;
+}
+
 // nt: packed tiles of the group with the most of them.
 template <bool kGateUp>
-hipError_t launch_gemm(Int8Args a, int64_t mtiles, int nt, hipStream_t s) {
-  a.ntn = nt;
+hipError_t launch_gemm(Int8Args a, int rows, int64_t mtiles, int nt, hipStream_t s) {
+  a.ntn = rows == kFewRows ? nt : (nt + 1) / 2;
   const int64_t work = mtiles * a.ntn;
-  if (work > kMaxGridThreads / kThreads8 - kXcdGrid) return hipErrorInvalidValue;
-  MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int8_few<true>" : "grouped_gemm_int8_few<false>",
-    hipLaunchKernelGGL((grouped_gemm_int8_few<kGateUp>), dim3(xcd_grid(work)), dim3(kThreads8), 0,
-                       s, a));
+  if (work > kMaxGridThreads / kManyThreads - kXcdGrid) return hipErrorInvalidValue;
+  const dim3 grid(xcd_grid(work));
+  if (rows == kFewRows)
+    MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int8_few<true>" : "grouped_gemm_int8_few<false>",
+      hipLaunchKernelGGL((grouped_gemm_int8_few<kGateUp>), grid, dim3(kThreads8), 0, s, a));
+  else
+    MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int8_many<true>" : "grouped_gemm_int8_many<false>",
+      hipLaunchKernelGGL((rows == 64 ? grouped_gemm_int8_many<kGateUp, 64>
+                                     : grouped_gemm_int8_many<kGateUp, 128>),
+                         grid, dim3(kManyThreads), 0, s, a));
   return hipGetLastError();
 }
 
@@ -311,7 +495,8 @@ hipError_t launch_ffn_int8(const FfnDims& d, const int8_t* xq, const float* xs,
                            const void* ws13p, const float* ws13s, const void* ws2p,
                            const float* ws2s, float* h, int8_t* hq, float* hs, uint16_t* y,
                            uint16_t* ys, hipStream_t s) {
-  const int64_t mt = ffn_grid_mtiles(d, kFewRows);
+  const int rows = tile_rows(d);
+  const int64_t mt = ffn_grid_mtiles(d, rows);
   const bool routed = d.groups & kGroupRouted, shared = (d.groups & kGroupShared) && d.Is > 0;
   Int8Args a{};
   a.offsets = offsets;
@@ -334,7 +519,7 @@ hipError_t launch_ffn_int8(const FfnDims& d, const int8_t* xq, const float* xs,
   a.ncol_s = d.Is;
   a.c_r = h;
   a.c_s = h + d.N * d.I;
-  hipError_t e = launch_gemm<true>(a, mt, std::max(a.nt_r, a.nt_s), s);
+  hipError_t e = launch_gemm<true>(a, rows, mt, std::max(a.nt_r, a.nt_s), s);
   if (e != hipSuccess) return e;
 
   int8_t* hq_s = hq + d.N * d.I;
@@ -362,7 +547,7 @@ hipError_t launch_ffn_int8(const FfnDims& d, const int8_t* xq, const float* xs,
   a.ncol_r = a.ncol_s = d.H;
   a.c_r = y;
   a.c_s = ys;
-  return launch_gemm<false>(a, mt, a.nt_r, s);
+  return launch_gemm<false>(a, rows, mt, a.nt_r, s);
 }
 
 }  // namespace moe

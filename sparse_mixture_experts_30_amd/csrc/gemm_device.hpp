@@ -49,6 +49,32 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, u32x4* lds
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, offset, 0, 0, 0);
 }
 
+// The same from an address of its own a lane into the 64 pieces from lds (the
+// same in every lane); kNt: not kept in cache.  The instruction is written out
+// for pipelines of more than two stages: what the compiler sees of it makes it
+// wait, at a loop's first read of LDS, for every load under way.  It has no
+// result register; wait_and_meet waits for it.
+template <bool kNt>
+__device__ __forceinline__ void load_global_to_lds(const void* p, u32x4* lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)lds;
+  if (kNt)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
+                 ::"s"(at), "v"(p) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 ::"s"(at), "v"(p) : "memory");
+}
+
+// Waits until at most kLeft of this wave's loads to LDS are under way and its
+// LDS reads are done, then for the other waves.  (A barrier by itself would
+// let the compiler move LDS accesses across it, __syncthreads waits for every
+// load.)
+template <int kLeft>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(kLeft < 63, "the counter's range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+}
+
 __device__ __forceinline__ int row_chunk(int r, int c) {
   return r * 8 + (c ^ ((r ^ (r >> 3)) & 7));
 }
@@ -121,8 +147,8 @@ __device__ __forceinline__ bf16x8 fragment(const u32x4* lds, int row, int kk, in
   return as_bf16x8(lds[row_chunk(row + (lane & 31), 2 * kk + (lane >> 5))]);
 }
 
-// The tile's accumulators: wave (wm, wn) of kWM x kWN holds rows
-// wm kM / kWM + 32 i, columns wn kN / kWN + 32 j.  lds0, lds1: two arrays of
+// The tile's accumulators: wave (wm, wn) of kWM x kWN holds rows row0() + 32 i,
+// columns col0() + 32 j.  lds0, lds1: two arrays of
 // (kM + kN) * 8 16-byte pieces, apart in the compiler's eyes, so that it sees
 // that a load into one does not touch reads of the other.
 template <int kM, int kN, int kWM, int kWN, int kOpA, int kOpB>
@@ -131,14 +157,18 @@ struct GemmTile {
   static constexpr int kMI = kM / kWM / 32, kNJ = kN / kWN / 32;
   static constexpr int kLds = (kM + kN) * 8;
 
+  static __device__ __forceinline__ int wave() {
+    return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  }
+  static __device__ __forceinline__ int row0() { return wave() / kWN * (kM / kWM); }
+  static __device__ __forceinline__ int col0() { return wave() % kWN * (kN / kWN); }
+
   static __device__ __forceinline__ void run(u32x4* lds0, u32x4* lds1, const Operand& A, int m0,
                                              const Operand& B, int n0, int64_t K,
                                              f32x16 (&acc)[kMI][kNJ]) {
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / kWN, wn = wave % kWN;
-    const Stager<kOpA, kM, kThreads> sa(A, m0, tid, wave);
-    const Stager<kOpB, kN, kThreads> sb(B, n0, tid, wave);
+    const Stager<kOpA, kM, kThreads> sa(A, m0, tid, wave());
+    const Stager<kOpB, kN, kThreads> sb(B, n0, tid, wave());
     const int nsteps = (int)((K + kGemmBK - 1) / kGemmBK);
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
@@ -157,10 +187,10 @@ struct GemmTile {
         bf16x8 a[kMI], b[kNJ];
 #pragma unroll
         for (int i = 0; i < kMI; ++i)
-          a[i] = fragment<kOpA, kM>(l, wm * (kM / kWM) + i * 32, kk, lane);
+          a[i] = fragment<kOpA, kM>(l, row0() + i * 32, kk, lane);
 #pragma unroll
         for (int j = 0; j < kNJ; ++j)
-          b[j] = fragment<kOpB, kN>(l + kM * 8, wn * (kN / kWN) + j * 32, kk, lane);
+          b[j] = fragment<kOpB, kN>(l + kM * 8, col0() + j * 32, kk, lane);
 #pragma unroll
         for (int i = 0; i < kMI; ++i)
 #pragma unroll
@@ -188,66 +218,61 @@ struct GemmTile {
       __syncthreads();
     }
   }
+};
 
-  // Hands the tile out row by row: f(row, column, v) with v the fp32 values of
-  // kCols consecutive columns of a tile row, through the wave's own 32 x
-  // (32 kNJ) floats of LDS (no one reads the operands any more).  With kPair,
-  // column blocks 2 j and 2 j + 1 come together: f(row, column in block pair /
-  // 2, v, w).
-  template <bool kPair, class F>
-  static __device__ __forceinline__ void rows(u32x4* lds, const f32x16 (&acc)[kMI][kNJ], F f) {
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / kWN, wn = wave % kWN;
-    const int lr = lane & 31, lh = lane >> 5;
-    static_assert(kNJ == 1 || kNJ == 2, "one or two column blocks a wave");
-    constexpr int kCols = 32 * kNJ;
-    float* l = reinterpret_cast<float*>(lds) + wave * 32 * kCols;
-    // physical column: the other half for every second group of four rows
-    auto phys = [](int row, int col) { return row * kCols + (kNJ == 2 ? col ^ ((row & 4) * 8) : col); };
+// Hands a wave's part of a tile out row by row: f(row, column, v) with v the fp32
+// values of eight consecutive columns, through the wave's own 32 x 32 kNJ floats
+// of LDS.  acc [kMI][kNJ] are 32 x 32 blocks; rows and columns count from the
+// wave's first.  With kPair, the same columns of the two column blocks come
+// together: f(row, column in a block, v, w).
+template <bool kPair, int kMI, int kNJ, class F>
+__device__ __forceinline__ void wave_rows(float* l, const f32x16 (&acc)[kMI][kNJ], F f) {
+  static_assert(kNJ == 1 || kNJ == 2, "one or two column blocks a wave");
+  constexpr int kCols = 32 * kNJ;
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  // physical column: the other half for every second group of four rows
+  auto phys = [](int row, int col) {
+    return row * kCols + (kNJ == 2 ? col ^ ((row & 4) * 8) : col);
+  };
 #pragma unroll
-    for (int i = 0; i < kMI; ++i) {
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  for (int i = 0; i < kMI; ++i) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int j = 0; j < kNJ; ++j)
+    for (int j = 0; j < kNJ; ++j)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const int row = 8 * (q >> 2) + 4 * lh + (q & 3);
-          l[phys(row, j * 32 + lr)] = acc[i][j][q];
-        }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      const int row_t = wm * (kM / kWM) + i * 32;
-      auto get = [&](int row, int col, float (&v)[8]) {
-        const f32x4* p = reinterpret_cast<const f32x4*>(l + phys(row, col));
-        const f32x4 x = p[0], y = p[1];
+      for (int q = 0; q < 16; ++q)
+        l[phys(8 * (q >> 2) + 4 * lh + (q & 3), j * 32 + lr)] = acc[i][j][q];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    auto get = [&](int row, int col, float (&v)[8]) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(l + phys(row, col));
+      const f32x4 x = p[0], y = p[1];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          v[t] = x[t];
-          v[4 + t] = y[t];
-        }
-      };
-      if constexpr (kPair) {
-        static_assert(kNJ == 2, "a pair of column blocks a wave");
+      for (int t = 0; t < 4; ++t) {
+        v[t] = x[t];
+        v[4 + t] = y[t];
+      }
+    };
+    if constexpr (kPair) {
+      static_assert(kNJ == 2, "a pair of column blocks");
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int row = t * 16 + (lane >> 2), col = (lane & 3) * 8;
-          float v[8], w[8];
-          get(row, col, v);
-          get(row, 32 + col, w);
-          f(row_t + row, wn * 32 + col, v, w);
-        }
-      } else {
-        constexpr int kL = kCols / 8;   // lanes a row
+      for (int t = 0; t < 2; ++t) {
+        const int row = t * 16 + (lane >> 2), col = (lane & 3) * 8;
+        float v[8], w[8];
+        get(row, col, v);
+        get(row, 32 + col, w);
+        f(i * 32 + row, col, v, w);
+      }
+    } else {
+      constexpr int kL = kCols / 8;   // lanes a row
 #pragma unroll
-        for (int t = 0; t < kL / 2; ++t) {
-          const int row = t * (64 / kL) + lane / kL, col = (lane % kL) * 8;
-          float v[8];
-          get(row, col, v);
-          f(row_t + row, wn * kCols + col, v);
-        }
+      for (int t = 0; t < kL / 2; ++t) {
+        const int row = t * (64 / kL) + lane / kL, col = (lane % kL) * 8;
+        float v[8];
+        get(row, col, v);
+        f(i * 32 + row, col, v);
       }
     }
   }
-};
+}
 
 }  // namespace moe
