@@ -49,10 +49,10 @@ __device__ __forceinline__ bool tile_of(const DenseArgs& p, int& m, int& n) {
 }
 
 template <int kM, int kN, int kWM, int kWN, int kOpA, int kOpB, int kEpi>
-__global__ void __launch_bounds__(64 * kWM * kWN, kM* kN >= 256 * 256 ? 2 : 1)
+__global__ void __launch_bounds__(64 * kWM * kWN, kWM * kWN / 4)
 dense_gemm(DenseArgs p) {
   typedef GemmTile<kM, kN, kWM, kWN, kOpA, kOpB> Tile;
-  __shared__ u32x4 lds0[Tile::kLds], lds1[Tile::kLds];
+  __shared__ u32x4 lds[4 * Tile::kStage];
   int m, n;
   if (!tile_of(p, m, n)) return;
   constexpr int kNh = kEpi == EPI_SWIGLU ? kN / 2 : kN;   // output columns of a tile
@@ -71,12 +71,13 @@ dense_gemm(DenseArgs p) {
     B.rows = p.N - n0;
   }
   f32x16 acc[Tile::kMI][Tile::kNJ];
-  Tile::run(lds0, lds1, A, (int)m0, B, (int)n0, p.K, acc);
+  Tile::run(lds, A, (int)m0, B, (int)n0, p.K, acc);
 
   // The operands are read for the last time: the waves share their LDS out.
-  float* l = reinterpret_cast<float*>(lds0) + Tile::wave() * (32 * 32 * Tile::kNJ);
-  const int64_t row0 = m0 + Tile::row0();
-  const int64_t col0 = n0 + (kEpi == EPI_SWIGLU ? Tile::col0() / 2 : Tile::col0());
+  const int w = Tile::wave();
+  float* l = reinterpret_cast<float*>(lds) + w * (32 * (Tile::kNJ == 1 ? 32 : 64));
+  const int64_t row0 = m0 + Tile::row0(w);
+  const int64_t col0 = n0 + (kEpi == EPI_SWIGLU ? Tile::col0(w) / 2 : Tile::col0(w));
   if constexpr (kEpi == EPI_STORE) {
     wave_rows<false>(l, acc, [&](int r, int c, const float (&v)[8]) {
       const int64_t row = row0 + r, col = col0 + c;
@@ -122,14 +123,14 @@ dense_gemm(DenseArgs p) {
 
 template <int kOpA, int kOpB, int kEpi>
 hipError_t launch_gemm(DenseArgs a, const char* name, hipStream_t s) {
-  constexpr int kM = 256, kN = 256, kH = kEpi == EPI_SWIGLU ? kN / 2 : kN;
+  constexpr int kM = 256, kN = 256, kWM = 2, kWN = 4, kH = kEpi == EPI_SWIGLU ? kN / 2 : kN;
   a.mt = (int)((a.M + kM - 1) / kM);
   a.nt = (int)((a.N + kH - 1) / kH);
   const int64_t work = (int64_t)a.mt * a.nt;
   if (work == 0) return hipSuccess;
   const unsigned grid = (unsigned)((work + kNumXcd - 1) / kNumXcd * kNumXcd);
   MOE_TIMED_LAUNCH(s, name,
-    hipLaunchKernelGGL((dense_gemm<kM, kN, 2, 4, kOpA, kOpB, kEpi>), dim3(grid), dim3(512), 0, s,
+    hipLaunchKernelGGL((dense_gemm<kM, kN, kWM, kWN, kOpA, kOpB, kEpi>), dim3(grid), dim3(64 * kWM * kWN), 0, s,
                        a));
   return hipGetLastError();
 }

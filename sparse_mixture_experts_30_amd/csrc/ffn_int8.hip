@@ -173,6 +173,11 @@ __global__ void __launch_bounds__(kThreads8) grouped_gemm_int8_few(Int8Args p) {
 // wants 64 KiB and more in flight a CU.
 constexpr int kManyThreads = 512;
 
+// Place of 16-byte chunk c of row r among a step's rows of eight chunks.
+__device__ __forceinline__ int token_chunk(int r, int c) {
+  return r * 8 + (c ^ ((r ^ (r >> 3)) & 7));
+}
+
 template <bool kGateUp, int kM, bool kStream>
 __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u32x4* st1,
                                                u32x4* st2, const Item& it) {
@@ -199,16 +204,17 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u3
     const int r = (tid >> 3) + 64 * j, rr = r < it.nrows ? r : 0;
     const int arow = (!sh && kGateUp) ? p.perm[it.row0 + rr] / p.K : it.row0 + rr;
     src_a[j] = reinterpret_cast<const char*>(sh ? p.a_s : p.a_r) + (int64_t)arow * kdim +
-               ((tid & 7) ^ ((r ^ (r >> 3)) & 7)) * 16;
+               (token_chunk(r, tid & 7) - r * 8) * 16;
   }
-  auto load = [&](u32x4* l, int step) {
-    u32x4* lw = l + (wave >> 2) * kUnits + (wave & 3) * 64;
+  auto load = [&](const u32x4* l, int step) {
+    const uint32_t la = lds_address(l), lw = la + ((wave >> 2) * kUnits + (wave & 3) * 64) * 16;
 #pragma unroll
     for (int j = 0; j < kLoadsW; ++j)
-      load_global_to_lds<kStream>(src_w + (int64_t)step * kUnits + j * 256, lw + j * 256);
+      load_global_to_lds<kStream>(src_w + (int64_t)step * kUnits + j * 256, lw + j * 4096);
 #pragma unroll
     for (int j = 0; j < kLoadsA; ++j)
-      load_global_to_lds<false>(src_a[j] + step * kStepK, l + kW + j * kManyThreads + wave * 64);
+      load_global_to_lds<false>(src_a[j] + step * kStepK,
+                                la + (kW + j * kManyThreads + wave * 64) * 16);
   };
 
   i32x16 acc[kMI][2];
@@ -228,7 +234,7 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u3
 #pragma unroll
       for (int i = 0; i < kMI; ++i)
         a[i] = __builtin_bit_cast(
-            i32x4, l[kW + row_chunk(wm * (kM / 2) + i * 32 + lr, 2 * t + lh)]);
+            i32x4, l[kW + token_chunk(wm * (kM / 2) + i * 32 + lr, 2 * t + lh)]);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         b[j] = __builtin_bit_cast(i32x4, l[((frag0 + 2 * j) * 2 + (t >> 1)) * 64 +

@@ -4,18 +4,23 @@
 // A[k][m], B[k][n]), so that the products of a feed-forward block and of its
 // backward need no transposed copies.
 //
-// Tile kM x kN, k in steps of 64 through two LDS buffers that are filled by
-// loads from memory straight to LDS.  A row operand's step is [row][64 k] in
-// eight 16-byte chunks, chunk c of row r at c ^ (r & 7 ^ r >> 3 & 7); a col
-// operand's is [64 k][row], the 32-byte piece s of k row k at s ^ f(k),
-// f = (k & 3) ^ (k & 3) << 1, and is transposed by the LDS's 16-bit
-// transposing read: four k rows of 16 values a group of 16 lanes.  Either way
-// the lanes that read together fall in different banks.
+// Tile kM x kN, k in steps of 32 through four LDS stages that loads from memory
+// fill directly.  A row operand's step is [row][32 k] in four 16-byte chunks,
+// chunk c of row r at c ^ ((r >> 1 ^ r >> 3) & 3); a col operand's is [32 k][row], the
+// 32-byte piece s of k row k at s ^ f(k), f = (k & 3) ^ (k & 3) << 1, and is
+// transposed by the LDS's 16-bit transposing read: four k rows of 16 values a
+// group of 16 lanes.  Either way the lanes that read together fall in different
+// banks.
+//
+// At the start of step s the stages of s and s + 1 are filled, s + 2 is under
+// way and s + 3 is started into the stage that step s - 1 has read.  Each half
+// of a step's MFMAs runs while the operands of the next half are read, across
+// the barrier too: the matrix cores wait for neither memory nor LDS.
 //
 // Loads go through buffer descriptors that end at the operand's last valid
 // row (row operand) or last valid k (col operand): what lies past it arrives as
-// zeros, so no size has to be a multiple of the tile, and a k range that ends
-// inside a step adds nothing.
+// zeros, so no size has to be a multiple of the tile, a k range that ends
+// inside a step adds nothing, and steps past the last are loaded in vain.
 #pragma once
 
 #include "moe_internal.hpp"
@@ -26,7 +31,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kGemmBK = 64;
+constexpr int kGemmBK = 32;
 
 enum : int { OP_ROW = 0, OP_COL = 1, OP_GATE_UP = 2 };
 
@@ -40,23 +45,35 @@ struct Operand {
   int64_t rows;   // row operand: rows from p on; col operand: valid k
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const char* p, int64_t bytes) {
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ uint32_t scalar(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A buffer descriptor of `bytes` from p (clamped to what it can hold).
+__device__ __forceinline__ u32x4 buffer_of(const char* p, int64_t bytes) {
   const int64_t b = bytes < 0 ? 0 : bytes > 0xfffffff0LL ? 0xfffffff0LL : bytes;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, (int)(uint32_t)b, 0x00020000);
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  return (u32x4){scalar((uint32_t)a), scalar((uint32_t)(a >> 32) & 0xffffu), scalar((uint32_t)b),
+                 0x00020000u};
 }
 
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, u32x4* lds, int offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, offset, 0, 0, 0);
+// Byte address in LDS.
+__device__ __forceinline__ uint32_t lds_address(const u32x4* lds) {
+  return scalar((uint32_t)(uintptr_t)(lds_void*)lds);
 }
 
-// The same from an address of its own a lane into the 64 pieces from lds (the
-// same in every lane); kNt: not kept in cache.  The instruction is written out
-// for pipelines of more than two stages: what the compiler sees of it makes it
-// wait, at a loop's first read of LDS, for every load under way.  It has no
-// result register; wait_and_meet waits for it.
+// Loads of 16 bytes a lane from memory into 1 KiB of LDS from address lds (the
+// same in every lane): from an offset into a buffer, or from an address.  The
+// instructions are written out because of what the compiler does with more than
+// two stages: at a loop's first read of LDS it waits for every load under way.
+// They have no result register; wait_and_meet waits for them.
+__device__ __forceinline__ void load_to_lds(u32x4 buffer, uint32_t lds, int offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               ::"s"(lds), "v"(offset), "s"(buffer) : "memory");
+}
+
+// kNt: not kept in cache.
 template <bool kNt>
-__device__ __forceinline__ void load_global_to_lds(const void* p, u32x4* lds) {
-  const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)lds;
+__device__ __forceinline__ void load_global_to_lds(const void* p, uint32_t at) {
   if (kNt)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
                  ::"s"(at), "v"(p) : "memory");
@@ -75,9 +92,8 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
-__device__ __forceinline__ int row_chunk(int r, int c) {
-  return r * 8 + (c ^ ((r ^ (r >> 3)) & 7));
-}
+__device__ __forceinline__ int row_swizzle(int r, int c) { return c ^ ((r >> 1 ^ r >> 3) & 3); }
+__device__ __forceinline__ int row_chunk(int r, int c) { return r * 4 + row_swizzle(r, c); }
 template <int kRows>
 __device__ __forceinline__ int col_piece(int k, int s) {
   return s ^ (((k & 3) ^ ((k & 3) << 1)) & (kRows / 16 - 1));
@@ -86,8 +102,9 @@ __device__ __forceinline__ int col_piece(int k, int s) {
 // Stages one operand of kRows rows with kThreads threads.
 template <int kOp, int kRows, int kThreads>
 struct Stager {
-  static constexpr int kLoads = kRows * 8 / kThreads;   // 16-byte pieces a thread
+  static constexpr int kLoads = kRows * 4 / kThreads;   // 16-byte pieces a thread
   static constexpr int kPer = kRows / 8;                // pieces of a k row (col operand)
+  static constexpr int kPass = kThreads / 4;            // rows a load (row operand)
   const Operand& o;
   int wave;
   int at;   // this thread's offset of load 0, step 0
@@ -98,36 +115,25 @@ struct Stager {
       const int k = tid / kPer, c = tid % kPer;
       at = (int)(k * o.ld) + (row0 + (col_piece<kRows>(k, c >> 1) * 2 + (c & 1)) * 8) * 2;
     } else {
-      const int r = tid >> 3, c = (tid & 7) ^ ((r ^ (r >> 3)) & 7);
+      const int r = tid >> 2, c = row_swizzle(r, tid & 3);
       // gate / up: row blocks 2 i and 2 i + 1 of 32 are rows 32 i.. of the two
       at = (int)((kOp == OP_GATE_UP ? (r & 31) + (r >> 6) * 32 : r) * o.ld) + c * 16;
     }
   }
-  // Starts the loads of k step `step` into lds [kRows * 8].
-  __device__ __forceinline__ void load(u32x4* lds, int step) const {
-    if (kOp == OP_COL) {
-      const auto rs = buffer_of(o.p[0] + (int64_t)step * kGemmBK * o.ld,
-                                (o.rows - (int64_t)step * kGemmBK) * o.ld);
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j)   // k rows kThreads / kPer apart: a multiple of 4
-        load_to_lds(rs, lds + j * kThreads + wave * 64, at + j * (kThreads / kPer) * (int)o.ld);
-    } else if (kOp == OP_ROW) {
-      const auto rs = buffer_of(o.p[0], o.rows * o.ld);
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-        load_to_lds(rs, lds + j * kThreads + wave * 64,
-                    at + j * (kThreads / 8) * (int)o.ld + step * (kGemmBK * 2));
-    } else {
-      const auto r0 = buffer_of(o.p[0], o.rows * o.ld), r1 = buffer_of(o.p[1], o.rows * o.ld);
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        // kThreads / 8 rows a load: 64 (the wave decides the matrix) or 32 (j does)
-        const bool up = kThreads == 512 ? wave >= 4 : (j & 1);
-        const int rows = kThreads == 512 ? 32 * j : 32 * (j >> 1);
-        load_to_lds(up ? r1 : r0, lds + j * kThreads + wave * 64,
-                    at + rows * (int)o.ld + step * (kGemmBK * 2));
-      }
-    }
+  __device__ __forceinline__ u32x4 buffer(int step) const {
+    if (kOp == OP_COL)
+      return buffer_of(o.p[0] + (int64_t)step * kGemmBK * o.ld,
+                       (o.rows - (int64_t)step * kGemmBK) * o.ld);
+    // 16 rows a wave: one matrix
+    return buffer_of(kOp == OP_GATE_UP && (wave >> 1 & 1) ? o.p[1] : o.p[0], o.rows * o.ld);
+  }
+  // Starts load j of k step `step` into the operand's place of a stage.
+  __device__ __forceinline__ void load(u32x4 buf, uint32_t lds, int step, int j) const {
+    // k rows kThreads / kPer apart, a multiple of 4; or rows kPass apart
+    const int off = kOp == OP_COL        ? j * (kThreads / kPer) * (int)o.ld
+                    : kOp == OP_GATE_UP ? j * (kPass / 2) * (int)o.ld + step * (kGemmBK * 2)
+                                         : j * kPass * (int)o.ld + step * (kGemmBK * 2);
+    load_to_lds(buf, lds + (j * kThreads + wave * 64) * 16, at + off);
   }
 };
 
@@ -148,27 +154,26 @@ __device__ __forceinline__ bf16x8 fragment(const u32x4* lds, int row, int kk, in
 }
 
 // The tile's accumulators: wave (wm, wn) of kWM x kWN holds rows row0() + 32 i,
-// columns col0() + 32 j.  lds0, lds1: two arrays of
-// (kM + kN) * 8 16-byte pieces, apart in the compiler's eyes, so that it sees
-// that a load into one does not touch reads of the other.
+// columns col0() + 32 j.  lds: four stages of kStage 16-byte pieces.
 template <int kM, int kN, int kWM, int kWN, int kOpA, int kOpB>
 struct GemmTile {
   static constexpr int kThreads = 64 * kWM * kWN;
   static constexpr int kMI = kM / kWM / 32, kNJ = kN / kWN / 32;
-  static constexpr int kLds = (kM + kN) * 8;
+  static constexpr int kStage = (kM + kN) * 4;
 
-  static __device__ __forceinline__ int wave() {
-    return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  }
-  static __device__ __forceinline__ int row0() { return wave() / kWN * (kM / kWM); }
-  static __device__ __forceinline__ int col0() { return wave() % kWN * (kN / kWN); }
+  static __device__ __forceinline__ int wave() { return (int)scalar(threadIdx.x >> 6); }
+  static __device__ __forceinline__ int row0(int wave) { return wave / kWN * (kM / kWM); }
+  static __device__ __forceinline__ int col0(int wave) { return wave % kWN * (kN / kWN); }
 
-  static __device__ __forceinline__ void run(u32x4* lds0, u32x4* lds1, const Operand& A, int m0,
+  static __device__ __forceinline__ void run(u32x4* lds, const Operand& A, int m0,
                                              const Operand& B, int n0, int64_t K,
                                              f32x16 (&acc)[kMI][kNJ]) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const Stager<kOpA, kM, kThreads> sa(A, m0, tid, wave());
-    const Stager<kOpB, kN, kThreads> sb(B, n0, tid, wave());
+    const int tid = threadIdx.x, lane = tid & 63, w = wave();
+    const int wrow = row0(w), wcol = col0(w);
+    const uint32_t lds_at = lds_address(lds);
+    const Stager<kOpA, kM, kThreads> sa(A, m0, tid, w);
+    const Stager<kOpB, kN, kThreads> sb(B, n0, tid, w);
+    constexpr int kLoads = sa.kLoads + sb.kLoads;
     const int nsteps = (int)((K + kGemmBK - 1) / kGemmBK);
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
@@ -176,103 +181,137 @@ struct GemmTile {
       for (int j = 0; j < kNJ; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+    if (nsteps == 0) return;
 
-    auto load = [&](u32x4* l, int step) {
-      sa.load(l, step);
-      sb.load(l + kM * 8, step);
+    // Load i of a step, in [0, kLoads).
+    auto load = [&](const u32x4& ba, const u32x4& bb, int stage, int step, int i) {
+      const uint32_t at = lds_at + stage * (kStage * 16);
+      if (i < sa.kLoads) sa.load(ba, at, step, i);
+      else sb.load(bb, at + kM * 64, step, i - sa.kLoads);
     };
-    auto compute = [&](const u32x4* l) {
+    auto load_all = [&](int stage, int step) {
+      const u32x4 ba = sa.buffer(step), bb = sb.buffer(step);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        bf16x8 a[kMI], b[kNJ];
+      for (int i = 0; i < kLoads; ++i) load(ba, bb, stage, step, i);
+    };
+    struct Half {
+      bf16x8 a[kMI], b[kNJ];
+    };
+    // Operand i of half kk of a stage, in [0, kMI + kNJ): b[0], a[0], b[1], the rest.
+    constexpr int kReads = kMI + kNJ;
+    auto read = [&](Half& f, int stage, int kk, int i) {
+      const u32x4* l = lds + stage * kStage;
+      if (i == 0 || (i >= 2 && i <= kNJ))
+        f.b[i == 0 ? 0 : i - 1] =
+            fragment<kOpB, kN>(l + kM * 4, wcol + (i == 0 ? 0 : i - 1) * 32, kk, lane);
+      else
+        f.a[i == 1 ? 0 : i - kNJ] =
+            fragment<kOpA, kM>(l, wrow + (i == 1 ? 0 : i - kNJ) * 32, kk, lane);
+    };
+    // A half step's MFMAs, and between them the reads of the next half step's
+    // operands and the loads of a later step.
+    auto half = [&](const Half& f, Half& next, int stage, int kk, bool loads, int to, int step) {
+      u32x4 ba, bb;
+      if (loads) {
+        ba = sa.buffer(step);
+        bb = sb.buffer(step);
+      }
 #pragma unroll
-        for (int i = 0; i < kMI; ++i)
-          a[i] = fragment<kOpA, kM>(l, row0() + i * 32, kk, lane);
+      for (int q = 0; q < kMI * kNJ; ++q) {
+        const int i = q / kNJ, j = q % kNJ;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+        constexpr int kMfma = kMI * kNJ;
 #pragma unroll
-        for (int j = 0; j < kNJ; ++j)
-          b[j] = fragment<kOpB, kN>(l + kM * 8, col0() + j * 32, kk, lane);
+        for (int r = q; r < kReads; r += kMfma) read(next, stage, kk, r);
+        if (loads) {
 #pragma unroll
-        for (int i = 0; i < kMI; ++i)
-#pragma unroll
-          for (int j = 0; j < kNJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+          for (int r = q; r < kLoads; r += kMfma) load(ba, bb, to, step, r);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
-    // Step s computes from one buffer while step s + 1 arrives in the other;
-    // the barrier at its end waits for both.
-    load(lds0, 0);
-    __syncthreads();
-    int s = 0;
-    for (; s + 2 <= nsteps; s += 2) {
-      load(lds1, s + 1);
+    Half f0, f1;
+    // Step s: stages s and (behind the barrier) s + 1 are there.
+    auto step = [&](int stage, int s) {
+      half(f0, f1, stage, 1, false, 0, 0);
+      wait_and_meet<kLoads>();   // step s + 1 is there, the stage of s - 1 is read
       __builtin_amdgcn_sched_barrier(0);
-      compute(lds0);
-      __syncthreads();
-      if (s + 2 < nsteps) load(lds0, s + 2);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(lds1);
-      __syncthreads();
+      half(f1, f0, (stage + 1) & 3, 0, true, (stage + 3) & 3, s + 3);
+    };
+    load_all(0, 0);
+    load_all(1, 1);
+    load_all(2, 2);
+    wait_and_meet<2 * kLoads>();
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) read(f0, 0, 0, i);
+    for (int s = 0;;) {
+      step(0, s);
+      if (++s >= nsteps) break;
+      step(1, s);
+      if (++s >= nsteps) break;
+      step(2, s);
+      if (++s >= nsteps) break;
+      step(3, s);
+      if (++s >= nsteps) break;
     }
-    if (s < nsteps) {
-      compute(lds0);
-      __syncthreads();
-    }
+    wait_and_meet<0>();   // the LDS is free
   }
 };
 
 // Hands a wave's part of a tile out row by row: f(row, column, v) with v the fp32
-// values of eight consecutive columns, through the wave's own 32 x 32 kNJ floats
-// of LDS.  acc [kMI][kNJ] are 32 x 32 blocks; rows and columns count from the
-// wave's first.  With kPair, the same columns of the two column blocks come
-// together: f(row, column in a block, v, w).
+// values of eight consecutive columns, through the wave's own 32 x 64 (kNJ 1: 32
+// x 32) floats of LDS.  acc [kMI][kNJ] are 32 x 32 blocks; rows and columns count
+// from the wave's first.  With kPair, column blocks 2 j and 2 j + 1 come together:
+// f(row, column, v, w), the columns of the pairs counted by halves.
 template <bool kPair, int kMI, int kNJ, class F>
 __device__ __forceinline__ void wave_rows(float* l, const f32x16 (&acc)[kMI][kNJ], F f) {
-  static_assert(kNJ == 1 || kNJ == 2, "one or two column blocks a wave");
-  constexpr int kCols = 32 * kNJ;
+  constexpr int kB = kNJ == 1 ? 1 : 2, kCols = 32 * kB;   // column blocks at a time
+  static_assert(kNJ % kB == 0 && (!kPair || kB == 2), "pairs of column blocks");
   const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
   // physical column: the other half for every second group of four rows
   auto phys = [](int row, int col) {
-    return row * kCols + (kNJ == 2 ? col ^ ((row & 4) * 8) : col);
+    return row * kCols + (kB == 2 ? col ^ ((row & 4) * 8) : col);
   };
 #pragma unroll
-  for (int i = 0; i < kMI; ++i) {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  for (int i = 0; i < kMI; ++i)
 #pragma unroll
-    for (int j = 0; j < kNJ; ++j)
+    for (int j0 = 0; j0 < kNJ; j0 += kB) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        l[phys(8 * (q >> 2) + 4 * lh + (q & 3), j * 32 + lr)] = acc[i][j][q];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    auto get = [&](int row, int col, float (&v)[8]) {
-      const f32x4* p = reinterpret_cast<const f32x4*>(l + phys(row, col));
-      const f32x4 x = p[0], y = p[1];
+      for (int j = 0; j < kB; ++j)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        v[t] = x[t];
-        v[4 + t] = y[t];
-      }
-    };
-    if constexpr (kPair) {
-      static_assert(kNJ == 2, "a pair of column blocks");
+        for (int q = 0; q < 16; ++q)
+          l[phys(8 * (q >> 2) + 4 * lh + (q & 3), j * 32 + lr)] = acc[i][j0 + j][q];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      auto get = [&](int row, int col, float (&v)[8]) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(l + phys(row, col));
+        const f32x4 x = p[0], y = p[1];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int row = t * 16 + (lane >> 2), col = (lane & 3) * 8;
-        float v[8], w[8];
-        get(row, col, v);
-        get(row, 32 + col, w);
-        f(i * 32 + row, col, v, w);
-      }
-    } else {
-      constexpr int kL = kCols / 8;   // lanes a row
+        for (int t = 0; t < 4; ++t) {
+          v[t] = x[t];
+          v[4 + t] = y[t];
+        }
+      };
+      if constexpr (kPair) {
 #pragma unroll
-      for (int t = 0; t < kL / 2; ++t) {
-        const int row = t * (64 / kL) + lane / kL, col = (lane % kL) * 8;
-        float v[8];
-        get(row, col, v);
-        f(i * 32 + row, col, v);
+        for (int t = 0; t < 2; ++t) {
+          const int row = t * 16 + (lane >> 2), col = (lane & 3) * 8;
+          float v[8], w[8];
+          get(row, col, v);
+          get(row, 32 + col, w);
+          f(i * 32 + row, j0 * 16 + col, v, w);
+        }
+      } else {
+        constexpr int kL = kCols / 8;   // lanes a row
+#pragma unroll
+        for (int t = 0; t < kL / 2; ++t) {
+          const int row = t * (64 / kL) + lane / kL, col = (lane % kL) * 8;
+          float v[8];
+          get(row, col, v);
+          f(i * 32 + row, j0 * 32 + col, v);
+        }
       }
     }
-  }
 }
 
 }  // namespace moe
