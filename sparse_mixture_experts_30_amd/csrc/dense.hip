@@ -13,6 +13,8 @@
 #include "gemm_device.hpp"
 #include "rows_device.hpp"
 
+#include <stdlib.h>
+#include <stdio.h>
 #include <algorithm>
 
 namespace moe {
@@ -30,112 +32,243 @@ struct DenseArgs {
   uint16_t* c;           // EPI_STORE: [M, N]; else h [M, I] (may be null)
   uint16_t* gu;          // [M, 2 I]: written (EPI_SWIGLU; may be null) or read (EPI_DSWIGLU)
   uint16_t* da;          // EPI_DSWIGLU: [M, 2 I]
-  int mt, nt;
+  float* part;           // sums of each k range [splits][M][N, EPI_SWIGLU: 2 N]
+  int mt, nt, splits;
 };
 
-// Tile of workgroup b.  Each XCD takes one contiguous part of the tiles, in
-// groups of kGroupM tiles down by all across, column by column: the 32
+// What becomes of eight neighbouring sums (EPI_SWIGLU: of g and of u) from
+// (row, col) on.
+__device__ __forceinline__ void epi_store(const DenseArgs& p, int64_t row, int64_t col,
+                                          const float (&v)[8]) {
+  *reinterpret_cast<u32x4*>(p.c + row * p.N + col) = pack_bf16x8(v);
+}
+__device__ __forceinline__ void epi_swiglu(const DenseArgs& p, int64_t row, int64_t col,
+                                           const float (&g)[8], const float (&u)[8]) {
+  if (p.gu) {
+    uint16_t* o = p.gu + row * 2 * p.N + col;
+    *reinterpret_cast<u32x4*>(o) = pack_bf16x8(g);
+    *reinterpret_cast<u32x4*>(o + p.N) = pack_bf16x8(u);
+  }
+  if (p.c) {
+    float h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = g[j] / (1.0f + __expf(-g[j])) * u[j];
+    *reinterpret_cast<u32x4*>(p.c + row * p.N + col) = pack_bf16x8(h);
+  }
+}
+__device__ __forceinline__ u32x4 load_gu(const DenseArgs& p, int64_t row, int64_t col) {
+  return *reinterpret_cast<const u32x4*>(p.gu + row * 2 * p.N + col);
+}
+__device__ __forceinline__ void epi_dswiglu(const DenseArgs& p, int64_t row, int64_t col,
+                                            const float (&dh)[8], u32x4 g16, u32x4 u16) {
+  float g[8], u[8], dg[8], du[8], h[8];
+  unpack_bf16x8(g16, g);
+  unpack_bf16x8(u16, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float s = 1.0f / (1.0f + __expf(-g[j])), gs = g[j] * s;
+    dg[j] = dh[j] * u[j] * (s + gs * (1.0f - s));
+    du[j] = dh[j] * gs;
+    h[j] = gs * u[j];
+  }
+  uint16_t* dp = p.da + row * 2 * p.N + col;
+  *reinterpret_cast<u32x4*>(dp) = pack_bf16x8(dg);
+  *reinterpret_cast<u32x4*>(dp + p.N) = pack_bf16x8(du);
+  *reinterpret_cast<u32x4*>(p.c + row * p.N + col) = pack_bf16x8(h);
+}
+
+// Tile and k range of workgroup b.  Each XCD takes one contiguous part of the
+// tiles, in groups of kGroupM tiles down by all across, column by column: the 32
 // workgroups that run on an XCD together are then 8 x 4 tiles that share
 // operands in its L2.
 constexpr int kGroupM = 8;
-__device__ __forceinline__ bool tile_of(const DenseArgs& p, int& m, int& n) {
+__device__ __forceinline__ bool tile_of(const DenseArgs& p, int& m, int& n, int& split) {
   const int w = xcd_contiguous((int)blockIdx.x, (int)gridDim.x);
-  if (w >= p.mt * p.nt) return false;
-  const int per = kGroupM * p.nt, g = w / per, l = w % per;
+  const int tiles = p.mt * p.nt;
+  if (w >= tiles * p.splits) return false;
+  split = w / tiles;
+  const int t = w - split * tiles;
+  const int per = kGroupM * p.nt, g = t / per, l = t % per;
   const int rows = min(p.mt - g * kGroupM, kGroupM);
   m = g * kGroupM + l % rows;
   n = l / rows;
   return true;
 }
 
-template <int kM, int kN, int kWM, int kWN, int kOpA, int kOpB, int kEpi>
-__global__ void __launch_bounds__(64 * kWM * kWN, kWM * kWN / 4)
-dense_gemm(DenseArgs p) {
-  typedef GemmTile<kM, kN, kWM, kWN, kOpA, kOpB> Tile;
-  __shared__ u32x4 lds[4 * Tile::kStage];
-  int m, n;
-  if (!tile_of(p, m, n)) return;
+template <int kM, int kN, int kWM, int kWN, int kStages, int kOpA, int kOpB, int kEpi>
+__global__ void __launch_bounds__(64 * kWM * kWN, 2) dense_gemm(DenseArgs p) {
+  typedef GemmTile<kM, kN, kWM, kWN, kStages, kOpA, kOpB> Tile;
+  __shared__ u32x4 lds[kStages * Tile::kStage];
+  int m, n, split;
+  if (!tile_of(p, m, n, split)) return;
   constexpr int kNh = kEpi == EPI_SWIGLU ? kN / 2 : kN;   // output columns of a tile
   const int64_t m0 = (int64_t)m * kM, n0 = (int64_t)n * kNh;
   Operand A, B;
   A.ld = p.lda;
   B.ld = p.ldb;
-  A.p[0] = A.p[1] = kOpA == OP_COL ? p.a : p.a + m0 * p.lda;
+  A.to2 = 0;
+  A.p = kOpA == OP_COL ? p.a : p.a + m0 * p.lda;
   A.rows = kOpA == OP_COL ? p.K : p.M - m0;
   if (kOpB == OP_COL) {
-    B.p[0] = B.p[1] = p.b;
+    B.p = p.b;
+    B.to2 = 0;
     B.rows = p.K;
   } else {
-    B.p[0] = p.b + n0 * p.ldb;
-    B.p[1] = B.p[0] + p.N * p.ldb;
+    B.p = p.b + n0 * p.ldb;
+    B.to2 = p.N * p.ldb;
     B.rows = p.N - n0;
   }
+  const int steps = (int)((p.K + kGemmBK - 1) / kGemmBK);
   f32x16 acc[Tile::kMI][Tile::kNJ];
-  Tile::run(lds, A, (int)m0, B, (int)n0, p.K, acc);
+  Tile::run(lds, A, (int)m0, B, (int)n0, (int)((int64_t)steps * split / p.splits),
+            (int)((int64_t)steps * (split + 1) / p.splits), acc);
 
   // The operands are read for the last time: the waves share their LDS out.
   const int w = Tile::wave();
   float* l = reinterpret_cast<float*>(lds) + w * (32 * (Tile::kNJ == 1 ? 32 : 64));
   const int64_t row0 = m0 + Tile::row0(w);
   const int64_t col0 = n0 + (kEpi == EPI_SWIGLU ? Tile::col0(w) / 2 : Tile::col0(w));
-  if constexpr (kEpi == EPI_STORE) {
-    wave_rows<false>(l, acc, [&](int r, int c, const float (&v)[8]) {
-      const int64_t row = row0 + r, col = col0 + c;
-      if (row < p.M && col < p.N) *reinterpret_cast<u32x4*>(p.c + row * p.N + col) = pack_bf16x8(v);
-    });
-  } else if constexpr (kEpi == EPI_SWIGLU) {
+  auto keep = [&](int64_t at, const float (&v)[8]) {
+    f32x4* o = reinterpret_cast<f32x4*>(p.part + at);
+    o[0] = (f32x4){v[0], v[1], v[2], v[3]};
+    o[1] = (f32x4){v[4], v[5], v[6], v[7]};
+  };
+  if constexpr (kEpi == EPI_SWIGLU) {
     wave_rows<true>(l, acc, [&](int r, int c, const float (&g)[8], const float (&u)[8]) {
       const int64_t row = row0 + r, col = col0 + c;
       if (row >= p.M || col >= p.N) return;
-      if (p.gu) {
-        *reinterpret_cast<u32x4*>(p.gu + row * 2 * p.N + col) = pack_bf16x8(g);
-        *reinterpret_cast<u32x4*>(p.gu + row * 2 * p.N + p.N + col) = pack_bf16x8(u);
-      }
-      if (p.c) {
-        float h[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = g[j] / (1.0f + __expf(-g[j])) * u[j];
-        *reinterpret_cast<u32x4*>(p.c + row * p.N + col) = pack_bf16x8(h);
+      if (p.splits > 1) {
+        const int64_t at = (split * p.M + row) * 2 * p.N + col;
+        keep(at, g);
+        keep(at + p.N, u);
+      } else {
+        epi_swiglu(p, row, col, g, u);
       }
     });
-  } else {
-    wave_rows<false>(l, acc, [&](int r, int c, const float (&dh)[8]) {
+  } else if (kEpi == EPI_STORE || p.splits > 1) {
+    wave_rows<false>(l, acc, [&](int r, int c, const float (&v)[8]) {
       const int64_t row = row0 + r, col = col0 + c;
       if (row >= p.M || col >= p.N) return;
-      const uint16_t* gp = p.gu + row * 2 * p.N + col;
-      float g[8], u[8], dg[8], du[8], h[8];
-      unpack_bf16x8(*reinterpret_cast<const u32x4*>(gp), g);
-      unpack_bf16x8(*reinterpret_cast<const u32x4*>(gp + p.N), u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = 1.0f / (1.0f + __expf(-g[j])), gs = g[j] * s;
-        dg[j] = dh[j] * u[j] * (s + gs * (1.0f - s));
-        du[j] = dh[j] * gs;
-        h[j] = gs * u[j];
-      }
-      uint16_t* dp = p.da + row * 2 * p.N + col;
-      *reinterpret_cast<u32x4*>(dp) = pack_bf16x8(dg);
-      *reinterpret_cast<u32x4*>(dp + p.N) = pack_bf16x8(du);
-      *reinterpret_cast<u32x4*>(p.c + row * p.N + col) = pack_bf16x8(h);
+      if (p.splits > 1) keep((split * p.M + row) * p.N + col, v);
+      else epi_store(p, row, col, v);
     });
+  } else {
+    // g and u of 32 rows are loaded together, while the 32 before are worked on:
+    // one by one they would each wait for memory.  Past the edge the last value
+    // again.
+    static_assert(kEpi != EPI_DSWIGLU || Tile::kNJ == 2, "rows of 64 columns a wave");
+    const int lane = threadIdx.x & 63;
+    u32x4 g[2][4], u[2][4];
+    auto ahead = [&](int i) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int64_t row = min(row0 + i * 32 + t * 8 + (lane >> 3), p.M - 1),
+                      col = min(col0 + (lane & 7) * 8, p.N - 8);
+        g[i & 1][t] = load_gu(p, row, col);
+        u[i & 1][t] = load_gu(p, row, p.N + col);
+      }
+    };
+    ahead(0);
+#pragma unroll
+    for (int i = 0; i < Tile::kMI; ++i) {
+      if (i + 1 < Tile::kMI) ahead(i + 1);
+      int t = 0;
+      f32x16(&block)[1][Tile::kNJ] = reinterpret_cast<f32x16(&)[1][Tile::kNJ]>(acc[i]);
+      wave_rows<false>(l, block, [&](int r, int c, const float (&v)[8]) {
+        const int64_t row = row0 + i * 32 + r, col = col0 + c;
+        if (row < p.M && col < p.N) epi_dswiglu(p, row, col, v, g[i & 1][t], u[i & 1][t]);
+        ++t;
+      });
+    }
   }
+}
+
+// The k ranges' sums joined in their order, eight columns a thread.
+template <int kEpi>
+__global__ void __launch_bounds__(256) dense_join(DenseArgs p) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= p.M * p.N) return;
+  const int64_t row = i / p.N, col = i % p.N;
+  constexpr int kParts = kEpi == EPI_SWIGLU ? 2 : 1;
+  const int64_t all = p.M * p.N * kParts;
+  float v[kParts][8];
+#pragma unroll
+  for (int h = 0; h < kParts; ++h) {
+    const float* src = p.part + (row * kParts + h) * p.N + col;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    for (int s = 0; s < p.splits; ++s) {
+      a += *reinterpret_cast<const f32x4*>(src + s * all);
+      b += *reinterpret_cast<const f32x4*>(src + s * all + 4);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[h][j] = a[j];
+      v[h][4 + j] = b[j];
+    }
+  }
+  if constexpr (kEpi == EPI_SWIGLU) epi_swiglu(p, row, col, v[0], v[1]);
+  else if constexpr (kEpi == EPI_STORE) epi_store(p, row, col, v[0]);
+  else epi_dswiglu(p, row, col, v[0], load_gu(p, row, col), load_gu(p, row, p.N + col));
+}
+
+// Tile edge and k ranges of an M x n product (n columns of B's rows, so 2 I for
+// the gate and up projections) over K.
+struct Plan {
+  int edge, splits;
+};
+Plan plan_of(int64_t M, int64_t n, int64_t K) {
+  const int64_t steps = (K + kGemmBK - 1) / kGemmBK;
+  Plan q{256, 1};
+  if (getenv("DP")) { sscanf(getenv("DP"), "%d,%d", &q.edge, &q.splits);  }
+  // No range without a step; no ranges (and no workspace) without k.
+  q.splits = (int)std::max<int64_t>(1, std::min<int64_t>(q.splits, steps));
+  return q;
+}
+size_t part_bytes(int64_t M, int64_t n, int64_t K) {
+  const Plan q = plan_of(M, n, K);
+  return q.splits > 1 ? (size_t)q.splits * M * n * 4 : 0;
+}
+
+template <int kEdge, int kStages, int kOpA, int kOpB, int kEpi>
+void launch_tiles(const DenseArgs& a, unsigned grid, const char* name, hipStream_t s) {
+  constexpr int kWN = kEdge == 256 ? 4 : 2;
+  MOE_TIMED_LAUNCH(s, name,
+    hipLaunchKernelGGL((dense_gemm<kEdge, kEdge, 2, kWN, kStages, kOpA, kOpB, kEpi>), dim3(grid),
+                       dim3(128 * kWN), 0, s, a));
 }
 
 template <int kOpA, int kOpB, int kEpi>
 hipError_t launch_gemm(DenseArgs a, const char* name, hipStream_t s) {
-  constexpr int kM = 256, kN = 256, kWM = 2, kWN = 4, kH = kEpi == EPI_SWIGLU ? kN / 2 : kN;
-  a.mt = (int)((a.M + kM - 1) / kM);
-  a.nt = (int)((a.N + kH - 1) / kH);
-  const int64_t work = (int64_t)a.mt * a.nt;
+  const int64_t n = kEpi == EPI_SWIGLU ? 2 * a.N : a.N;
+  const Plan q = plan_of(a.M, n, a.K);
+  const int ed = q.edge & ~1;
+  a.mt = (int)((a.M + ed - 1) / ed);
+  a.nt = (int)((n + ed - 1) / ed);
+  a.splits = q.splits;
+  const int64_t work = (int64_t)a.mt * a.nt * a.splits;
   if (work == 0) return hipSuccess;
   const unsigned grid = (unsigned)((work + kNumXcd - 1) / kNumXcd * kNumXcd);
-  MOE_TIMED_LAUNCH(s, name,
-    hipLaunchKernelGGL((dense_gemm<kM, kN, kWM, kWN, kOpA, kOpB, kEpi>), dim3(grid), dim3(64 * kWM * kWN), 0, s,
-                       a));
+  if (q.edge == 256) launch_tiles<256, 4, kOpA, kOpB, kEpi>(a, grid, name, s);
+  else if (q.edge == 129) launch_tiles<128, 8, kOpA, kOpB, kEpi>(a, grid, name, s);
+  else launch_tiles<128, 4, kOpA, kOpB, kEpi>(a, grid, name, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  MOE_TIMED_LAUNCH(s, "dense_join",
+    hipLaunchKernelGGL(dense_join<kEpi>, dim3((unsigned)((a.M * a.N / 8 + 255) / 256)), dim3(256),
+                       0, s, a));
   return hipGetLastError();
 }
 
 }  // namespace
+
+size_t dense_part_bytes(int64_t T, int64_t H, int64_t I, bool backward) {
+  size_t b = part_bytes(T, 2 * I, H);
+  if (!backward) return std::max(b, part_bytes(T, H, I));
+  b = std::max(b, part_bytes(T, I, H));
+  b = std::max(b, part_bytes(T, H, 2 * I));
+  b = std::max(b, part_bytes(2 * I, H, T));
+  return std::max(b, part_bytes(H, I, T));
+}
 
 bool dense_fits(int64_t T, int64_t H, int64_t I) {
   // At most 2^23 tiles of 256 x 128 a product (a launch holds 2^32 threads), and
@@ -147,8 +280,9 @@ bool dense_fits(int64_t T, int64_t H, int64_t I) {
 }
 
 hipError_t launch_dense_gate_up(const uint16_t* x, const uint16_t* w13, int64_t T, int H, int I,
-                                uint16_t* gu, uint16_t* h, hipStream_t s) {
+                                uint16_t* gu, uint16_t* h, float* part, hipStream_t s) {
   DenseArgs a{};
+  a.part = part;
   a.a = (const char*)x;
   a.lda = (int64_t)H * 2;
   a.b = (const char*)w13;
@@ -162,8 +296,9 @@ hipError_t launch_dense_gate_up(const uint16_t* x, const uint16_t* w13, int64_t 
 }
 
 hipError_t launch_dense_down(const uint16_t* h, const uint16_t* w2, int64_t T, int H, int I,
-                             uint16_t* y, hipStream_t s) {
+                             uint16_t* y, float* part, hipStream_t s) {
   DenseArgs a{};
+  a.part = part;
   a.a = (const char*)h;
   a.lda = (int64_t)I * 2;
   a.b = (const char*)w2;
@@ -178,9 +313,10 @@ hipError_t launch_dense_down(const uint16_t* h, const uint16_t* w2, int64_t T, i
 hipError_t launch_dense_backward(const uint16_t* x, const uint16_t* w13, const uint16_t* w2,
                                  const uint16_t* gu, const uint16_t* dy, int64_t T, int H, int I,
                                  uint16_t* da, uint16_t* h, uint16_t* dx, uint16_t* dw13,
-                                 uint16_t* dw2, hipStream_t s) {
+                                 uint16_t* dw2, float* part, hipStream_t s) {
   const int64_t rh = (int64_t)H * 2, ri = (int64_t)I * 2;   // bytes of rows of H and I
   DenseArgs a{};
+  a.part = part;
   a.a = (const char*)dy;
   a.lda = rh;
   a.b = (const char*)w2;
@@ -195,6 +331,7 @@ hipError_t launch_dense_backward(const uint16_t* x, const uint16_t* w13, const u
   if (e != hipSuccess) return e;
 
   a = DenseArgs{};
+  a.part = part;
   a.a = (const char*)da;
   a.lda = 2 * ri;
   a.b = (const char*)x;
@@ -207,6 +344,7 @@ hipError_t launch_dense_backward(const uint16_t* x, const uint16_t* w13, const u
   if (e != hipSuccess) return e;
 
   a = DenseArgs{};
+  a.part = part;
   a.a = (const char*)dy;
   a.lda = rh;
   a.b = (const char*)h;
@@ -220,6 +358,7 @@ hipError_t launch_dense_backward(const uint16_t* x, const uint16_t* w13, const u
 
   // Last: dx may be dy.
   a = DenseArgs{};
+  a.part = part;
   a.a = (const char*)da;
   a.lda = 2 * ri;
   a.b = (const char*)w13;

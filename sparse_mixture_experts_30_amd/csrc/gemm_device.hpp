@@ -4,7 +4,7 @@
 // A[k][m], B[k][n]), so that the products of a feed-forward block and of its
 // backward need no transposed copies.
 //
-// Tile kM x kN, k in steps of 32 through four LDS stages that loads from memory
+// Tile kM x kN, k in steps of 32 through four or more LDS stages that loads from memory
 // fill directly.  A row operand's step is [row][32 k] in four 16-byte chunks,
 // chunk c of row r at c ^ ((r >> 1 ^ r >> 3) & 3); a col operand's is [32 k][row], the
 // 32-byte piece s of k row k at s ^ f(k), f = (k & 3) ^ (k & 3) << 1, and is
@@ -12,10 +12,10 @@
 // group of 16 lanes.  Either way the lanes that read together fall in different
 // banks.
 //
-// At the start of step s the stages of s and s + 1 are filled, s + 2 is under
-// way and s + 3 is started into the stage that step s - 1 has read.  Each half
-// of a step's MFMAs runs while the operands of the next half are read, across
-// the barrier too: the matrix cores wait for neither memory nor LDS.
+// In the middle of step s the stage of s + 1 is filled, the next ones are under
+// way and one more load is started into the stage that step s - 1 has read.
+// Each half of a step's MFMAs runs while the operands of the next half are
+// read, across the barrier too.
 //
 // Loads go through buffer descriptors that end at the operand's last valid
 // row (row operand) or last valid k (col operand): what lies past it arrives as
@@ -40,7 +40,8 @@ enum : int { OP_ROW = 0, OP_COL = 1, OP_GATE_UP = 2 };
 // of rows in bytes, and the valid rows.  OP_GATE_UP is a row operand whose row
 // blocks of 32 alternate between two matrices.
 struct Operand {
-  const char* p[2];
+  const char* p;
+  int64_t to2;    // OP_GATE_UP: from p to the same row of the second matrix
   int64_t ld;     // bytes
   int64_t rows;   // row operand: rows from p on; col operand: valid k
 };
@@ -105,34 +106,36 @@ struct Stager {
   static constexpr int kLoads = kRows * 4 / kThreads;   // 16-byte pieces a thread
   static constexpr int kPer = kRows / 8;                // pieces of a k row (col operand)
   static constexpr int kPass = kThreads / 4;            // rows a load (row operand)
-  const Operand& o;
-  int wave;
-  int at;   // this thread's offset of load 0, step 0
+  const char* p;
+  int64_t rows;
+  int ld, wave;
+  u32x4 fixed;   // row operand: the buffer of every step
+  int at;        // this thread's offset of load 0, step 0
 
-  __device__ __forceinline__ Stager(const Operand& op, int row0, int tid, int wave_)
-      : o(op), wave(wave_) {
+  __device__ __forceinline__ Stager(const Operand& o, int row0, int tid, int wave_)
+      : p(o.p), rows(o.rows), ld((int)o.ld), wave(wave_) {
+    if (kOp != OP_COL)   // 16 rows a wave: one matrix
+      fixed = buffer_of(kOp == OP_GATE_UP ? o.p + (wave >> 1 & 1) * o.to2 : o.p, o.rows * o.ld);
     if (kOp == OP_COL) {
       const int k = tid / kPer, c = tid % kPer;
-      at = (int)(k * o.ld) + (row0 + (col_piece<kRows>(k, c >> 1) * 2 + (c & 1)) * 8) * 2;
+      at = k * ld + (row0 + (col_piece<kRows>(k, c >> 1) * 2 + (c & 1)) * 8) * 2;
     } else {
       const int r = tid >> 2, c = row_swizzle(r, tid & 3);
       // gate / up: row blocks 2 i and 2 i + 1 of 32 are rows 32 i.. of the two
-      at = (int)((kOp == OP_GATE_UP ? (r & 31) + (r >> 6) * 32 : r) * o.ld) + c * 16;
+      at = (kOp == OP_GATE_UP ? (r & 31) + (r >> 6) * 32 : r) * ld + c * 16;
     }
   }
   __device__ __forceinline__ u32x4 buffer(int step) const {
-    if (kOp == OP_COL)
-      return buffer_of(o.p[0] + (int64_t)step * kGemmBK * o.ld,
-                       (o.rows - (int64_t)step * kGemmBK) * o.ld);
-    // 16 rows a wave: one matrix
-    return buffer_of(kOp == OP_GATE_UP && (wave >> 1 & 1) ? o.p[1] : o.p[0], o.rows * o.ld);
+    if (kOp != OP_COL) return fixed;
+    const int64_t k = (int64_t)step * kGemmBK;
+    return buffer_of(p + k * ld, (rows - k) * ld);
   }
   // Starts load j of k step `step` into the operand's place of a stage.
   __device__ __forceinline__ void load(u32x4 buf, uint32_t lds, int step, int j) const {
     // k rows kThreads / kPer apart, a multiple of 4; or rows kPass apart
-    const int off = kOp == OP_COL        ? j * (kThreads / kPer) * (int)o.ld
-                    : kOp == OP_GATE_UP ? j * (kPass / 2) * (int)o.ld + step * (kGemmBK * 2)
-                                         : j * kPass * (int)o.ld + step * (kGemmBK * 2);
+    const int off = kOp == OP_COL        ? j * (kThreads / kPer) * ld
+                    : kOp == OP_GATE_UP ? j * (kPass / 2) * ld + step * (kGemmBK * 2)
+                                         : j * kPass * ld + step * (kGemmBK * 2);
     load_to_lds(buf, lds + (j * kThreads + wave * 64) * 16, at + off);
   }
 };
@@ -154,8 +157,8 @@ __device__ __forceinline__ bf16x8 fragment(const u32x4* lds, int row, int kk, in
 }
 
 // The tile's accumulators: wave (wm, wn) of kWM x kWN holds rows row0() + 32 i,
-// columns col0() + 32 j.  lds: four stages of kStage 16-byte pieces.
-template <int kM, int kN, int kWM, int kWN, int kOpA, int kOpB>
+// columns col0() + 32 j.  lds: kStages (a power of two) of kStage 16-byte pieces.
+template <int kM, int kN, int kWM, int kWN, int kStages, int kOpA, int kOpB>
 struct GemmTile {
   static constexpr int kThreads = 64 * kWM * kWN;
   static constexpr int kMI = kM / kWM / 32, kNJ = kN / kWN / 32;
@@ -165,8 +168,9 @@ struct GemmTile {
   static __device__ __forceinline__ int row0(int wave) { return wave / kWN * (kM / kWM); }
   static __device__ __forceinline__ int col0(int wave) { return wave % kWN * (kN / kWN); }
 
+  // Sums over k steps [s0, s1).
   static __device__ __forceinline__ void run(u32x4* lds, const Operand& A, int m0,
-                                             const Operand& B, int n0, int64_t K,
+                                             const Operand& B, int n0, int s0, int s1,
                                              f32x16 (&acc)[kMI][kNJ]) {
     const int tid = threadIdx.x, lane = tid & 63, w = wave();
     const int wrow = row0(w), wcol = col0(w);
@@ -174,14 +178,13 @@ struct GemmTile {
     const Stager<kOpA, kM, kThreads> sa(A, m0, tid, w);
     const Stager<kOpB, kN, kThreads> sb(B, n0, tid, w);
     constexpr int kLoads = sa.kLoads + sb.kLoads;
-    const int nsteps = (int)((K + kGemmBK - 1) / kGemmBK);
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
 #pragma unroll
       for (int j = 0; j < kNJ; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
-    if (nsteps == 0) return;
+    if (s0 >= s1) return;
 
     // Load i of a step, in [0, kLoads).
     auto load = [&](const u32x4& ba, const u32x4& bb, int stage, int step, int i) {
@@ -234,25 +237,21 @@ struct GemmTile {
     // Step s: stages s and (behind the barrier) s + 1 are there.
     auto step = [&](int stage, int s) {
       half(f0, f1, stage, 1, false, 0, 0);
-      wait_and_meet<kLoads>();   // step s + 1 is there, the stage of s - 1 is read
+      // step s + 1 is there, the stage of s - 1 is read
+      wait_and_meet<(kStages - 3) * kLoads>();
       __builtin_amdgcn_sched_barrier(0);
-      half(f1, f0, (stage + 1) & 3, 0, true, (stage + 3) & 3, s + 3);
+      half(f1, f0, (stage + 1) % kStages, 0, true, (stage + kStages - 1) % kStages,
+           s + kStages - 1);
     };
-    load_all(0, 0);
-    load_all(1, 1);
-    load_all(2, 2);
-    wait_and_meet<2 * kLoads>();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load_all(i, s0 + i);
+    wait_and_meet<(kStages - 2) * kLoads>();
 #pragma unroll
     for (int i = 0; i < kReads; ++i) read(f0, 0, 0, i);
-    for (int s = 0;;) {
-      step(0, s);
-      if (++s >= nsteps) break;
-      step(1, s);
-      if (++s >= nsteps) break;
-      step(2, s);
-      if (++s >= nsteps) break;
-      step(3, s);
-      if (++s >= nsteps) break;
+    for (int s = s0; s < s1;) {
+#pragma unroll
+      for (int i = 0; i < kStages; ++i)
+        if (s < s1) step(i, s++);
     }
     wait_and_meet<0>();   // the LDS is free
   }

@@ -593,16 +593,19 @@ Layout dense_layout(const moe_config* c, int64_t T) {
                  c->n_routed_experts, c->num_experts_per_tok};
   L.tiles = take(moe::ffn_tiles_bytes(d));
   ffn_segments(L, c, 0, T, take);
+  if (c->weight_dtype == MOE_BF16)
+    L.part = take(moe::dense_part_bytes(T, c->hidden_size, c->shared_intermediate_size, false));
   L.total = o;
   return L;
 }
 
 struct DenseBackwardLayout {
-  size_t gu, da, h, total;
+  size_t gu, da, h, part, total;
 };
 DenseBackwardLayout dense_backward_layout(const moe_config* c, int64_t T) {
   const size_t row = up((size_t)T * c->shared_intermediate_size * 2);
-  return {0, 2 * row, 4 * row, 5 * row};
+  return {0, 2 * row, 4 * row, 5 * row,
+          5 * row + up(moe::dense_part_bytes(T, c->hidden_size, c->shared_intermediate_size, true))};
 }
 
 // ---- gradients --------------------------------------------------------------
@@ -1224,9 +1227,10 @@ moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const 
   const int H = cfg->hidden_size, I = cfg->shared_intermediate_size;
   uint16_t* h = at<uint16_t>(ws, L.h);
   HIPCALL(moe::launch_dense_gate_up((const uint16_t*)x, (const uint16_t*)w->ws13, T, H, I,
-                                    (uint16_t*)gu, h, s),
+                                    (uint16_t*)gu, h, at<float>(ws, L.part), s),
           "dense gate/up");
-  HIPCALL(moe::launch_dense_down(h, (const uint16_t*)w->ws2, T, H, I, (uint16_t*)y, s),
+  HIPCALL(moe::launch_dense_down(h, (const uint16_t*)w->ws2, T, H, I, (uint16_t*)y,
+                                 at<float>(ws, L.part), s),
           "dense down");
   return MOE_OK;
 }
@@ -1271,14 +1275,14 @@ moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* 
   const uint16_t* g = (const uint16_t*)gu;
   if (T && !g) {   // computed again
     HIPCALL(moe::launch_dense_gate_up((const uint16_t*)x, (const uint16_t*)w->ws13, T, H, I,
-                                      at<uint16_t>(ws, L.gu), nullptr, s),
+                                      at<uint16_t>(ws, L.gu), nullptr, at<float>(ws, L.part), s),
             "dense gate/up");
     g = at<uint16_t>(ws, L.gu);
   }
   HIPCALL(moe::launch_dense_backward((const uint16_t*)x, (const uint16_t*)w->ws13,
                                      (const uint16_t*)w->ws2, g, (const uint16_t*)dy, T, H, I,
                                      at<uint16_t>(ws, L.da), at<uint16_t>(ws, L.h), (uint16_t*)dx,
-                                     (uint16_t*)dws13, (uint16_t*)dws2, s),
+                                     (uint16_t*)dws13, (uint16_t*)dws2, at<float>(ws, L.part), s),
           "dense backward");
   return MOE_OK;
 }
