@@ -248,9 +248,9 @@ hipError_t launch_gemm(DenseArgs a, const char* name, hipStream_t s) {
   const int64_t work = (int64_t)a.mt * a.nt * a.splits;
   if (work == 0) return hipSuccess;
   const unsigned grid = (unsigned)((work + kNumXcd - 1) / kNumXcd * kNumXcd);
-  if (q.edge == 256) launch_tiles<256, 4, kOpA, kOpB, kEpi>(a, grid, name, s);
-  else if (q.edge == 129) launch_tiles<128, 8, kOpA, kOpB, kEpi>(a, grid, name, s);
-  else launch_tiles<128, 4, kOpA, kOpB, kEpi>(a, grid, name, s);
+  if (q.edge == 256) launch_tiles<256, 2, kOpA, kOpB, kEpi>(a, grid, name, s);
+  else if (q.edge == 129) launch_tiles<128, 4, kOpA, kOpB, kEpi>(a, grid, name, s);
+  else launch_tiles<128, 2, kOpA, kOpB, kEpi>(a, grid, name, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   MOE_TIMED_LAUNCH(s, "dense_join",

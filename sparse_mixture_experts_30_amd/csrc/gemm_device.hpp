@@ -4,18 +4,22 @@
 // A[k][m], B[k][n]), so that the products of a feed-forward block and of its
 // backward need no transposed copies.
 //
-// Tile kM x kN, k in steps of 32 through four or more LDS stages that loads from memory
-// fill directly.  A row operand's step is [row][32 k] in four 16-byte chunks,
-// chunk c of row r at c ^ ((r >> 1 ^ r >> 3) & 3); a col operand's is [32 k][row], the
-// 32-byte piece s of k row k at s ^ f(k), f = (k & 3) ^ (k & 3) << 1, and is
+// Tile kM x kN, k in steps of 64 through two or more LDS stages that loads from
+// memory fill directly.  A row operand's step is [row][64 k] in eight 16-byte
+// chunks, chunk c of row r at c ^ (r & 7) ^ (r >> 3 & 3); a col operand's is [64 k][row],
+// the 32-byte piece s of k row k at s ^ f(k), f = (k & 3) ^ (k & 3) << 1, and is
 // transposed by the LDS's 16-bit transposing read: four k rows of 16 values a
 // group of 16 lanes.  Either way the lanes that read together fall in different
-// banks.
+// banks, and every load takes whole 128-byte lines (steps of 32, half a line of
+// a row operand a load, took 14% longer where both operands are rows).
 //
-// In the middle of step s the stage of s + 1 is filled, the next ones are under
-// way and one more load is started into the stage that step s - 1 has read.
-// Each half of a step's MFMAs runs while the operands of the next half are
-// read, across the barrier too.
+// A step's MFMAs come in four slices of 16 k.  Each runs while the operands of
+// the next are read from LDS, across steps too.  Before a step's last slice its
+// stage has been read for good and the next one has to be there: the waves
+// meet, and among the last slice's MFMAs the stage's next loads are started.
+// A wave alone on its SIMD would have no issue slots for this beside its MFMAs
+// of a 256 x 256 tile's quarter (and its registers do not hold it): eight
+// waves of 128 x 64.
 //
 // Loads go through buffer descriptors that end at the operand's last valid
 // row (row operand) or last valid k (col operand): what lies past it arrives as
@@ -31,7 +35,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kGemmBK = 32;
+constexpr int kGemmBK = 64;
 
 enum : int { OP_ROW = 0, OP_COL = 1, OP_GATE_UP = 2 };
 
@@ -93,8 +97,8 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
-__device__ __forceinline__ int row_swizzle(int r, int c) { return c ^ ((r >> 1 ^ r >> 3) & 3); }
-__device__ __forceinline__ int row_chunk(int r, int c) { return r * 4 + row_swizzle(r, c); }
+__device__ __forceinline__ int row_swizzle(int r, int c) { return c ^ (r & 7) ^ (r >> 3 & 3); }
+__device__ __forceinline__ int row_chunk(int r, int c) { return r * 8 + row_swizzle(r, c); }
 template <int kRows>
 __device__ __forceinline__ int col_piece(int k, int s) {
   return s ^ (((k & 3) ^ ((k & 3) << 1)) & (kRows / 16 - 1));
@@ -103,26 +107,30 @@ __device__ __forceinline__ int col_piece(int k, int s) {
 // Stages one operand of kRows rows with kThreads threads.
 template <int kOp, int kRows, int kThreads>
 struct Stager {
-  static constexpr int kLoads = kRows * 4 / kThreads;   // 16-byte pieces a thread
+  static constexpr int kLoads = kRows * 8 / kThreads;   // 16-byte pieces a thread
   static constexpr int kPer = kRows / 8;                // pieces of a k row (col operand)
-  static constexpr int kPass = kThreads / 4;            // rows a load (row operand)
+  static constexpr int kPass = kThreads / 8;            // rows a load (row operand)
   const char* p;
   int64_t rows;
   int ld, wave;
-  u32x4 fixed;   // row operand: the buffer of every step
+  u32x4 fixed, second;   // row operand: the buffer of every step
   int at;        // this thread's offset of load 0, step 0
 
   __device__ __forceinline__ Stager(const Operand& o, int row0, int tid, int wave_)
       : p(o.p), rows(o.rows), ld((int)o.ld), wave(wave_) {
-    if (kOp != OP_COL)   // 16 rows a wave: one matrix
-      fixed = buffer_of(kOp == OP_GATE_UP ? o.p + (wave >> 1 & 1) * o.to2 : o.p, o.rows * o.ld);
+    // Gate / up: 32-row blocks 2 i and 2 i + 1 are rows 32 i.. of the two matrices; a
+    // wave's 8 rows of a load are of one of them, the same in every load of 64
+    // rows (of 32 rows: in every second load, see load).
+    if (kOp != OP_COL)
+      fixed = buffer_of(kOp == OP_GATE_UP && kPass == 64 ? o.p + (wave >> 2 & 1) * o.to2 : o.p,
+                        o.rows * o.ld);
+    if (kOp == OP_GATE_UP && kPass == 32) second = buffer_of(o.p + o.to2, o.rows * o.ld);
     if (kOp == OP_COL) {
       const int k = tid / kPer, c = tid % kPer;
       at = k * ld + (row0 + (col_piece<kRows>(k, c >> 1) * 2 + (c & 1)) * 8) * 2;
     } else {
-      const int r = tid >> 2, c = row_swizzle(r, tid & 3);
-      // gate / up: row blocks 2 i and 2 i + 1 of 32 are rows 32 i.. of the two
-      at = (kOp == OP_GATE_UP ? (r & 31) + (r >> 6) * 32 : r) * ld + c * 16;
+      const int r = tid >> 3, c = row_swizzle(r, tid & 7);
+      at = (kOp == OP_GATE_UP ? r & 31 : r) * ld + c * 16;
     }
   }
   __device__ __forceinline__ u32x4 buffer(int step) const {
@@ -134,9 +142,10 @@ struct Stager {
   __device__ __forceinline__ void load(u32x4 buf, uint32_t lds, int step, int j) const {
     // k rows kThreads / kPer apart, a multiple of 4; or rows kPass apart
     const int off = kOp == OP_COL        ? j * (kThreads / kPer) * ld
-                    : kOp == OP_GATE_UP ? j * (kPass / 2) * ld + step * (kGemmBK * 2)
+                    : kOp == OP_GATE_UP ? j * kPass / 64 * 32 * ld + step * (kGemmBK * 2)
                                          : j * kPass * ld + step * (kGemmBK * 2);
-    load_to_lds(buf, lds + (j * kThreads + wave * 64) * 16, at + off);
+    static_assert(kOp != OP_GATE_UP || kPass == 32 || kPass == 64, "rows a load");
+    load_to_lds(kOp == OP_GATE_UP && kPass == 32 && (j & 1) ? second : buf, lds + (j * kThreads + wave * 64) * 16, at + off);
   }
 };
 
@@ -157,12 +166,12 @@ __device__ __forceinline__ bf16x8 fragment(const u32x4* lds, int row, int kk, in
 }
 
 // The tile's accumulators: wave (wm, wn) of kWM x kWN holds rows row0() + 32 i,
-// columns col0() + 32 j.  lds: kStages (a power of two) of kStage 16-byte pieces.
+// columns col0() + 32 j.  lds: kStages of kStage 16-byte pieces.
 template <int kM, int kN, int kWM, int kWN, int kStages, int kOpA, int kOpB>
 struct GemmTile {
   static constexpr int kThreads = 64 * kWM * kWN;
   static constexpr int kMI = kM / kWM / 32, kNJ = kN / kWN / 32;
-  static constexpr int kStage = (kM + kN) * 4;
+  static constexpr int kStage = (kM + kN) * 8;
 
   static __device__ __forceinline__ int wave() { return (int)scalar(threadIdx.x >> 6); }
   static __device__ __forceinline__ int row0(int wave) { return wave / kWN * (kM / kWM); }
@@ -190,40 +199,39 @@ struct GemmTile {
     auto load = [&](const u32x4& ba, const u32x4& bb, int stage, int step, int i) {
       const uint32_t at = lds_at + stage * (kStage * 16);
       if (i < sa.kLoads) sa.load(ba, at, step, i);
-      else sb.load(bb, at + kM * 64, step, i - sa.kLoads);
+      else sb.load(bb, at + kM * 128, step, i - sa.kLoads);
     };
     auto load_all = [&](int stage, int step) {
       const u32x4 ba = sa.buffer(step), bb = sb.buffer(step);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) load(ba, bb, stage, step, i);
     };
-    struct Half {
+    struct Slice {
       bf16x8 a[kMI], b[kNJ];
     };
-    // Operand i of half kk of a stage, in [0, kMI + kNJ): b[0], a[0], b[1], the rest.
-    constexpr int kReads = kMI + kNJ;
-    auto read = [&](Half& f, int stage, int kk, int i) {
+    // Operand i of slice kk of a stage, in [0, kMI + kNJ): b[0], a[0], b[1], the rest.
+    constexpr int kReads = kMI + kNJ, kMfma = kMI * kNJ;
+    auto read = [&](Slice& f, int stage, int kk, int i) {
       const u32x4* l = lds + stage * kStage;
       if (i == 0 || (i >= 2 && i <= kNJ))
         f.b[i == 0 ? 0 : i - 1] =
-            fragment<kOpB, kN>(l + kM * 4, wcol + (i == 0 ? 0 : i - 1) * 32, kk, lane);
+            fragment<kOpB, kN>(l + kM * 8, wcol + (i == 0 ? 0 : i - 1) * 32, kk, lane);
       else
         f.a[i == 1 ? 0 : i - kNJ] =
             fragment<kOpA, kM>(l, wrow + (i == 1 ? 0 : i - kNJ) * 32, kk, lane);
     };
-    // A half step's MFMAs, and between them the reads of the next half step's
-    // operands and the loads of a later step.
-    auto half = [&](const Half& f, Half& next, int stage, int kk, bool loads, int to, int step) {
+    // A slice's MFMAs, and between them the reads of the next slice's operands
+    // and, with `loads`, the loads of a later step.
+    auto slice = [&](const Slice& f, Slice& next, int stage, int kk, bool loads, int to, int step) {
       u32x4 ba, bb;
       if (loads) {
         ba = sa.buffer(step);
         bb = sb.buffer(step);
       }
 #pragma unroll
-      for (int q = 0; q < kMI * kNJ; ++q) {
+      for (int q = 0; q < kMfma; ++q) {
         const int i = q / kNJ, j = q % kNJ;
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
-        constexpr int kMfma = kMI * kNJ;
 #pragma unroll
         for (int r = q; r < kReads; r += kMfma) read(next, stage, kk, r);
         if (loads) {
@@ -233,19 +241,18 @@ struct GemmTile {
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    Half f0, f1;
-    // Step s: stages s and (behind the barrier) s + 1 are there.
+    Slice f0, f1;
     auto step = [&](int stage, int s) {
-      half(f0, f1, stage, 1, false, 0, 0);
-      // step s + 1 is there, the stage of s - 1 is read
-      wait_and_meet<(kStages - 3) * kLoads>();
+      slice(f0, f1, stage, 1, false, 0, 0);
+      slice(f1, f0, stage, 2, false, 0, 0);
+      slice(f0, f1, stage, 3, false, 0, 0);
+      wait_and_meet<(kStages - 2) * kLoads>();   // step s + 1 is there, s is read
       __builtin_amdgcn_sched_barrier(0);
-      half(f1, f0, (stage + 1) % kStages, 0, true, (stage + kStages - 1) % kStages,
-           s + kStages - 1);
+      slice(f1, f0, (stage + 1) % kStages, 0, true, stage, s + kStages);
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) load_all(i, s0 + i);
-    wait_and_meet<(kStages - 2) * kLoads>();
+    for (int i = 0; i < kStages; ++i) load_all(i, s0 + i);
+    wait_and_meet<(kStages - 1) * kLoads>();
 #pragma unroll
     for (int i = 0; i < kReads; ++i) read(f0, 0, 0, i);
     for (int s = s0; s < s1;) {
