@@ -95,10 +95,10 @@ __device__ __forceinline__ bool tile_of(const DenseArgs& p, int& m, int& n, int&
   return true;
 }
 
-template <int kM, int kN, int kWM, int kWN, int kStages, int kOpA, int kOpB, int kEpi>
+template <int kM, int kN, int kWM, int kWN, int kSA, int kSB, int kOpA, int kOpB, int kEpi>
 __global__ void __launch_bounds__(64 * kWM * kWN, 2) dense_gemm(DenseArgs p) {
-  typedef GemmTile<kM, kN, kWM, kWN, kStages, kOpA, kOpB> Tile;
-  __shared__ u32x4 lds[kStages * Tile::kStage];
+  typedef GemmTile<kM, kN, kWM, kWN, kSA, kSB, kOpA, kOpB> Tile;
+  __shared__ u32x4 lds[Tile::kPieces];
   int m, n, split;
   if (!tile_of(p, m, n, split)) return;
   constexpr int kNh = kEpi == EPI_SWIGLU ? kN / 2 : kN;   // output columns of a tile
@@ -229,11 +229,11 @@ size_t part_bytes(int64_t M, int64_t n, int64_t K) {
   return q.splits > 1 ? (size_t)q.splits * M * n * 4 : 0;
 }
 
-template <int kEdge, int kStages, int kOpA, int kOpB, int kEpi>
+template <int kEdge, int kSA, int kSB, int kOpA, int kOpB, int kEpi>
 void launch_tiles(const DenseArgs& a, unsigned grid, const char* name, hipStream_t s) {
   constexpr int kWN = kEdge == 256 ? 4 : 2;
   MOE_TIMED_LAUNCH(s, name,
-    hipLaunchKernelGGL((dense_gemm<kEdge, kEdge, 2, kWN, kStages, kOpA, kOpB, kEpi>), dim3(grid),
+    hipLaunchKernelGGL((dense_gemm<kEdge, kEdge, 2, kWN, kSA, kSB, kOpA, kOpB, kEpi>), dim3(grid),
                        dim3(128 * kWN), 0, s, a));
 }
 
@@ -248,9 +248,9 @@ hipError_t launch_gemm(DenseArgs a, const char* name, hipStream_t s) {
   const int64_t work = (int64_t)a.mt * a.nt * a.splits;
   if (work == 0) return hipSuccess;
   const unsigned grid = (unsigned)((work + kNumXcd - 1) / kNumXcd * kNumXcd);
-  if (q.edge == 256) launch_tiles<256, 2, kOpA, kOpB, kEpi>(a, grid, name, s);
-  else if (q.edge == 129) launch_tiles<128, 4, kOpA, kOpB, kEpi>(a, grid, name, s);
-  else launch_tiles<128, 2, kOpA, kOpB, kEpi>(a, grid, name, s);
+  if (q.edge == 256) launch_tiles<256, 3, 2, kOpA, kOpB, kEpi>(a, grid, name, s);
+  else if (q.edge == 129) launch_tiles<128, 4, 4, kOpA, kOpB, kEpi>(a, grid, name, s);
+  else launch_tiles<128, 3, 2, kOpA, kOpB, kEpi>(a, grid, name, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   MOE_TIMED_LAUNCH(s, "dense_join",

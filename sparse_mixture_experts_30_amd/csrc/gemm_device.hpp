@@ -166,12 +166,13 @@ __device__ __forceinline__ bf16x8 fragment(const u32x4* lds, int row, int kk, in
 }
 
 // The tile's accumulators: wave (wm, wn) of kWM x kWN holds rows row0() + 32 i,
-// columns col0() + 32 j.  lds: kStages of kStage 16-byte pieces.
-template <int kM, int kN, int kWM, int kWN, int kStages, int kOpA, int kOpB>
+// columns col0() + 32 j.  lds: kPieces 16-byte pieces, kSA stages of A (as many as
+// of B or one more), then kSB of B.
+template <int kM, int kN, int kWM, int kWN, int kSA, int kSB, int kOpA, int kOpB>
 struct GemmTile {
   static constexpr int kThreads = 64 * kWM * kWN;
   static constexpr int kMI = kM / kWM / 32, kNJ = kN / kWN / 32;
-  static constexpr int kStage = (kM + kN) * 8;
+  static constexpr int kPieces = kSA * kM * 8 + kSB * kN * 8;
 
   static __device__ __forceinline__ int wave() { return (int)scalar(threadIdx.x >> 6); }
   static __device__ __forceinline__ int row0(int wave) { return wave / kWN * (kM / kWM); }
@@ -186,7 +187,6 @@ struct GemmTile {
     const uint32_t lds_at = lds_address(lds);
     const Stager<kOpA, kM, kThreads> sa(A, m0, tid, w);
     const Stager<kOpB, kN, kThreads> sb(B, n0, tid, w);
-    constexpr int kLoads = sa.kLoads + sb.kLoads;
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
 #pragma unroll
@@ -195,69 +195,85 @@ struct GemmTile {
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
     if (s0 >= s1) return;
 
-    // Load i of a step, in [0, kLoads).
-    auto load = [&](const u32x4& ba, const u32x4& bb, int stage, int step, int i) {
-      const uint32_t at = lds_at + stage * (kStage * 16);
-      if (i < sa.kLoads) sa.load(ba, at, step, i);
-      else sb.load(bb, at + kM * 128, step, i - sa.kLoads);
+    // Loads of a step: B's (to stage sb), then A's (to stage sa).
+    const uint32_t lds_b = lds_at + kSA * kM * 128;
+    auto load_b = [&](const u32x4& bb, int stage, int step, int i) {
+      sb.load(bb, lds_b + stage * (kN * 128), step, i);
     };
-    auto load_all = [&](int stage, int step) {
-      const u32x4 ba = sa.buffer(step), bb = sb.buffer(step);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) load(ba, bb, stage, step, i);
+    auto load_a = [&](const u32x4& ba, int stage, int step, int i) {
+      sa.load(ba, lds_at + stage * (kM * 128), step, i);
     };
     struct Slice {
       bf16x8 a[kMI], b[kNJ];
     };
     // Operand i of slice kk of a stage, in [0, kMI + kNJ): b[0], a[0], b[1], the rest.
     constexpr int kReads = kMI + kNJ, kMfma = kMI * kNJ;
-    auto read = [&](Slice& f, int stage, int kk, int i) {
-      const u32x4* l = lds + stage * kStage;
+    constexpr int kPer = (sa.kLoads + sb.kLoads + kMfma - 1) / kMfma;   // loads an MFMA
+    auto read = [&](Slice& f, int s, int kk, int i) {   // s: the step, modulo the stages
+      const u32x4 *la = lds + s % kSA * (kM * 8), *lb = lds + (kSA * kM + s % kSB * kN) * 8;
       if (i == 0 || (i >= 2 && i <= kNJ))
         f.b[i == 0 ? 0 : i - 1] =
-            fragment<kOpB, kN>(l + kM * 8, wcol + (i == 0 ? 0 : i - 1) * 32, kk, lane);
+            fragment<kOpB, kN>(lb, wcol + (i == 0 ? 0 : i - 1) * 32, kk, lane);
       else
         f.a[i == 1 ? 0 : i - kNJ] =
-            fragment<kOpA, kM>(l, wrow + (i == 1 ? 0 : i - kNJ) * 32, kk, lane);
+            fragment<kOpA, kM>(la, wrow + (i == 1 ? 0 : i - kNJ) * 32, kk, lane);
     };
     // A slice's MFMAs, and between them the reads of the next slice's operands
-    // and, with `loads`, the loads of a later step.
-    auto slice = [&](const Slice& f, Slice& next, int stage, int kk, bool loads, int to, int step) {
+    // (slice kk of the step that is s modulo the stages) and, with `loads`, the
+    // loads of later steps into the stages that step s - 1 was in, B's first (the
+    // waits count on the order).
+    auto slice = [&](const Slice& f, Slice& next, int s, int kk, bool loads, int step) {
       u32x4 ba, bb;
       if (loads) {
-        ba = sa.buffer(step);
-        bb = sb.buffer(step);
+        ba = sa.buffer(step + kSA);
+        bb = sb.buffer(step + kSB);
       }
 #pragma unroll
       for (int q = 0; q < kMfma; ++q) {
         const int i = q / kNJ, j = q % kNJ;
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
 #pragma unroll
-        for (int r = q; r < kReads; r += kMfma) read(next, stage, kk, r);
+        for (int r = q; r < kReads; r += kMfma) read(next, s, kk, r);
         if (loads) {
 #pragma unroll
-          for (int r = q; r < kLoads; r += kMfma) load(ba, bb, to, step, r);
+          for (int r = q * kPer; r < (q + 1) * kPer && r < sa.kLoads + sb.kLoads; ++r)
+            if (r < sb.kLoads) load_b(bb, (s + kSB - 1) % kSB, step + kSB, r);
+            else load_a(ba, (s + kSA - 1) % kSA, step + kSA, r - sb.kLoads);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     };
+    // Loads that may be under way when the next step has to be there: those of
+    // the steps behind it.
+    constexpr int kAhead = (kSA - 2) * sa.kLoads + (kSB - 2) * sb.kLoads;
+    static_assert(kSA == kSB || kSA == kSB + 1, "stages");
     Slice f0, f1;
-    auto step = [&](int stage, int s) {
-      slice(f0, f1, stage, 1, false, 0, 0);
-      slice(f1, f0, stage, 2, false, 0, 0);
-      slice(f0, f1, stage, 3, false, 0, 0);
-      wait_and_meet<(kStages - 2) * kLoads>();   // step s + 1 is there, s is read
+    auto step = [&](int i, int s) {   // i: s modulo the stages
+      slice(f0, f1, i, 1, false, 0);
+      slice(f1, f0, i, 2, false, 0);
+      slice(f0, f1, i, 3, false, 0);
+      wait_and_meet<kAhead>();   // step s + 1 is there, s is read
       __builtin_amdgcn_sched_barrier(0);
-      slice(f1, f0, (stage + 1) % kStages, 0, true, stage, s + kStages);
+      slice(f1, f0, i + 1, 0, true, s);
     };
+    // In the loop's order: B's of a step, then A's of a step or of the one after.
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) load_all(i, s0 + i);
-    wait_and_meet<(kStages - 1) * kLoads>();
+    for (int i = 0; i < kSA; ++i) {
+      const u32x4 ba = sa.buffer(s0 + i), bb = sb.buffer(s0 + i - (kSA - kSB));
+      if (i >= kSA - kSB) {
+#pragma unroll
+        for (int r = 0; r < sb.kLoads; ++r) load_b(bb, i - (kSA - kSB), s0 + i - (kSA - kSB), r);
+      }
+#pragma unroll
+      for (int r = 0; r < sa.kLoads; ++r) load_a(ba, i, s0 + i, r);
+    }
+    wait_and_meet<kAhead + sa.kLoads + sb.kLoads>();
 #pragma unroll
     for (int i = 0; i < kReads; ++i) read(f0, 0, 0, i);
+    constexpr int kTurn = kSA == kSB ? kSA : kSA * kSB;
     for (int s = s0; s < s1;) {
 #pragma unroll
-      for (int i = 0; i < kStages; ++i)
+      for (int i = 0; i < kTurn; ++i)
         if (s < s1) step(i, s++);
     }
     wait_and_meet<0>();   // the LDS is free
