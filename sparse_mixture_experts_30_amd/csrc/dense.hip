@@ -13,8 +13,8 @@
 #include "gemm_device.hpp"
 #include "rows_device.hpp"
 
-#include <stdlib.h>
-#include <stdio.h>
+#include <math.h>
+
 #include <algorithm>
 
 namespace moe {
@@ -211,18 +211,38 @@ __global__ void __launch_bounds__(256) dense_join(DenseArgs p) {
   else epi_dswiglu(p, row, col, v[0], load_gu(p, row, col), load_gu(p, row, p.N + col));
 }
 
-// Tile edge and k ranges of an M x n product (n columns of B's rows, so 2 I for
-// the gate and up projections) over K.
+// Tile edge and k ranges of an M x n product (n rows of B, so 2 I for the gate and
+// up projections) over K, by estimated time.  Measured, a step of 64 k: a tile
+// of 256 takes 1.45 us with every CU at work (1.1 with few), a tile of 128 0.55,
+// whether one or two share the CU (both are then bound by loading 60 GB/s a CU);
+// 0.75 alone with operands that no other tile reads, from HBM.  Ranges of k make
+// more workgroups of a small product and cost a pass over their sums.
+//   T = 1, H = 7168, I = 18432 (both products): tiles of 128 in 1 / 4 / 7 / 16
+//   ranges 324 / 181 / 162 / 195 us, of 256 474; T = 300: 1 / 2 / 4 ranges 448 /
+//   395 / 410, of 256 639; T = 1500, H = 2048, I = 5632: 1 / 2 ranges 138 / 186,
+//   of 256 190; T = 4096: of 256 2440, of 128 about 3400.
 struct Plan {
   int edge, splits;
 };
 Plan plan_of(int64_t M, int64_t n, int64_t K) {
-  const int64_t steps = (K + kGemmBK - 1) / kGemmBK;
-  Plan q{256, 1};
-  if (getenv("DP")) { sscanf(getenv("DP"), "%d,%d", &q.edge, &q.splits);  }
-  // No range without a step; no ranges (and no workspace) without k.
-  q.splits = (int)std::max<int64_t>(1, std::min<int64_t>(q.splits, steps));
-  return q;
+  constexpr double kCus = 256, kTurn = 1.0, kFill = 5.0, kJoin = 3.0, kBytes = 5e6;   // us, bytes/us
+  const double steps = (double)((K + kGemmBK - 1) / kGemmBK);
+  auto tiles = [&](int64_t e) { return (double)((M + e - 1) / e) * ((n + e - 1) / e); };
+  const double t256 = tiles(256), full = floor(t256 / kCus), rest = t256 - full * kCus;
+  Plan best{256, 1};
+  double least = full * (steps * 1.45 + kTurn) + kFill +
+                 (rest > 0 ? steps * (1.1 + 0.35 * rest / kCus) + kTurn : 0);
+  // At least two steps a range: a range without one would leave its sums unset.
+  for (int s = 1; s <= 16 && (s == 1 || steps >= 2 * s); ++s) {
+    const double turns = ceil(tiles(128) * s / kCus), per = ceil(steps / s);
+    const double t = turns * (per * (turns == 1 && M <= 256 ? 0.75 : 0.55) + kTurn) + kFill +
+                     (s > 1 ? kJoin + 8.0 * s * (double)M * (double)n / kBytes : 0);
+    if (t < least) {
+      least = t;
+      best = {128, s};
+    }
+  }
+  return best;
 }
 size_t part_bytes(int64_t M, int64_t n, int64_t K) {
   const Plan q = plan_of(M, n, K);
@@ -241,15 +261,13 @@ template <int kOpA, int kOpB, int kEpi>
 hipError_t launch_gemm(DenseArgs a, const char* name, hipStream_t s) {
   const int64_t n = kEpi == EPI_SWIGLU ? 2 * a.N : a.N;
   const Plan q = plan_of(a.M, n, a.K);
-  const int ed = q.edge & ~1;
-  a.mt = (int)((a.M + ed - 1) / ed);
-  a.nt = (int)((n + ed - 1) / ed);
+  a.mt = (int)((a.M + q.edge - 1) / q.edge);
+  a.nt = (int)((n + q.edge - 1) / q.edge);
   a.splits = q.splits;
   const int64_t work = (int64_t)a.mt * a.nt * a.splits;
   if (work == 0) return hipSuccess;
   const unsigned grid = (unsigned)((work + kNumXcd - 1) / kNumXcd * kNumXcd);
   if (q.edge == 256) launch_tiles<256, 3, 2, kOpA, kOpB, kEpi>(a, grid, name, s);
-  else if (q.edge == 129) launch_tiles<128, 4, 4, kOpA, kOpB, kEpi>(a, grid, name, s);
   else launch_tiles<128, 3, 2, kOpA, kOpB, kEpi>(a, grid, name, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
@@ -271,12 +289,15 @@ size_t dense_part_bytes(int64_t T, int64_t H, int64_t I, bool backward) {
 }
 
 bool dense_fits(int64_t T, int64_t H, int64_t I) {
-  // At most 2^23 tiles of 256 x 128 a product (a launch holds 2^32 threads), and
-  // rows of up to 4 MiB (a tile's offsets are 31 bits).
-  auto tiles = [](int64_t m, int64_t n) { return (double)((m + 255) / 256) * ((n + 127) / 128); };
-  const double most = 8.0e6;
-  return I <= (1 << 20) && H <= (1 << 21) && tiles(T, I) < most && tiles(T, H) < most &&
-         tiles(2 * I, H) < most;
+  // Fewer than 2^32 threads a launch, also of the kernel that joins ranges of k,
+  // and rows of up to 4 MiB (a tile's offsets are 31 bits).
+  auto fits = [](int64_t m, int64_t n, int64_t K) {
+    const Plan q = plan_of(m, n, K);
+    const double work = (double)((m + q.edge - 1) / q.edge) * ((n + q.edge - 1) / q.edge) * q.splits;
+    return work * (q.edge * 2) < 4.29e9 && work < 2.1e9 && (double)m * n / 8 < 4.29e9;
+  };
+  return I <= (1 << 20) && H <= (1 << 21) && fits(T, 2 * I, H) && fits(T, H, I) &&
+         fits(T, I, H) && fits(T, H, 2 * I) && fits(2 * I, H, T) && fits(H, I, T);
 }
 
 hipError_t launch_dense_gate_up(const uint16_t* x, const uint16_t* w13, int64_t T, int H, int I,
