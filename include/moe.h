@@ -468,8 +468,9 @@ typedef struct {
  * sum in 64 bits in a fixed order, the result rounded to fp32.
  *   norm [1] fp32 out (device); a NaN or infinity among the gradients gives
  *   NaN or infinity; 0 for an empty list.
- * Workspace: moe_grad_norm_workspace_bytes(g) bytes (it depends on n alone),
- * 256-byte aligned. */
+ * Workspace: moe_grad_norm_workspace_bytes(g) bytes (it depends on n and on
+ * counts past 2^30; 0 for a list that is refused), 256-byte aligned; not needed
+ * for n == 0. */
 size_t moe_grad_norm_workspace_bytes(const moe_gradients* g);
 moe_status moe_grad_norm(const moe_gradients* g, float* norm, void* ws, size_t ws_bytes,
                          void* stream);

@@ -213,30 +213,40 @@ __global__ void __launch_bounds__(256) dense_join(DenseArgs p) {
 
 // Tile edge and k ranges of an M x n product (n rows of B, so 2 I for the gate and
 // up projections) over K, by estimated time.  Measured, a step of 64 k: a tile
-// of 256 takes 1.45 us with every CU at work (1.1 with few), a tile of 128 0.55,
-// whether one or two share the CU (both are then bound by loading 60 GB/s a CU);
-// 0.75 alone with operands that no other tile reads, from HBM.  Ranges of k make
-// more workgroups of a small product and cost a pass over their sums.
-//   T = 1, H = 7168, I = 18432 (both products): tiles of 128 in 1 / 4 / 7 / 16
-//   ranges 324 / 181 / 162 / 195 us, of 256 474; T = 300: 1 / 2 / 4 ranges 448 /
-//   395 / 410, of 256 639; T = 1500, H = 2048, I = 5632: 1 / 2 ranges 138 / 186,
-//   of 256 190; T = 4096: of 256 2440, of 128 about 3400.
+// of 256 takes 1.45 us with every CU at work (1.1 with few); tiles of 128 share
+// a CU by twos, 1.1 us both or 0.55 one alone (bound by loading 60 GB/s a CU),
+// 0.75 one alone with operands that no other tile reads, from HBM.  Ranges of k
+// make more workgroups of a small product and cost a pass over their sums.
+//   T = 1, H = 7168, I = 18432, gate and up projections in 1 / 3 / 4 / 7 ranges
+//   about 150 / 103 / 114 / 111 us, down projection 4 / 8 / 10 ranges 71 / 55 /
+//   72; both as tiles of 256 474.  T = 300: tiles of 128 in 1 / 2 / 4 ranges 448 /
+//   395 / 410, of 256 639.  T = 1500, H = 2048, I = 5632: 1 / 2 ranges 138 / 186,
+//   of 256 190.  T = 4096, H = 7168: of 256 2440.
 struct Plan {
   int edge, splits;
 };
 Plan plan_of(int64_t M, int64_t n, int64_t K) {
-  constexpr double kCus = 256, kTurn = 1.0, kFill = 5.0, kJoin = 3.0, kBytes = 5e6;   // us, bytes/us
+  constexpr double kCus = 256, kFill = 5.0, kJoin = 3.0;   // us
+  constexpr double kHbm = 5.3e6, kSums = 5e6;                           // bytes / us
   const double steps = (double)((K + kGemmBK - 1) / kGemmBK);
   auto tiles = [&](int64_t e) { return (double)((M + e - 1) / e) * ((n + e - 1) / e); };
-  const double t256 = tiles(256), full = floor(t256 / kCus), rest = t256 - full * kCus;
+  // The time of `work` tiles, `slots` at once, `one` alone on a CU, `all` with
+  // every slot taken, per step; `turn` what start and end of a tile add.
+  auto turns = [&](double work, double slots, double per, double one, double all, double turn) {
+    const double full = floor(work / slots), rest = work - full * slots;
+    const double last = rest == 0 ? 0 : rest <= kCus && slots > kCus ? one
+                                       : one + (all - one) * rest / slots;
+    return full * (per * all + turn) + (rest > 0 ? per * last + turn : 0) + kFill;
+  };
+  const double floor_us = 2.0 * ((double)M + (double)n) * (double)K / kHbm;
   Plan best{256, 1};
-  double least = full * (steps * 1.45 + kTurn) + kFill +
-                 (rest > 0 ? steps * (1.1 + 0.35 * rest / kCus) + kTurn : 0);
-  // At least two steps a range: a range without one would leave its sums unset.
+  double least = std::max(turns(tiles(256), kCus, steps, 1.1, 1.45, 6.0), floor_us + kFill);
+  // At least two steps a range: one without any would leave its sums unset.
   for (int s = 1; s <= 16 && (s == 1 || steps >= 2 * s); ++s) {
-    const double turns = ceil(tiles(128) * s / kCus), per = ceil(steps / s);
-    const double t = turns * (per * (turns == 1 && M <= 256 ? 0.75 : 0.55) + kTurn) + kFill +
-                     (s > 1 ? kJoin + 8.0 * s * (double)M * (double)n / kBytes : 0);
+    const double work = tiles(128) * s, per = ceil(steps / s);
+    const double t =
+        std::max(turns(work, 2 * kCus, per, M <= 256 ? 0.75 : 0.55, 1.1, 1.0), floor_us + kFill) +
+        (s > 1 ? kJoin + 8.0 * s * (double)M * (double)n / kSums : 0);
     if (t < least) {
       least = t;
       best = {128, s};

@@ -15,8 +15,10 @@ struct GradList {
   const uint8_t* bf16;
 };
 
-size_t grad_norm_ws_bytes(int n);
+size_t grad_norm_ws_bytes(const GradList& l);
 hipError_t launch_grad_norm(const GradList& l, double* part, float* norm, hipStream_t s);
-hipError_t launch_grad_scale(const GradList& l, const float* norm, float max_norm, hipStream_t s);
+// norm_given: norm is read and part not used.
+hipError_t launch_clip(const GradList& l, double* part, float* norm, bool norm_given,
+                       float max_norm, hipStream_t s);
 
 }  // namespace moe

@@ -668,7 +668,7 @@ moe_status check_overlap(const moe_gradients* g) {
 moe_status check_gradients(const moe_gradients* g, bool writes, GradArrays* a) {
   NONNULL(g);
   if (g->n < 0) return fail(MOE_ERR_INVALID_ARG, "n < 0");
-  if (g->n == 0) return MOE_OK;
+  if (g->n == 0) return MOE_OK;   // its arrays may be NULL
   NONNULL(g->grad);
   NONNULL(g->count);
   NONNULL(g->dtype);
@@ -694,9 +694,9 @@ moe_status check_gradients(const moe_gradients* g, bool writes, GradArrays* a) {
   return writes ? check_overlap(g) : MOE_OK;
 }
 
-moe_status check_grad_ws(const moe_gradients* g, void* ws, size_t ws_bytes) {
-  const size_t need = moe::grad_norm_ws_bytes(g->n);
-  if (g->n && (!ws || ws_bytes < need || ((uintptr_t)ws & 255)))
+moe_status check_grad_ws(const moe::GradList& l, void* ws, size_t ws_bytes) {
+  const size_t need = moe::grad_norm_ws_bytes(l);
+  if (l.n && (!ws || ws_bytes < need || ((uintptr_t)ws & 255)))
     return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned and >= %zu bytes", need);
   return MOE_OK;
 }
@@ -1288,8 +1288,8 @@ moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* 
 }
 
 size_t moe_grad_norm_workspace_bytes(const moe_gradients* g) {
-  if (!g || g->n < 0) return 0;
-  return std::max<size_t>(moe::grad_norm_ws_bytes(g->n), kAlign);
+  GradArrays a;
+  return check_gradients(g, false, &a) == MOE_OK ? moe::grad_norm_ws_bytes(a.list(g)) : 0;
 }
 
 moe_status moe_grad_norm(const moe_gradients* g, float* norm, void* ws, size_t ws_bytes,
@@ -1297,8 +1297,9 @@ moe_status moe_grad_norm(const moe_gradients* g, float* norm, void* ws, size_t w
   GradArrays a;
   CHECK(check_gradients(g, false, &a));
   NONNULL(norm);
-  CHECK(check_grad_ws(g, ws, ws_bytes));
-  HIPCALL(moe::launch_grad_norm(a.list(g), (double*)ws, norm, (hipStream_t)stream),
+  const moe::GradList l = a.list(g);
+  CHECK(check_grad_ws(l, ws, ws_bytes));
+  HIPCALL(moe::launch_grad_norm(l, (double*)ws, norm, (hipStream_t)stream),
           "gradient norm");
   return MOE_OK;
 }
@@ -1309,11 +1310,11 @@ moe_status moe_clip_grads(const moe_gradients* g, float max_norm, float* norm, i
   CHECK(check_gradients(g, true, &a));
   if (!(max_norm >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must be >= 0");
   NONNULL(norm);
-  if (!norm_given) CHECK(check_grad_ws(g, ws, ws_bytes));
-  const hipStream_t s = (hipStream_t)stream;
   const moe::GradList l = a.list(g);
-  if (!norm_given) HIPCALL(moe::launch_grad_norm(l, (double*)ws, norm, s), "gradient norm");
-  HIPCALL(moe::launch_grad_scale(l, norm, max_norm, s), "gradient clipping");
+  if (!norm_given) CHECK(check_grad_ws(l, ws, ws_bytes));
+  const hipStream_t s = (hipStream_t)stream;
+  HIPCALL(moe::launch_clip(l, (double*)ws, norm, norm_given != 0, max_norm, s),
+          "gradient clipping");
   return MOE_OK;
 }
 

@@ -204,7 +204,11 @@ def test_gradient_refusals():
     assert L.moe_grad_norm(ctypes.byref(l), FAKE, FAKE * 256, 0, None) == WS
     assert L.moe_grad_norm(ctypes.byref(l), None, FAKE * 256, 1 << 30, None) == INV
     assert L.moe_grad_norm(None, FAKE, FAKE * 256, 1 << 30, None) == INV
-    assert moe.moe_grad_norm_workspace_bytes(_list([a] * 97)) == 2 * moe.moe_grad_norm_workspace_bytes(_list([a]))
+    assert moe.moe_grad_norm_workspace_bytes(_list([a])) == 2048 * 8
+    # 168 runs a launch, of 2^30 values at most each
+    assert moe.moe_grad_norm_workspace_bytes(_list([a] * 168)) == 2 * 2048 * 8
+    assert moe.moe_grad_norm_workspace_bytes(_list([a], counts=[168 << 30])) == 2 * 2048 * 8
+    assert moe.moe_grad_norm_workspace_bytes(_list([a], types=[9])) == 0
 
 
 @pytest.mark.parametrize("grads,out,counts,ok", [

@@ -72,7 +72,7 @@ def test_norm_and_clipping(shapes, share):
     assert torch.equal(n2, norm) and all(torch.equal(a, b) for a, b in zip(inplace, out))
 
 
-@pytest.mark.parametrize("n", [95, 96, 97, 193, 400])
+@pytest.mark.parametrize("n", [97, 167, 168, 169, 337, 700])
 def test_more_gradients_than_a_table(n):
     r = np.random.default_rng(n)
     grads = _make([(int(r.integers(0, 3000)), F32 if r.random() < 0.4 else B16, int(r.integers(0, 8))) for _ in range(n)])
@@ -91,6 +91,31 @@ def test_pieces_of_a_flat_buffer_leave_the_rest():
     _check(grads, want, norm, 1.0)
     for a, b in ((0, 3), (1001, 1005), (9000, 10_000)):
         assert torch.equal(flat[a:b], old[a:b])
+
+
+def test_flat_buffers_of_both_types_are_the_separate_tensors():
+    """Pieces of one buffer per type, in mixed order, join to runs: the values of the same pieces apart."""
+    r = np.random.default_rng(11)
+    shapes = [(int(r.integers(0, 9000)), F32 if r.random() < 0.5 else B16) for _ in range(300)]
+    apart = _make([(n, t, int(r.integers(0, 4))) for n, t in shapes])
+    flat = {t: torch.cat([g for g in apart if g.dtype == t] + [torch.full((5,), 7.0, dtype=t, device=DEV)]) for t in (F32, B16)}
+    out = {t: torch.full_like(b, 3.0) for t, b in flat.items()}
+    at, pieces, outs = {F32: 0, B16: 0}, [], []
+    for n, t in shapes:
+        pieces.append(flat[t][at[t]:at[t] + n])
+        outs.append(out[t][at[t]:at[t] + n])
+        at[t] += n
+    norm = _clip(pieces, 1.5, outs)
+    _check(outs, apart, norm, 1.5)
+    want = [torch.empty_like(g) for g in apart]
+    norm2 = _clip(apart, 1.5, want)
+    assert torch.equal(norm, norm2) and all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert all((b[-5:] == 3.0).all() for b in out.values())
+    mixed = [outs[i] if i % 7 else torch.empty_like(p) for i, p in enumerate(pieces)]   # outputs that leave the buffer
+    for b in out.values():
+        b.fill_(3.0)
+    _clip(pieces, 1.5, mixed)
+    assert all(torch.equal(a, b) for a, b in zip(mixed, want))
 
 
 def test_neighbours_of_the_output_stay():
