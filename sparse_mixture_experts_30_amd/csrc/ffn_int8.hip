@@ -166,55 +166,62 @@ __global__ void __launch_bounds__(kThreads8) grouped_gemm_int8_few(Int8Args p) {
 }
 
 // --------------------------------------------------------------- many rows
-// A tile of at most kM rows (64 or 128) and two packed output tiles, eight
-// waves of kM / 2 rows x 64 columns.  Rows and weights pass through three LDS
-// stages that loads from memory fill directly, two steps ahead: at 64 and 128
-// rows a weight byte the memory, not the matrix cores, sets the pace, and it
-// wants 64 KiB and more in flight a CU.
-constexpr int kManyThreads = 512;
+// A tile of at most 128 rows and two packed output tiles, four waves of all rows
+// x 64 columns, two workgroups a CU.  Each weight goes straight to the registers
+// of the one wave that multiplies it, two steps ahead; the rows pass through
+// three LDS stages that loads from memory fill directly.  Bound by the weight
+// stream up to about 128 rows an expert: T = 4096 (H = 7168, I = 2048, top-8 of
+// 256) MANYFIGURES.
+constexpr int kManyRows = 128;
 
 // Place of 16-byte chunk c of row r among a step's rows of eight chunks.
 __device__ __forceinline__ int token_chunk(int r, int c) {
-  return r * 8 + (c ^ ((r ^ (r >> 3)) & 7));
+  return r * 8 + (c ^ (r & 7) ^ (r >> 3 & 3));
 }
 
-template <bool kGateUp, int kM, bool kStream>
-__device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u32x4* st1,
-                                               u32x4* st2, const Item& it) {
-  constexpr int kMI = kM / 64;          // 32-row blocks a wave
-  constexpr int kW = 2 * kUnits;        // pieces of a step's weights (two packed tiles)
-  constexpr int kLoadsW = kW / kManyThreads, kLoadsA = kM * 8 / kManyThreads;
+template <bool kGateUp, int kMI, bool kStream>
+__device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* lds, const Item& it) {
+  constexpr int kStage = kMI * 32 * 8;   // pieces of a step's rows
   const bool sh = it.g == p.E;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
+  const int wave = (int)scalar(tid >> 6);
   const int kdim = sh ? p.kdim_s : p.kdim_r, nsteps = kdim / kStepK;
   const int nt = sh ? p.nt_s : p.nt_r;
   // An odd number of packed tiles leaves the last pair's second half to no
-  // one: it repeats the first, and its waves store nothing.
-  const int tile0 = it.ntile * 2, tile1 = min(tile0 + 1, nt - 1);
-  const u32x4* bw = sh ? p.b_s : p.b_r + (int64_t)it.g * nt * nsteps * kUnits;
-  // Waves 0-3 load the first packed tile's blocks, 4-7 the second's.
-  const u32x4* src_w = bw + (int64_t)(wave < 4 ? tile0 : tile1) * nsteps * kUnits +
-                       (wave & 3) * 64 + lane;
-  // Rows tid / 8 + 64 j; past the end the first row again (not stored).
-  const char* src_a[kLoadsA];
+  // one: its waves repeat the first half and store nothing.
+  const int tile = it.ntile * 2 + (wave >> 1);
+  const bool mine = tile < nt;
+  // Fragments 4 (wave & 1) + 2 j and + 2 j + 1 are the wave's column block j (gate
+  // and up, or 32 columns each).
+  const u32x4* bw = (sh ? p.b_s : p.b_r + (int64_t)it.g * nt * nsteps * kUnits) +
+                    (int64_t)(mine ? tile : tile - 1) * nsteps * kUnits +
+                    ((wave & 1) * 4 + (lr >> 4)) * 128 + lh * 16 + (lr & 15);
+  u32x4 rb[2][2][4];   // [slot][column block][k slice of 32]
+  auto load_w = [&](int slot, int step) {
+    const u32x4* src = bw + (int64_t)min(step, nsteps - 1) * kUnits;
 #pragma unroll
-  for (int j = 0; j < kLoadsA; ++j) {
-    const int r = (tid >> 3) + 64 * j, rr = r < it.nrows ? r : 0;
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const u32x4* q = src + j * 256 + (t >> 1) * 64 + (t & 1) * 32;
+        rb[slot][j][t] = kStream ? __builtin_nontemporal_load(q) : *q;
+      }
+  };
+  // Rows tid / 8 + 32 i; past the end the first row again (not stored).
+  const char* src_a[kMI];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i) {
+    const int r = (tid >> 3) + 32 * i, rr = r < it.nrows ? r : 0;
     const int arow = (!sh && kGateUp) ? p.perm[it.row0 + rr] / p.K : it.row0 + rr;
-    src_a[j] = reinterpret_cast<const char*>(sh ? p.a_s : p.a_r) + (int64_t)arow * kdim +
+    src_a[i] = reinterpret_cast<const char*>(sh ? p.a_s : p.a_r) + (int64_t)arow * kdim +
                (token_chunk(r, tid & 7) - r * 8) * 16;
   }
-  auto load = [&](const u32x4* l, int step) {
-    const uint32_t la = lds_address(l), lw = la + ((wave >> 2) * kUnits + (wave & 3) * 64) * 16;
+  const uint32_t lds_at = lds_address(lds) + wave * 1024;
+  auto load_a = [&](int stage, int step) {
 #pragma unroll
-    for (int j = 0; j < kLoadsW; ++j)
-      load_global_to_lds<kStream>(src_w + (int64_t)step * kUnits + j * 256, lw + j * 4096);
-#pragma unroll
-    for (int j = 0; j < kLoadsA; ++j)
-      load_global_to_lds<false>(src_a[j] + step * kStepK,
-                                la + (kW + j * kManyThreads + wave * 64) * 16);
+    for (int i = 0; i < kMI; ++i)
+      load_global_to_lds<false>(src_a[i] + min(step, nsteps - 1) * kStepK,
+                                lds_at + (stage * kStage + i * 256) * 16);
   };
 
   i32x16 acc[kMI][2];
@@ -224,62 +231,61 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u3
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-  const int lr = lane & 31, lh = lane >> 5;
-  // Wave wn's four fragments of the 16: two blocks of 32 columns (gate and up).
-  const int frag0 = wn * 4 + (lr >> 4);
-  auto compute = [&](const u32x4* l) {
+  auto compute = [&](int stage, int slot) {
+    const u32x4* l = lds + stage * kStage;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      i32x4 a[kMI], b[2];
+      i32x4 a[kMI];
 #pragma unroll
       for (int i = 0; i < kMI; ++i)
-        a[i] = __builtin_bit_cast(
-            i32x4, l[kW + token_chunk(wm * (kM / 2) + i * 32 + lr, 2 * t + lh)]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        b[j] = __builtin_bit_cast(i32x4, l[((frag0 + 2 * j) * 2 + (t >> 1)) * 64 +
-                                           (2 * (t & 1) + lh) * 16 + (lr & 15)]);
+        a[i] = __builtin_bit_cast(i32x4, l[token_chunk(i * 32 + lr, 2 * t + lh)]);
 #pragma unroll
       for (int i = 0; i < kMI; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+              a[i], __builtin_bit_cast(i32x4, rb[slot][j][t]), acc[i][j], 0, 0, 0);
     }
   };
-  // Step s: its stage has arrived (only step s + 1's loads may be under way) and
-  // no wave reads the stage of step s - 1 any more, which step s + 2 fills.
-  auto one = [&](u32x4* now, u32x4* next, int s) {
-    wait_and_meet<kLoadsW + kLoadsA>();
-    load(next, s + 2);
+  // Step s.  Behind the loads of its rows come those of 8 weights, the next step's
+  // rows and 8 weights more; the stage of s - 1, which s + 2 fills, has been read.
+  auto one = [&](int stage, int slot, int s) {
+    wait_and_meet<16 + kMI>();
+    load_a((stage + 2) % 3, s + 2);
     __builtin_amdgcn_sched_barrier(0);
-    compute(now);
+    compute(stage, slot);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(slot, s + 2);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  auto last = [&](u32x4* now, u32x4* next, int s) {
-    if (s >= nsteps) return;
-    if (s + 1 < nsteps) wait_and_meet<kLoadsW + kLoadsA>();
-    else wait_and_meet<0>();
-    if (s + 2 < nsteps) load(next, s + 2);
-    compute(now);
-  };
-  load(st0, 0);
-  load(st1, min(1, nsteps - 1));
-  int s = 0;
-  for (; s + 5 <= nsteps; s += 3) {
-    one(st0, st2, s);
-    one(st1, st0, s + 1);
-    one(st2, st1, s + 2);
+  load_a(0, 0);
+  load_w(0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  load_a(1, 1);
+  load_w(1, 1);
+  __builtin_amdgcn_sched_barrier(0);
+  // Left by breaks: where a path joins that skips a step the compiler takes the
+  // weights for just loaded and waits for all.
+  for (int s = 0;;) {
+    one(0, 0, s);
+    if (++s >= nsteps) break;
+    one(1, 1, s);
+    if (++s >= nsteps) break;
+    one(2, 0, s);
+    if (++s >= nsteps) break;
+    one(0, 1, s);
+    if (++s >= nsteps) break;
+    one(1, 0, s);
+    if (++s >= nsteps) break;
+    one(2, 1, s);
+    if (++s >= nsteps) break;
   }
-  last(st0, st2, s);
-  last(st1, st0, s + 1);
-  last(st2, st1, s + 2);
-  last(st0, st2, s + 3);
   wait_and_meet<0>();   // the stages are free
+  if (!mine) return;    // the whole wave; nothing waits behind this
 
   const int ncol = sh ? p.ncol_s : p.ncol_r;
   const float* as = sh ? p.as_s : p.as_r;
   const float* bs = sh ? p.bs_s : p.bs_r + (int64_t)it.g * (kGateUp ? 2 : 1) * ncol;
-  const int tile = tile0 + (wn >> 1);
-  if (tile >= nt) return;   // the whole wave; nothing waits behind this
   f32x16 v[kMI][2];
 #pragma unroll
   for (int i = 0; i < kMI; ++i)
@@ -287,8 +293,7 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u3
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) v[i][j][q] = (float)acc[i][j][q];
-  float* l = reinterpret_cast<float*>(wave < 4 ? st0 : st1) + (wave & 3) * (32 * 64);
-  const int row0 = wm * (kM / 2);
+  float* l = reinterpret_cast<float*>(lds) + wave * (32 * 64);
   auto scaled = [&](float (&x)[8], float s, const float* c) {
     const f32x4 c0 = *reinterpret_cast<const f32x4*>(c),
                 c1 = *reinterpret_cast<const f32x4*>(c + 4);
@@ -299,10 +304,10 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u3
     }
   };
   if constexpr (kGateUp) {
-    const int col0 = tile * 64 + (wn & 1) * 32;
-    wave_rows<true>(l, v, [&](int r, int c, float (&g)[8], float (&u)[8]) {
-      const int row = row0 + r, col = col0 + c;
+    const int col0 = tile * 64 + (wave & 1) * 32;
+    wave_rows<true>(l, v, [&](int row, int c, float (&g)[8], float (&u)[8]) {
       if (row >= it.nrows) return;
+      const int col = col0 + c;
       const int64_t crow = it.row0 + row;
       const float s = as[sh ? crow : p.perm[crow] / p.K];
       scaled(g, s, bs + col);
@@ -315,10 +320,10 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u3
                        swiglu(g[4 * j + 2], u[4 * j + 2]), swiglu(g[4 * j + 3], u[4 * j + 3])};
     });
   } else {
-    const int col0 = tile * 128 + (wn & 1) * 64;
-    wave_rows<false>(l, v, [&](int r, int c, float (&x)[8]) {
-      const int row = row0 + r, col = col0 + c;
+    const int col0 = tile * 128 + (wave & 1) * 64;
+    wave_rows<false>(l, v, [&](int row, int c, float (&x)[8]) {
       if (row >= it.nrows) return;
+      const int col = col0 + c;
       const int64_t crow = it.row0 + row;
       scaled(x, as[crow], bs + col);
       *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(sh ? p.c_s : p.c_r) + crow * ncol +
@@ -327,17 +332,23 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* st0, u3
   }
 }
 
-template <bool kGateUp, int kM>
-__global__ void __launch_bounds__(kManyThreads, 2) grouped_gemm_int8_many(Int8Args p) {
-  constexpr int kStage = 2 * kUnits + kM * 8;
-  __shared__ u32x4 st0[kStage], st1[kStage], st2[kStage];
+template <bool kGateUp>
+__global__ void __launch_bounds__(kThreads8, 2) grouped_gemm_int8_many(Int8Args p) {
+  __shared__ u32x4 lds[3 * kManyRows * 8];
   Item it;
-  if (!find_item<kM>(p, it)) return;
+  if (!find_item<kManyRows>(p, it)) return;
   if (2 * it.ntile >= (it.g == p.E ? p.nt_s : p.nt_r)) return;
-  if (it.alone)
-    int8_many_tile<kGateUp, kM, true>(p, st0, st1, st2, it);
-  else
-    int8_many_tile<kGateUp, kM, false>(p, st0, st1, st2, it);
+  const int blocks = (it.nrows + 31) >> 5;
+#define MOE_INT8_CASE(n)                                          \
+  if (blocks == n) {                                              \
+    if (it.alone) int8_many_tile<kGateUp, n, true>(p, lds, it);   \
+    else int8_many_tile<kGateUp, n, false>(p, lds, it);           \
+  }
+  MOE_INT8_CASE(1)
+  MOE_INT8_CASE(2)
+  MOE_INT8_CASE(3)
+  MOE_INT8_CASE(4)
+#undef MOE_INT8_CASE
 }
 
 // ---------------------------------------------------------------- quantising
@@ -445,7 +456,7 @@ pack_int8_kernel(bool gate_up, const int8_t* __restrict__ codes, u32x4* __restri
 // Rows of an M-tile, which name the kernel, for the whole layer.
 int tile_rows(const FfnDims& d) {
   if (d.T <= kFewRows || d.N <= 8 * (int64_t)d.E) return kFewRows;
-  return d.N <= 64 * (int64_t)d.E ? 64 : 128;
+  return kManyRows;
 }
 
 // nt: packed tiles of the group with the most of them.
@@ -453,16 +464,14 @@ template <bool kGateUp>
 hipError_t launch_gemm(Int8Args a, int rows, int64_t mtiles, int nt, hipStream_t s) {
   a.ntn = rows == kFewRows ? nt : (nt + 1) / 2;
   const int64_t work = mtiles * a.ntn;
-  if (work > kMaxGridThreads / kManyThreads - kXcdGrid) return hipErrorInvalidValue;
+  if (work > kMaxGridThreads / kThreads8 - kXcdGrid) return hipErrorInvalidValue;
   const dim3 grid(xcd_grid(work));
   if (rows == kFewRows)
     MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int8_few<true>" : "grouped_gemm_int8_few<false>",
       hipLaunchKernelGGL((grouped_gemm_int8_few<kGateUp>), grid, dim3(kThreads8), 0, s, a));
   else
     MOE_TIMED_LAUNCH(s, kGateUp ? "grouped_gemm_int8_many<true>" : "grouped_gemm_int8_many<false>",
-      hipLaunchKernelGGL((rows == 64 ? grouped_gemm_int8_many<kGateUp, 64>
-                                     : grouped_gemm_int8_many<kGateUp, 128>),
-                         grid, dim3(kManyThreads), 0, s, a));
+      hipLaunchKernelGGL((grouped_gemm_int8_many<kGateUp>), grid, dim3(kThreads8), 0, s, a));
   return hipGetLastError();
 }
 
