@@ -31,7 +31,7 @@ size_t packed_int8_bytes(bool gate_up, int64_t experts, int n, int kd);
 hipError_t launch_pack_int8(bool gate_up, const int8_t* codes, void* dst, int64_t experts, int n,
                             int kd, hipStream_t s);
 constexpr int64_t quantize_rows_int8_max() { return kMaxGridThreads / 256; }
-hipError_t launch_quantize_rows_int8(const void* x, bool bf16, int64_t rows, int cols, int8_t* q,
+hipError_t launch_quantize_rows_int8(const uint16_t* x, int64_t rows, int cols, int8_t* q,
                                      float* scale, hipStream_t s);
 hipError_t launch_ffn_int8(const FfnDims& d, const int8_t* xq, const float* xs,
                            const int32_t* perm, const int32_t* offsets, const void* w13p,

@@ -171,7 +171,12 @@ __global__ void __launch_bounds__(kThreads8) grouped_gemm_int8_few(Int8Args p) {
 // of the one wave that multiplies it, two steps ahead; the rows pass through
 // three LDS stages that loads from memory fill directly.  Bound by the weight
 // stream up to about 128 rows an expert: T = 4096 (H = 7168, I = 2048, top-8 of
-// 256) MANYFIGURES.
+// 256) 2.90 ms
+// for both products, 4.1 TB/s of weights and rows; a step of a workgroup takes
+// 1.2 us, about what its matrix instructions, its LDS reads and its loads take
+// one after another.  Tiles of 256 rows, one workgroup a CU: 4.06 ms; both
+// operands through LDS, eight waves in step: 3.04; the step's loads behind its
+// matrix instructions instead of among them: 2.96.
 constexpr int kManyRows = 128;
 
 // Place of 16-byte chunk c of row r among a step's rows of eight chunks.
@@ -197,15 +202,13 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* lds, co
                     (int64_t)(mine ? tile : tile - 1) * nsteps * kUnits +
                     ((wave & 1) * 4 + (lr >> 4)) * 128 + lh * 16 + (lr & 15);
   u32x4 rb[2][2][4];   // [slot][column block][k slice of 32]
-  auto load_w = [&](int slot, int step) {
+  auto load_w = [&](int slot, int step, int t) {
     const u32x4* src = bw + (int64_t)min(step, nsteps - 1) * kUnits;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const u32x4* q = src + j * 256 + (t >> 1) * 64 + (t & 1) * 32;
-        rb[slot][j][t] = kStream ? __builtin_nontemporal_load(q) : *q;
-      }
+    for (int j = 0; j < 2; ++j) {
+      const u32x4* q = src + j * 256 + (t >> 1) * 64 + (t & 1) * 32;
+      rb[slot][j][t] = kStream ? __builtin_nontemporal_load(q) : *q;
+    }
   };
   // Rows tid / 8 + 32 i; past the end the first row again (not stored).
   const char* src_a[kMI];
@@ -217,11 +220,9 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* lds, co
                (token_chunk(r, tid & 7) - r * 8) * 16;
   }
   const uint32_t lds_at = lds_address(lds) + wave * 1024;
-  auto load_a = [&](int stage, int step) {
-#pragma unroll
-    for (int i = 0; i < kMI; ++i)
-      load_global_to_lds<false>(src_a[i] + min(step, nsteps - 1) * kStepK,
-                                lds_at + (stage * kStage + i * 256) * 16);
+  auto load_a = [&](int stage, int step, int i) {
+    load_global_to_lds<false>(src_a[i] + min(step, nsteps - 1) * kStepK,
+                              lds_at + (stage * kStage + i * 256) * 16);
   };
 
   i32x16 acc[kMI][2];
@@ -231,39 +232,49 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* lds, co
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-  auto compute = [&](int stage, int slot) {
+  // Slice t of step s in its stage: behind its MFMAs the loads of the rows' pass t
+  // and of the slice's weights of step s + 2 are started, into the stage that
+  // step s - 1 has read and into the registers that the slice has.
+  auto slice = [&](const i32x4 (&a)[kMI], int stage, int slot, int t, int s) {
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+            a[i], __builtin_bit_cast(i32x4, rb[slot][j][t]), acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (t < kMI) load_a((stage + 2) % 3, s + 2, t);
+    load_w(slot, s + 2, t);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Loads behind the last of a step's rows: the weights of its slices from there
+  // on, then a whole step's.
+  constexpr int kAhead = 2 * (5 - kMI) + 8 + kMI;
+  auto one = [&](int stage, int slot, int s) {
     const u32x4* l = lds + stage * kStage;
+    i32x4 a[2][kMI];   // a slice's rows are read while the one before is multiplied
+    auto read = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < kMI; ++i)
+        a[t & 1][i] = __builtin_bit_cast(i32x4, l[token_chunk(i * 32 + lr, 2 * t + lh)]);
+    };
+    wait_and_meet<kAhead>();
+    read(0);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      i32x4 a[kMI];
-#pragma unroll
-      for (int i = 0; i < kMI; ++i)
-        a[i] = __builtin_bit_cast(i32x4, l[token_chunk(i * 32 + lr, 2 * t + lh)]);
-#pragma unroll
-      for (int i = 0; i < kMI; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
-              a[i], __builtin_bit_cast(i32x4, rb[slot][j][t]), acc[i][j], 0, 0, 0);
+      if (t < 3) read(t + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      slice(a[t & 1], stage, slot, t, s);
     }
   };
-  // Step s.  Behind the loads of its rows come those of 8 weights, the next step's
-  // rows and 8 weights more; the stage of s - 1, which s + 2 fills, has been read.
-  auto one = [&](int stage, int slot, int s) {
-    wait_and_meet<16 + kMI>();
-    load_a((stage + 2) % 3, s + 2);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(stage, slot);
-    __builtin_amdgcn_sched_barrier(0);
-    load_w(slot, s + 2);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  load_a(0, 0);
-  load_w(0, 0);
-  __builtin_amdgcn_sched_barrier(0);
-  load_a(1, 1);
-  load_w(1, 1);
-  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t < kMI) load_a(s, s, t);
+      load_w(s, s, t);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   // Left by breaks: where a path joins that skips a step the compiler takes the
   // weights for just loaded and waits for all.
   for (int s = 0;;) {
@@ -339,10 +350,10 @@ __global__ void __launch_bounds__(kThreads8, 2) grouped_gemm_int8_many(Int8Args 
   if (!find_item<kManyRows>(p, it)) return;
   if (2 * it.ntile >= (it.g == p.E ? p.nt_s : p.nt_r)) return;
   const int blocks = (it.nrows + 31) >> 5;
-#define MOE_INT8_CASE(n)                                          \
-  if (blocks == n) {                                              \
-    if (it.alone) int8_many_tile<kGateUp, n, true>(p, lds, it);   \
-    else int8_many_tile<kGateUp, n, false>(p, lds, it);           \
+#define MOE_INT8_CASE(n)                                               \
+  if (blocks == n) {                                                   \
+    if (it.alone) int8_many_tile<kGateUp, n, true>(p, lds, it);        \
+    else int8_many_tile<kGateUp, n, false>(p, lds, it);                \
   }
   MOE_INT8_CASE(1)
   MOE_INT8_CASE(2)
@@ -356,16 +367,20 @@ __global__ void __launch_bounds__(kThreads8, 2) grouped_gemm_int8_many(Int8Args 
 // 127 x is exact for bf16 and its quotient by the maximum, if not a tie, is
 // at least 2^-9 from one, so the code is that of the exact quotient, ties to
 // even.  A row with a NaN or an infinity gets the scale NaN, a row of zeros
-// codes 0 and the scale 1.  Rows of up to 8192 values stay in registers.
+// codes 0 and the scale 1.  Rows of up to 8192 values stay in registers.  The
+// first rows have cols values, rows from rows1 on (h's, behind the routed ones)
+// cols2; h is not read again and passes the caches by.
 template <typename IO>
 __global__ void __launch_bounds__(256)
-quantize_rows_int8_kernel(const IO* __restrict__ x, int cols, int8_t* __restrict__ q,
-                          float* __restrict__ scale) {
+quantize_rows_int8_kernel(const IO* __restrict__ x, int64_t rows1, int cols1, int cols2,
+                          int8_t* __restrict__ q, float* __restrict__ scale) {
   constexpr int kKeep = 4;
   __shared__ uint32_t red[4];
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
-  const IO* xr = x + row * cols;
+  const int cols = row < rows1 ? cols1 : cols2;
+  const int64_t at = row < rows1 ? row * cols1 : rows1 * cols1 + (row - rows1) * cols2;
+  const IO* xr = x + at;
   const int chunks = cols / 8;
   auto load = [&](int c, float* v) {
     if constexpr (sizeof(IO) == 2) {
@@ -376,8 +391,8 @@ quantize_rows_int8_kernel(const IO* __restrict__ x, int cols, int8_t* __restrict
         v[2 * j + 1] = __uint_as_float(p[j] & 0xFFFF0000u);
       }
     } else {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(xr + c * 8),
-                  b = *reinterpret_cast<const f32x4*>(xr + c * 8 + 4);
+      const f32x4* p = reinterpret_cast<const f32x4*>(xr + c * 8);
+      const f32x4 a = __builtin_nontemporal_load(p), b = __builtin_nontemporal_load(p + 1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] = a[j];
@@ -420,7 +435,7 @@ quantize_rows_int8_kernel(const IO* __restrict__ x, int cols, int8_t* __restrict
         w[j >> 2] |= ((uint32_t)(int)fminf(fmaxf(r, -127.0f), 127.0f) & 0xFFu) << (8 * (j & 3));
       }
     }
-    *reinterpret_cast<uint2*>(q + row * cols + c * 8) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(q + at + c * 8) = make_uint2(w[0], w[1]);
   };
 #pragma unroll
   for (int i = 0; i < kKeep; ++i)
@@ -453,9 +468,22 @@ pack_int8_kernel(bool gate_up, const int8_t* __restrict__ codes, u32x4* __restri
                                            16 * (lane >> 4));
 }
 
-// Rows of an M-tile, which name the kernel, for the whole layer.
-int tile_rows(const FfnDims& d) {
-  if (d.T <= kFewRows || d.N <= 8 * (int64_t)d.E) return kFewRows;
+// Rows of an M-tile, which name the kernel: the few-row kernel up to kFewAverage
+// rows per expert on average, and where the tall tiles would be too few
+// workgroups (its own split k over four waves and are shorter).  Measured few /
+// many at H = 7168, I = 2048, E = 256, K = 8: T = 384 (12 rows an expert) 1.84 /
+// 1.88 ms, T = 512 1.94 / 1.93, T = 700 2.24 / 1.98.  By tall workgroups x rows an
+// expert: 92 x 50 34 / 46 us, 114 x 100 34 / 44, 156 x 500 34 / 42, 160 x 32 67 / 64,
+// 288 x 16 143 / 128, 368 x 250 207 / 137, 540 x 47 117 / 101.
+// The choice is the whole layer's, whichever of its groups the launch computes.
+constexpr int kFewAverage = 14;
+constexpr int64_t kTallGrid = 256, kTallWork = 100000;
+int tile_rows(FfnDims d) {
+  d.groups = kGroupsAll;
+  const int64_t tall = ffn_grid_mtiles(d, kManyRows) * (std::max(d.I, d.Is) / 128);
+  if (d.T <= kFewRows || (d.N && d.N <= (int64_t)kFewAverage * d.E) ||
+      (tall < kTallGrid && tall * (d.N ? d.N : d.T) < kTallWork * (d.N ? d.E : 1)))
+    return kFewRows;
   return kManyRows;
 }
 
@@ -491,16 +519,12 @@ hipError_t launch_pack_int8(bool gate_up, const int8_t* codes, void* dst, int64_
   return hipGetLastError();
 }
 
-hipError_t launch_quantize_rows_int8(const void* x, bool bf16, int64_t rows, int cols, int8_t* q,
+hipError_t launch_quantize_rows_int8(const uint16_t* x, int64_t rows, int cols, int8_t* q,
                                      float* scale, hipStream_t s) {
   if (rows > quantize_rows_int8_max()) return hipErrorInvalidValue;
   MOE_TIMED_LAUNCH(s, "quantize_rows_int8_kernel",
-    if (bf16)
-      hipLaunchKernelGGL(quantize_rows_int8_kernel<uint16_t>, dim3((unsigned)rows), dim3(256), 0, s,
-                         (const uint16_t*)x, cols, q, scale);
-    else
-      hipLaunchKernelGGL(quantize_rows_int8_kernel<float>, dim3((unsigned)rows), dim3(256), 0, s,
-                         (const float*)x, cols, q, scale));
+    hipLaunchKernelGGL(quantize_rows_int8_kernel<uint16_t>, dim3((unsigned)rows), dim3(256), 0, s,
+                       x, rows, cols, 0, q, scale));
   return hipGetLastError();
 }
 
@@ -539,12 +563,16 @@ hipError_t launch_ffn_int8(const FfnDims& d, const int8_t* xq, const float* xs,
 
   int8_t* hq_s = hq + d.N * d.I;
   float* hs_s = hs + d.N;
-  if (routed && d.N) {
-    e = launch_quantize_rows_int8(h, false, d.N, d.I, hq, hs, s);
-    if (e != hipSuccess) return e;
-  }
-  if (shared) {
-    e = launch_quantize_rows_int8(h + d.N * d.I, false, d.T, d.Is, hq_s, hs_s, s);
+  // The routed rows and the shared expert's lie one behind the other; either may
+  // be another launch's.
+  const int64_t first = routed ? 0 : d.N, end = d.N + (shared ? d.T : 0);
+  if (end - first > quantize_rows_int8_max()) return hipErrorInvalidValue;
+  if (end > first) {
+    MOE_TIMED_LAUNCH(s, "quantize_rows_int8_kernel<h>",
+      hipLaunchKernelGGL(quantize_rows_int8_kernel<float>, dim3((unsigned)(end - first)),
+                         dim3(256), 0, s, h + first * d.I, d.N - first, d.I, d.Is,
+                         hq + first * d.I, hs + first));
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
 

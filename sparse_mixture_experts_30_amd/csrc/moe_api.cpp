@@ -98,8 +98,9 @@ moe_status check_T(int64_t T, const moe_config* c) {
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T < 0");
   if (T * (int64_t)c->num_experts_per_tok > 0x7fffffffLL || T > 0x7fffffffLL)
     return fail(MOE_ERR_UNSUPPORTED, "T * top_k exceeds int32 indexing");
-  if (is_int8(c->weight_dtype) && T * c->num_experts_per_tok > moe::quantize_rows_int8_max())
-    return fail(MOE_ERR_UNSUPPORTED, "T * top_k: one launch quantises %lld rows",
+  if (is_int8(c->weight_dtype) &&
+      T * ((int64_t)c->num_experts_per_tok + 1) > moe::quantize_rows_int8_max())
+    return fail(MOE_ERR_UNSUPPORTED, "T * (top_k + 1): one launch quantises %lld rows",
                 (long long)moe::quantize_rows_int8_max());
   return MOE_OK;
 }
@@ -251,7 +252,7 @@ moe_status run_permute(const moe_config* c, int64_t T, const int32_t* idx, int32
 moe_status quantise_tokens(const moe_config* c, int64_t T, const void* x, void* ws,
                            const Layout& L, hipStream_t s) {
   if (is_int8(c->weight_dtype))
-    HIPCALL(moe::launch_quantize_rows_int8(x, true, T, c->hidden_size, at<int8_t>(ws, L.xq),
+    HIPCALL(moe::launch_quantize_rows_int8((const uint16_t*)x, T, c->hidden_size, at<int8_t>(ws, L.xq),
                                            at<float>(ws, L.xs), s),
             "quantise x");
   else
@@ -1348,8 +1349,8 @@ moe_status moe_quantize_act(const moe_config* cfg, int64_t rows, const void* x, 
   if (is_int8(cfg->weight_dtype)) {
     ALIGNED16(x);
     ALIGNED16(xq);
-    HIPCALL(moe::launch_quantize_rows_int8(x, true, rows, cfg->hidden_size, (int8_t*)xq, xs,
-                                           (hipStream_t)stream),
+    HIPCALL(moe::launch_quantize_rows_int8((const uint16_t*)x, rows, cfg->hidden_size,
+                                           (int8_t*)xq, xs, (hipStream_t)stream),
             "quantise");
     return MOE_OK;
   }
@@ -1426,8 +1427,8 @@ moe_status moe_quantize_weight(const moe_config* cfg, moe_weight_id which, const
     NONNULL(scales);
     ALIGNED16(src);
     ALIGNED16(codes);
-    HIPCALL(moe::launch_quantize_rows_int8(src, true, rows, m.kd, (int8_t*)codes, (float*)scales,
-                                           (hipStream_t)stream),
+    HIPCALL(moe::launch_quantize_rows_int8((const uint16_t*)src, rows, m.kd, (int8_t*)codes,
+                                           (float*)scales, (hipStream_t)stream),
             "quantise weight");
     return MOE_OK;
   }
