@@ -208,7 +208,7 @@ def _prepare_own(s, c):
     s["y"] = new(T, H)
     ws = moe.moe_dense_ffn_workspace_bytes(C, T)
     if c["op"] == "dense_train":
-        s["gu"], s["dx"] = new(T, 2 * I), new(T, H)
+        s["gu"], s["dx"] = new(T, 2 * I, dtype=torch.float32), new(T, H)
         s["dw13"], s["dw2"] = torch.empty_like(s["w13"]), torch.empty_like(s["w2"])
         ws = max(ws, moe.moe_dense_ffn_backward_workspace_bytes(C, T))
     s["ws"] = new(ws, dtype=torch.uint8)
