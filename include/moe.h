@@ -422,7 +422,7 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
  * the routed sizes of cfg take no part and the routed weights may be NULL.
  *   x [T, H], y [T, H] act_dtype, 16-byte aligned.  Every weight type and layout
  *   that the shared expert takes.
- *   gu [T, 2Is] bf16 out, for the backward: the gate's and the up projection's
+ *   gu [T, 2Is] fp32 out, for the backward: the gate's and the up projection's
  *   outputs side by side (NULL: not kept; row-major bf16 weights only,
  *   MOE_ERR_UNSUPPORTED otherwise).
  * bf16 weights: h kept in bf16; fp32 accumulation.
@@ -432,13 +432,14 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
  * it does not handle, shared_intermediate_size == 0 among them). */
 size_t moe_dense_ffn_workspace_bytes(const moe_config* cfg, int64_t T);
 moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w,
-                         void* gu, void* y, void* ws, size_t ws_bytes, void* stream);
+                         float* gu, void* y, void* ws, size_t ws_bytes, void* stream);
 
 /* Its backward, for row-major bf16 weights.  With [g u] = gu and dy the gradient
  * of y:
  *   dh = dy W2;  dg = dh u silu'(g);  du = dh silu(g);
  *   dx = [dg du] W13;  dW2 = dy^T h;  dW13 = [dg du]^T x,  h = silu(g) u.
- * g, u, h and [dg du] are bf16 operands, every product accumulates in fp32.
+ * g and u are fp32, h and [dg du] are rounded to bf16 as operands, every product
+ * accumulates in fp32.
  *   x, dy [T, H] bf16; gu [T, 2Is] as the forward wrote it (NULL: computed again
  *   from x); dx [T, H] bf16 out (may be dy itself; NULL: not wanted); dws13
  *   [2Is, H], dws2 [H, Is] bf16 out, written whole, zeros for T == 0 (the outputs
@@ -447,7 +448,7 @@ moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const 
  * aligned (0 for a configuration it does not handle; not needed for T == 0). */
 size_t moe_dense_ffn_backward_workspace_bytes(const moe_config* cfg, int64_t T);
 moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* x,
-                                  const moe_weights* w, const void* gu, const void* dy, void* dx,
+                                  const moe_weights* w, const float* gu, const void* dy, void* dx,
                                   void* dws13, void* dws2, void* ws, size_t ws_bytes,
                                   void* stream);
 

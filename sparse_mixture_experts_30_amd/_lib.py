@@ -383,9 +383,16 @@ def moe_dense_ffn_workspace_bytes(cfg: MoeConfig, T: int) -> int:
     return lib().moe_dense_ffn_workspace_bytes(ctypes.byref(cfg), T)
 
 
+def _fp32(t) -> Optional[int]:
+    """_flat of an fp32 tensor: half the bytes would be written past their end."""
+    if t is not None and type(t) is not int and t.element_size() != 4:
+        raise ValueError(f"{t.dtype} tensor, not float32")
+    return _flat(t)
+
+
 def moe_dense_ffn(cfg, T, x, w: MoeWeights, y, ws, gu=None, stream=None):
-    """y = W2 (silu(W_gate x) * (W_up x)) with ws13 and ws2 of w; gu keeps both projections."""
-    _check(lib().moe_dense_ffn(ctypes.byref(cfg), T, _flat(x), ctypes.byref(w), _flat(gu), _flat(y),
+    """y = W2 (silu(W_gate x) * (W_up x)) with ws13 and ws2 of w; gu (fp32) keeps both projections."""
+    _check(lib().moe_dense_ffn(ctypes.byref(cfg), T, _flat(x), ctypes.byref(w), _fp32(gu), _flat(y),
                                _flat(ws), _nbytes(ws) if ws is not None else 0, _stream(stream)))
 
 
@@ -396,7 +403,7 @@ def moe_dense_ffn_backward_workspace_bytes(cfg: MoeConfig, T: int) -> int:
 def moe_dense_ffn_backward(cfg, T, x, w: MoeWeights, dy, dx, dws13, dws2, ws, gu=None,
                            stream=None):
     """Gradients of x, ws13 and ws2 for dy; gu as the forward wrote it, or None: computed again."""
-    _check(lib().moe_dense_ffn_backward(ctypes.byref(cfg), T, _flat(x), ctypes.byref(w), _flat(gu),
+    _check(lib().moe_dense_ffn_backward(ctypes.byref(cfg), T, _flat(x), ctypes.byref(w), _fp32(gu),
                                         _flat(dy), _flat(dx), _flat(dws13), _flat(dws2), _flat(ws),
                                         _nbytes(ws) if ws is not None else 0, _stream(stream)))
 

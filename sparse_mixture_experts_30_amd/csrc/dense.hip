@@ -6,9 +6,11 @@
 // Six matrix products, two fused epilogues (the activation behind [g; u], its
 // derivative behind dh).  Every operand is read as it lies: the products
 // that contract over tokens or over a weight's rows read it through the
-// LDS's transposing loads.  g and u are kept in bf16 for the backward (half
-// the bytes of fp32; they are read once, elementwise), h and [dg du] are
-// rounded to bf16 as operands of the products that follow.
+// LDS's transposing loads.  g and u are kept in fp32 for the backward: in
+// bf16 they would save 1.5% of a training step's time and double the error of
+// [dg du] (gradients 3.5e-3 from 64 bits instead of 2.4e-3, of which their own
+// rounding is 1.7e-3).  h and [dg du] are rounded to bf16 as operands of the
+// products that follow.
 #include "dense.hpp"
 #include "gemm_device.hpp"
 #include "rows_device.hpp"
@@ -30,11 +32,16 @@ struct DenseArgs {
   int64_t ldb;
   int64_t M, N, K;       // EPI_SWIGLU: N = I, the columns of h
   uint16_t* c;           // EPI_STORE: [M, N]; else h [M, I] (may be null)
-  uint16_t* gu;          // [M, 2 I]: written (EPI_SWIGLU; may be null) or read (EPI_DSWIGLU)
+  float* gu;             // [M, 2 I]: written (EPI_SWIGLU; may be null) or read (EPI_DSWIGLU)
   uint16_t* da;          // EPI_DSWIGLU: [M, 2 I]
   float* part;           // sums of each k range [splits][M][N, EPI_SWIGLU: 2 N]
   int mt, nt, splits;
 };
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<f32x4*>(p)[0] = (f32x4){v[0], v[1], v[2], v[3]};
+  reinterpret_cast<f32x4*>(p)[1] = (f32x4){v[4], v[5], v[6], v[7]};
+}
 
 // What becomes of eight neighbouring sums (EPI_SWIGLU: of g and of u) from
 // (row, col) on.
@@ -45,9 +52,9 @@ __device__ __forceinline__ void epi_store(const DenseArgs& p, int64_t row, int64
 __device__ __forceinline__ void epi_swiglu(const DenseArgs& p, int64_t row, int64_t col,
                                            const float (&g)[8], const float (&u)[8]) {
   if (p.gu) {
-    uint16_t* o = p.gu + row * 2 * p.N + col;
-    *reinterpret_cast<u32x4*>(o) = pack_bf16x8(g);
-    *reinterpret_cast<u32x4*>(o + p.N) = pack_bf16x8(u);
+    float* o = p.gu + row * 2 * p.N + col;
+    store8(o, g);
+    store8(o + p.N, u);
   }
   if (p.c) {
     float h[8];
@@ -56,20 +63,27 @@ __device__ __forceinline__ void epi_swiglu(const DenseArgs& p, int64_t row, int6
     *reinterpret_cast<u32x4*>(p.c + row * p.N + col) = pack_bf16x8(h);
   }
 }
-__device__ __forceinline__ u32x4 load_gu(const DenseArgs& p, int64_t row, int64_t col) {
-  return *reinterpret_cast<const u32x4*>(p.gu + row * 2 * p.N + col);
-}
+struct GateUp {   // g and u of eight columns
+  f32x4 g[2], u[2];
+  __device__ __forceinline__ void load(const DenseArgs& p, int64_t row, int64_t col) {
+    const float* at = p.gu + row * 2 * p.N + col;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      g[i] = reinterpret_cast<const f32x4*>(at)[i];
+      u[i] = reinterpret_cast<const f32x4*>(at + p.N)[i];
+    }
+  }
+};
 __device__ __forceinline__ void epi_dswiglu(const DenseArgs& p, int64_t row, int64_t col,
-                                            const float (&dh)[8], u32x4 g16, u32x4 u16) {
-  float g[8], u[8], dg[8], du[8], h[8];
-  unpack_bf16x8(g16, g);
-  unpack_bf16x8(u16, u);
+                                            const float (&dh)[8], const GateUp& v) {
+  float dg[8], du[8], h[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float s = 1.0f / (1.0f + __expf(-g[j])), gs = g[j] * s;
-    dg[j] = dh[j] * u[j] * (s + gs * (1.0f - s));
+    const float g = v.g[j >> 2][j & 3], u = v.u[j >> 2][j & 3];
+    const float s = 1.0f / (1.0f + __expf(-g)), gs = g * s;
+    dg[j] = dh[j] * u * (s + gs * (1.0f - s));
     du[j] = dh[j] * gs;
-    h[j] = gs * u[j];
+    h[j] = gs * u;
   }
   uint16_t* dp = p.da + row * 2 * p.N + col;
   *reinterpret_cast<u32x4*>(dp) = pack_bf16x8(dg);
@@ -128,11 +142,7 @@ __global__ void __launch_bounds__(64 * kWM * kWN, 2) dense_gemm(DenseArgs p) {
   float* l = reinterpret_cast<float*>(lds) + w * (32 * (Tile::kNJ == 1 ? 32 : 64));
   const int64_t row0 = m0 + Tile::row0(w);
   const int64_t col0 = n0 + (kEpi == EPI_SWIGLU ? Tile::col0(w) / 2 : Tile::col0(w));
-  auto keep = [&](int64_t at, const float (&v)[8]) {
-    f32x4* o = reinterpret_cast<f32x4*>(p.part + at);
-    o[0] = (f32x4){v[0], v[1], v[2], v[3]};
-    o[1] = (f32x4){v[4], v[5], v[6], v[7]};
-  };
+  auto keep = [&](int64_t at, const float (&v)[8]) { store8(p.part + at, v); };
   if constexpr (kEpi == EPI_SWIGLU) {
     wave_rows<true>(l, acc, [&](int r, int c, const float (&g)[8], const float (&u)[8]) {
       const int64_t row = row0 + r, col = col0 + c;
@@ -153,30 +163,26 @@ __global__ void __launch_bounds__(64 * kWM * kWN, 2) dense_gemm(DenseArgs p) {
       else epi_store(p, row, col, v);
     });
   } else {
-    // g and u of 32 rows are loaded together, while the 32 before are worked on:
-    // one by one they would each wait for memory.  Past the edge the last value
-    // again.
+    // g and u of 32 rows are loaded together, each piece as soon as the one of the
+    // 32 rows before is used: one by one they would each wait for memory.  Past
+    // the edge the last value again.
     static_assert(kEpi != EPI_DSWIGLU || Tile::kNJ == 2, "rows of 64 columns a wave");
     const int lane = threadIdx.x & 63;
-    u32x4 g[2][4], u[2][4];
-    auto ahead = [&](int i) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int64_t row = min(row0 + i * 32 + t * 8 + (lane >> 3), p.M - 1),
-                      col = min(col0 + (lane & 7) * 8, p.N - 8);
-        g[i & 1][t] = load_gu(p, row, col);
-        u[i & 1][t] = load_gu(p, row, p.N + col);
-      }
+    GateUp v[4];
+    auto load = [&](int i, int t) {
+      v[t].load(p, min(row0 + i * 32 + t * 8 + (lane >> 3), p.M - 1),
+                min(col0 + (lane & 7) * 8, p.N - 8));
     };
-    ahead(0);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) load(0, t);
 #pragma unroll
     for (int i = 0; i < Tile::kMI; ++i) {
-      if (i + 1 < Tile::kMI) ahead(i + 1);
       int t = 0;
       f32x16(&block)[1][Tile::kNJ] = reinterpret_cast<f32x16(&)[1][Tile::kNJ]>(acc[i]);
-      wave_rows<false>(l, block, [&](int r, int c, const float (&v)[8]) {
+      wave_rows<false>(l, block, [&](int r, int c, const float (&dh)[8]) {
         const int64_t row = row0 + i * 32 + r, col = col0 + c;
-        if (row < p.M && col < p.N) epi_dswiglu(p, row, col, v, g[i & 1][t], u[i & 1][t]);
+        if (row < p.M && col < p.N) epi_dswiglu(p, row, col, dh, v[t]);
+        if (i + 1 < Tile::kMI) load(i + 1, t);
         ++t;
       });
     }
@@ -208,7 +214,11 @@ __global__ void __launch_bounds__(256) dense_join(DenseArgs p) {
   }
   if constexpr (kEpi == EPI_SWIGLU) epi_swiglu(p, row, col, v[0], v[1]);
   else if constexpr (kEpi == EPI_STORE) epi_store(p, row, col, v[0]);
-  else epi_dswiglu(p, row, col, v[0], load_gu(p, row, col), load_gu(p, row, p.N + col));
+  else {
+    GateUp gu;
+    gu.load(p, row, col);
+    epi_dswiglu(p, row, col, v[0], gu);
+  }
 }
 
 // Tile edge and k ranges of an M x n product (n rows of B, so 2 I for the gate and
@@ -311,7 +321,7 @@ bool dense_fits(int64_t T, int64_t H, int64_t I) {
 }
 
 hipError_t launch_dense_gate_up(const uint16_t* x, const uint16_t* w13, int64_t T, int H, int I,
-                                uint16_t* gu, uint16_t* h, float* part, hipStream_t s) {
+                                float* gu, uint16_t* h, float* part, hipStream_t s) {
   DenseArgs a{};
   a.part = part;
   a.a = (const char*)x;
@@ -342,7 +352,7 @@ hipError_t launch_dense_down(const uint16_t* h, const uint16_t* w2, int64_t T, i
 }
 
 hipError_t launch_dense_backward(const uint16_t* x, const uint16_t* w13, const uint16_t* w2,
-                                 const uint16_t* gu, const uint16_t* dy, int64_t T, int H, int I,
+                                 const float* gu, const uint16_t* dy, int64_t T, int H, int I,
                                  uint16_t* da, uint16_t* h, uint16_t* dx, uint16_t* dw13,
                                  uint16_t* dw2, float* part, hipStream_t s) {
   const int64_t rh = (int64_t)H * 2, ri = (int64_t)I * 2;   // bytes of rows of H and I
@@ -356,7 +366,7 @@ hipError_t launch_dense_backward(const uint16_t* x, const uint16_t* w13, const u
   a.N = I;
   a.K = H;
   a.c = h;
-  a.gu = const_cast<uint16_t*>(gu);
+  a.gu = const_cast<float*>(gu);
   a.da = da;
   hipError_t e = launch_gemm<OP_ROW, OP_COL, EPI_DSWIGLU>(a, "dense_gemm<dh>", s);
   if (e != hipSuccess) return e;

@@ -12,13 +12,13 @@ bool dense_fits(int64_t T, int64_t H, int64_t I);
 size_t dense_part_bytes(int64_t T, int64_t H, int64_t I, bool backward);
 // h = silu(g) u of [g u] = x W13^T; gu [T, 2 I] and h [T, I] may be null.
 hipError_t launch_dense_gate_up(const uint16_t* x, const uint16_t* w13, int64_t T, int H, int I,
-                                uint16_t* gu, uint16_t* h, float* part, hipStream_t s);
+                                float* gu, uint16_t* h, float* part, hipStream_t s);
 // y = h W2^T.
 hipError_t launch_dense_down(const uint16_t* h, const uint16_t* w2, int64_t T, int H, int I,
                              uint16_t* y, float* part, hipStream_t s);
 // da [T, 2 I] and h [T, I] are scratch; dx may be null.
 hipError_t launch_dense_backward(const uint16_t* x, const uint16_t* w13, const uint16_t* w2,
-                                 const uint16_t* gu, const uint16_t* dy, int64_t T, int H, int I,
+                                 const float* gu, const uint16_t* dy, int64_t T, int H, int I,
                                  uint16_t* da, uint16_t* h, uint16_t* dx, uint16_t* dw13,
                                  uint16_t* dw2, float* part, hipStream_t s);
 

@@ -605,8 +605,8 @@ struct DenseBackwardLayout {
 };
 DenseBackwardLayout dense_backward_layout(const moe_config* c, int64_t T) {
   const size_t row = up((size_t)T * c->shared_intermediate_size * 2);
-  return {0, 2 * row, 4 * row, 5 * row,
-          5 * row + up(moe::dense_part_bytes(T, c->hidden_size, c->shared_intermediate_size, true))};
+  return {0, 4 * row, 6 * row, 7 * row,
+          7 * row + up(moe::dense_part_bytes(T, c->hidden_size, c->shared_intermediate_size, true))};
 }
 
 // ---- gradients --------------------------------------------------------------
@@ -1205,7 +1205,7 @@ size_t moe_dense_ffn_workspace_bytes(const moe_config* cfg, int64_t T) {
 }
 
 moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w,
-                         void* gu, void* y, void* ws, size_t ws_bytes, void* stream) {
+                         float* gu, void* y, void* ws, size_t ws_bytes, void* stream) {
   CHECK(check_dense(cfg, T));
   NONNULL(w);
   const bool rowmajor = cfg->weight_dtype == MOE_BF16 && !w->packed;
@@ -1228,7 +1228,7 @@ moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const 
   const int H = cfg->hidden_size, I = cfg->shared_intermediate_size;
   uint16_t* h = at<uint16_t>(ws, L.h);
   HIPCALL(moe::launch_dense_gate_up((const uint16_t*)x, (const uint16_t*)w->ws13, T, H, I,
-                                    (uint16_t*)gu, h, at<float>(ws, L.part), s),
+                                    gu, h, at<float>(ws, L.part), s),
           "dense gate/up");
   HIPCALL(moe::launch_dense_down(h, (const uint16_t*)w->ws2, T, H, I, (uint16_t*)y,
                                  at<float>(ws, L.part), s),
@@ -1242,7 +1242,7 @@ size_t moe_dense_ffn_backward_workspace_bytes(const moe_config* cfg, int64_t T) 
 }
 
 moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* x,
-                                  const moe_weights* w, const void* gu, const void* dy, void* dx,
+                                  const moe_weights* w, const float* gu, const void* dy, void* dx,
                                   void* dws13, void* dws2, void* ws, size_t ws_bytes,
                                   void* stream) {
   CHECK(check_dense(cfg, T));
@@ -1273,12 +1273,12 @@ moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* 
   ALIGNED16(dws13);
   ALIGNED16(dws2);
   const hipStream_t s = (hipStream_t)stream;
-  const uint16_t* g = (const uint16_t*)gu;
+  const float* g = gu;
   if (T && !g) {   // computed again
     HIPCALL(moe::launch_dense_gate_up((const uint16_t*)x, (const uint16_t*)w->ws13, T, H, I,
-                                      at<uint16_t>(ws, L.gu), nullptr, at<float>(ws, L.part), s),
+                                      at<float>(ws, L.gu), nullptr, at<float>(ws, L.part), s),
             "dense gate/up");
-    g = at<uint16_t>(ws, L.gu);
+    g = at<float>(ws, L.gu);
   }
   HIPCALL(moe::launch_dense_backward((const uint16_t*)x, (const uint16_t*)w->ws13,
                                      (const uint16_t*)w->ws2, g, (const uint16_t*)dy, T, H, I,

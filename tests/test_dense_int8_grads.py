@@ -94,6 +94,14 @@ def test_dense_refusals():
         assert moe.moe_dense_ffn_workspace_bytes(_cfg(wd=wd), 4) >= 4 * 128
 
 
+def test_binding_refuses_kept_projections_of_two_bytes():
+    w, gu = moe.weights(ws13=FAKE, ws2=FAKE), torch.empty(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="float32"):
+        moe.moe_dense_ffn(_cfg(), 4, FAKE, w, FAKE, None, gu=gu, stream=0)
+    with pytest.raises(ValueError, match="float32"):
+        moe.moe_dense_ffn_backward(_cfg(), 4, FAKE, w, FAKE, FAKE, FAKE, FAKE, None, gu=gu, stream=0)
+
+
 def test_dense_backward_refusals():
     def f(c=_cfg(), T=4, x=FAKE, w=moe.weights(ws13=FAKE, ws2=FAKE), gu=FAKE, dy=FAKE, dx=FAKE, dw13=FAKE, dw2=FAKE,
           ws=FAKE * 256, n=1 << 50):
@@ -110,7 +118,7 @@ def test_dense_backward_refusals():
         assert f(c=_cfg(wd=wd)) == UNS
         assert moe.moe_dense_ffn_backward_workspace_bytes(_cfg(wd=wd), 4) == 0
     assert f(c=_cfg(act="f32", wd="f32")) == UNS
-    assert moe.moe_dense_ffn_backward_workspace_bytes(_cfg(), 4) >= 5 * 4 * 128 * 2
+    assert moe.moe_dense_ffn_backward_workspace_bytes(_cfg(), 4) >= 7 * 4 * 128 * 2
 
 
 # -------------------------------------------------------------------- int8

@@ -45,12 +45,12 @@ class Block:
         f = moe.moe_dense_ffn_backward_workspace_bytes if backward else moe.moe_dense_ffn_workspace_bytes
         return torch.full((f(self.C, self.T),), 0xFF, dtype=torch.uint8, device=DEV)
 
-    def rows(self, n, cols):
+    def rows(self, n, cols, dtype=torch.bfloat16):
         """n rows and some behind them that no call may touch."""
-        return torch.full((n + GUARD, cols), float("nan"), dtype=torch.bfloat16, device=DEV)
+        return torch.full((n + GUARD, cols), float("nan"), dtype=dtype, device=DEV)
 
     def forward(self, keep=True):
-        y, gu = self.rows(self.T, self.H), self.rows(self.T, 2 * self.I) if keep else None
+        y, gu = self.rows(self.T, self.H), self.rows(self.T, 2 * self.I, torch.float32) if keep else None
         moe.moe_dense_ffn(self.C, self.T, self.dev["x"], self.W, y, self.ws(), gu=gu)
         return y, gu
 
@@ -75,8 +75,8 @@ class Block:
         y = h @ w2.T
         ey = eh16 @ a(w2).T + _sum(self.I) * ((a(h) + eh16) @ a(w2).T)
         r = {"y": (y, ey + U * (a(y) + ey)), "gu": (np.concatenate([g, u], 1),
-             np.concatenate([dg_ + U * (a(g) + dg_), du_ + U * (a(u) + du_)], 1))}
-        # backward from the bf16 g, u
+             np.concatenate([dg_, du_], 1))}
+        # backward from the kept g, u
         eg, eu = np.split(r["gu"][1], 2, axis=1)
         dh = dy @ w2
         edh = _sum(self.H) * (a(dy) @ a(w2))
