@@ -1,12 +1,14 @@
 """The feed-forward half of a transformer layer, from residual stream to residual stream, on the
 library's operators:
 
-  serving    residual add + RMS norm -> the MoE layer on 4-bit expert weights (`Serving`), or the norm's
-             e4m3 rows -> FP8 experts (`ServingFp8`)
+  serving    residual add + RMS norm -> the MoE layer on 4-bit or 8-bit integer expert weights (`Serving`),
+             or the norm's e4m3 rows -> FP8 experts (`ServingFp8`)
   training   residual add + RMS norm -> gate -> sorted rows -> experts and a per-expert adapter of the
              user's own -> combine, and the way back (`Training`)
+  dense      residual add + RMS norm -> the dense feed-forward block of the first layers, its way back and
+             the clipping of its gradients (`DenseTraining`)
 
-    python examples/moe_block.py            # a small block on cuda:0: the three once, with their times
+    python examples/moe_block.py            # a small block on cuda:0: each once, with its time
 
 The adapter stands for any user-made expert part: it works on the sorted rows (`moe_dispatch`), its output
 is added to the library's expert outputs, and its gradient comes from `moe_combine_backward` and goes back
@@ -52,19 +54,26 @@ def _check_rows(T, H, at_most=None, **rows):
 
 
 class Serving:
-    """One decode or prompt step on 4-bit experts: (x, residual) -> (out, residual)."""
+    """One decode or prompt step on integer experts, 4-bit with a scale per `group` inputs or, with bits=8,
+    8-bit with a scale per channel (and per token): (x, residual) -> (out, residual)."""
 
-    def __init__(self, w, H, E, G, TG, K, I, Is, rho, max_tokens, group=128):
+    def __init__(self, w, H, E, G, TG, K, I, Is, rho, max_tokens, group=128, bits=4):
         self.H, self.norm = H, w["norm"]
-        self.cfg = C = moe.config(H, E, G, TG, K, I, Is, rho, "bf16", f"int4g{group}")
+        self.cfg = C = moe.config(H, E, G, TG, K, I, Is, rho, "bf16", f"int4g{group}" if bits == 4 else "int8")
         packed = {}
         for name, which in WHICH.items():
             m = w[name]
-            codes = _empty(*m.shape[:-1], m.shape[-1] // 2, dtype=torch.uint8)
-            scales = _empty(*m.shape[:-1], m.shape[-1] // group)
-            moe.moe_quantize_weight(C, which, m, codes, scales)
             packed[name] = _empty(moe.moe_packed_bytes(C, which), dtype=torch.uint8)
-            moe.moe_pack_quantized(C, which, codes, scales, packed[name])
+            if bits == 4:
+                codes = _empty(*m.shape[:-1], m.shape[-1] // 2, dtype=torch.uint8)
+                scales = _empty(*m.shape[:-1], m.shape[-1] // group)
+                moe.moe_quantize_weight(C, which, m, codes, scales)
+                moe.moe_pack_quantized(C, which, codes, scales, packed[name])
+            else:
+                codes, scales = _empty(*m.shape, dtype=torch.int8), _empty(*m.shape[:-1], dtype=torch.float32)
+                moe.moe_quantize_weight(C, which, m, codes, scales)
+                moe.moe_pack_weight(C, which, codes, packed[name])
+                packed[name + "_scale"] = scales
         self.keep = (packed, w["gate_w"], w["bias"])
         self.weights = moe.weights(gate_w=w["gate_w"], bias=w["bias"], packed=True, **packed)
         self.ws = _empty(moe.moe_workspace_bytes(C, max_tokens), dtype=torch.uint8)
@@ -176,6 +185,41 @@ class Training:
         return d
 
 
+class DenseTraining:
+    """Training step of a dense layer's feed-forward half for T tokens: the block's forward, its backward and
+    the gradients clipped to a global norm."""
+
+    def __init__(self, w, H, I, T):
+        self.w, self.T, f32 = w, T, torch.float32
+        self.cfg = C = moe.config(H, 2, 1, 1, 1, 64, I, 1.0, "bf16", "bf16")   # no routed part
+        self.weights = moe.weights(ws13=w["ws13"], ws2=w["ws2"])
+        self.sum, self.n, self.out, self.dn, self.dx = (_empty(T, H) for _ in range(5))
+        self.gu = _empty(T, 2 * I, dtype=f32)
+        self.grads = {k: torch.zeros_like(w[k]) for k in ("norm", "ws13", "ws2")}
+        self.list = moe.gradients(self.grads.values())
+        self.grad_norm = _empty(1, dtype=f32)
+        self.ws = _empty(max(moe.moe_dense_ffn_workspace_bytes(C, T), moe.moe_dense_ffn_backward_workspace_bytes(C, T),
+                             moe.moe_add_rmsnorm_backward_workspace_bytes(C, T),
+                             moe.moe_grad_norm_workspace_bytes(self.list)), dtype=torch.uint8)
+
+    def forward(self, x, residual):
+        """(out, sum): the block's output and the new residual stream."""
+        C, T = self.cfg, self.T
+        _check_rows(T, self.n.shape[1], x=x, residual=residual)
+        moe.moe_add_rmsnorm(C, T, x, residual, self.w["norm"], EPS, sum=self.sum, y=self.n)
+        moe.moe_dense_ffn(C, T, self.n, self.weights, self.out, self.ws, gu=self.gu)
+        return self.out, self.sum
+
+    def backward(self, dout, dsum, max_norm):
+        """(gradient of x and of residual, the weights' clipped gradients, their norm before it)."""
+        C, T, g = self.cfg, self.T, self.grads
+        _check_rows(T, self.n.shape[1], dout=dout, dsum=dsum)
+        moe.moe_dense_ffn_backward(C, T, self.n, self.weights, dout, self.dn, g["ws13"], g["ws2"], self.ws, gu=self.gu)
+        moe.moe_add_rmsnorm_backward(C, T, self.sum, self.w["norm"], EPS, self.dn, self.dx, g["norm"], self.ws, dsum=dsum)
+        moe.moe_clip_grads(self.list, max_norm, self.grad_norm, self.ws)
+        return self.dx, g, self.grad_norm
+
+
 def fp8_weights(w, cfg):
     """Packed e4m3 copies of the bf16 expert weights and their 128x128 block scales."""
     packed, scales = {}, {}
@@ -211,6 +255,8 @@ def main():
     x, res, out = rows(T, 1), rows(T, 2), _empty(T, H)
     s4 = Serving(w, *shape, max_tokens=T)
     timed(f"decode step, {T} tokens, 4-bit experts", lambda: s4.step(x, res.clone(), out))
+    s8i = Serving(w, *shape, max_tokens=T, bits=8)
+    timed(f"decode step, {T} tokens, 8-bit integer experts", lambda: s8i.step(x, res.clone(), out))
     T = 256
     x, res, out = rows(T, 3), rows(T, 4), _empty(T, H)
     s8 = ServingFp8(*fp8_weights(w, moe.config(*shape, "bf16", "fp8")), w, *shape, max_tokens=T)
@@ -224,6 +270,13 @@ def main():
         return tr.backward(dout, dsum)
 
     timed(f"training step, {T} tokens, bf16 experts and an adapter", train)
+    dense = DenseTraining(w, H, Is, T)
+
+    def train_dense():
+        dense.forward(x, res)
+        return dense.backward(dout, dsum, 1.0)
+
+    timed(f"training step, {T} tokens, dense layer with clipping", train_dense)
 
 
 if __name__ == "__main__":
