@@ -429,7 +429,8 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
  * Row-major bf16 weights serve training and prompts; a few tokens at a time
  * read either layout at the rate of memory.
  * Workspace: moe_dense_ffn_workspace_bytes(cfg, T) bytes (0 for a configuration
- * it does not handle, shared_intermediate_size == 0 among them). */
+ * it does not handle, shared_intermediate_size == 0 among them); one for the
+ * largest batch does for the smaller ones. */
 size_t moe_dense_ffn_workspace_bytes(const moe_config* cfg, int64_t T);
 moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w,
                          float* gu, void* y, void* ws, size_t ws_bytes, void* stream);
@@ -445,7 +446,8 @@ moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const 
  *   [2Is, H], dws2 [H, Is] bf16 out, written whole, zeros for T == 0 (the outputs
  *   that a call without tokens writes).
  * Workspace: moe_dense_ffn_backward_workspace_bytes(cfg, T) bytes, 256-byte
- * aligned (0 for a configuration it does not handle; not needed for T == 0). */
+ * aligned (0 for a configuration it does not handle; not needed for T == 0); one
+ * for the largest batch does for the smaller ones. */
 size_t moe_dense_ffn_backward_workspace_bytes(const moe_config* cfg, int64_t T);
 moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* x,
                                   const moe_weights* w, const float* gu, const void* dy, void* dx,

@@ -438,13 +438,13 @@ def moe_grad_norm_workspace_bytes(g: MoeGradients) -> int:
 
 def moe_grad_norm(g: MoeGradients, norm, ws, stream=None):
     """norm [1] = the 2-norm of all gradients together."""
-    _check(lib().moe_grad_norm(ctypes.byref(g), _flat(norm), _flat(ws),
+    _check(lib().moe_grad_norm(ctypes.byref(g), _fp32(norm), _flat(ws),
                                _nbytes(ws) if ws is not None else 0, _stream(stream)))
 
 
 def moe_clip_grads(g: MoeGradients, max_norm, norm, ws=None, norm_given=False, stream=None):
     """Gradients times min(1, max_norm / (norm + 1e-6)); norm [1] is written first, or read."""
-    _check(lib().moe_clip_grads(ctypes.byref(g), float(max_norm), _flat(norm), int(bool(norm_given)),
+    _check(lib().moe_clip_grads(ctypes.byref(g), float(max_norm), _fp32(norm), int(bool(norm_given)),
                                 _flat(ws), _nbytes(ws) if ws is not None else 0, _stream(stream)))
 
 

@@ -7,7 +7,7 @@
 // derivative behind dh).  Every operand is read as it lies: the products
 // that contract over tokens or over a weight's rows read it through the
 // LDS's transposing loads.  g and u are kept in fp32 for the backward: in
-// bf16 they would save 1.5% of a training step's time and double the error of
+// bf16 they would save 2.8% of a training step's time and double the error of
 // [dg du] (gradients 3.5e-3 from 64 bits instead of 2.4e-3, of which their own
 // rounding is 1.7e-3).  h and [dg du] are rounded to bf16 as operands of the
 // products that follow.
@@ -232,6 +232,9 @@ __global__ void __launch_bounds__(256) dense_join(DenseArgs p) {
 //   72; both as tiles of 256 474.  T = 300: tiles of 128 in 1 / 2 / 4 ranges 448 /
 //   395 / 410, of 256 639.  T = 1500, H = 2048, I = 5632: 1 / 2 ranges 138 / 186,
 //   of 256 190.  T = 4096, H = 7168: of 256 2440.
+// More than kMostParts workgroups' sums are never kept apart (a plan for which that
+// would pay was estimated 2.5% faster at best), which bounds the workspace.
+constexpr int kMostSplits = 16, kMostParts = 1024;
 struct Plan {
   int edge, splits;
 };
@@ -252,8 +255,9 @@ Plan plan_of(int64_t M, int64_t n, int64_t K) {
   Plan best{256, 1};
   double least = std::max(turns(tiles(256), kCus, steps, 1.1, 1.45, 6.0), floor_us + kFill);
   // At least two steps a range: one without any would leave its sums unset.
-  for (int s = 1; s <= 16 && (s == 1 || steps >= 2 * s); ++s) {
+  for (int s = 1; s <= kMostSplits && (s == 1 || steps >= 2 * s); ++s) {
     const double work = tiles(128) * s, per = ceil(steps / s);
+    if (s > 1 && work > kMostParts) break;
     const double t =
         std::max(turns(work, 2 * kCus, per, M <= 256 ? 0.75 : 0.55, 1.1, 1.0), floor_us + kFill) +
         (s > 1 ? kJoin + 8.0 * s * (double)M * (double)n / kSums : 0);
@@ -264,9 +268,12 @@ Plan plan_of(int64_t M, int64_t n, int64_t K) {
   }
   return best;
 }
+// Room for the sums of any plan of up to this size: a workspace for the largest
+// batch does for the smaller ones too, which may take more ranges.
 size_t part_bytes(int64_t M, int64_t n, int64_t K) {
-  const Plan q = plan_of(M, n, K);
-  return q.splits > 1 ? (size_t)q.splits * M * n * 4 : 0;
+  const int64_t splits = std::min<int64_t>(kMostSplits, (K + kGemmBK - 1) / kGemmBK / 2);
+  if (splits < 2) return 0;
+  return (size_t)std::min((double)splits * M * n * 4, kMostParts * 128.0 * 128.0 * 4);
 }
 
 template <int kEdge, int kSA, int kSB, int kOpA, int kOpB, int kEpi>

@@ -278,3 +278,11 @@ def test_binding_checks_gradients():
         moe.gradients([t], [t[:4]])
     l = moe.gradients([t, t.bfloat16()])
     assert l.n == 2
+
+
+@pytest.mark.parametrize("H,I", [(7168, 18432), (2048, 5632), (512, 1024), (7168, 2048), (128, 128)])
+def test_a_workspace_for_a_batch_does_for_smaller_ones(H, I):
+    for f in (moe.moe_dense_ffn_workspace_bytes, moe.moe_dense_ffn_backward_workspace_bytes):
+        for wd in ("bf16", "int8"):
+            sizes = [f(_cfg(H=H, Is=I, wd=wd), T) for T in range(0, 5000)]
+            assert sizes == sorted(sizes)
