@@ -169,14 +169,14 @@ __global__ void __launch_bounds__(kThreads8) grouped_gemm_int8_few(Int8Args p) {
 // A tile of at most 128 rows and two packed output tiles, four waves of all rows
 // x 64 columns, two workgroups a CU.  Each weight goes straight to the registers
 // of the one wave that multiplies it, two steps ahead; the rows pass through
-// three LDS stages that loads from memory fill directly.  Bound by the weight
-// stream up to about 128 rows an expert: T = 4096 (H = 7168, I = 2048, top-8 of
-// 256) 2.90 ms
-// for both products, 4.1 TB/s of weights and rows; a step of a workgroup takes
-// 1.2 us, about what its matrix instructions, its LDS reads and its loads take
-// one after another.  Tiles of 256 rows, one workgroup a CU: 4.06 ms; both
-// operands through LDS, eight waves in step: 3.04; the step's loads behind its
-// matrix instructions instead of among them: 2.96.
+// three LDS stages that loads from memory fill directly.  Bound by HBM up to
+// about 128 rows an expert: T = 4096 (H = 7168, I = 2048, top-8 of 256) 2.83 ms
+// with both quantisers, 4.2 TB/s of weights and rows counted once; the kernels
+// themselves move 5.0 (experts of several tiles, rows read by more than one XCD).
+// A step of a workgroup takes 1.2 us, about what its matrix instructions, its LDS
+// reads and its loads take one after another.  Tiles of 256 rows, one workgroup a
+// CU: 4.06 ms; both operands through LDS, eight waves in step: 3.04; the step's
+// loads behind its matrix instructions instead of among them: 2.96.
 constexpr int kManyRows = 128;
 
 // Place of 16-byte chunk c of row r among a step's rows of eight chunks.
@@ -199,11 +199,13 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* lds, co
   // Fragments 4 (wave & 1) + 2 j and + 2 j + 1 are the wave's column block j (gate
   // and up, or 32 columns each).
   const u32x4* bw = (sh ? p.b_s : p.b_r + (int64_t)it.g * nt * nsteps * kUnits) +
-                    (int64_t)(mine ? tile : tile - 1) * nsteps * kUnits +
-                    ((wave & 1) * 4 + (lr >> 4)) * 128 + lh * 16 + (lr & 15);
+                    (int64_t)(mine ? tile : tile - 1) * nsteps * kUnits;
+  const int bl = ((wave & 1) * 4 + (lr >> 4)) * 128 + lh * 16 + (lr & 15);
   u32x4 rb[2][2][4];   // [slot][column block][k slice of 32]
   auto load_w = [&](int slot, int step, int t) {
-    const u32x4* src = bw + (int64_t)min(step, nsteps - 1) * kUnits;
+    // Past the last step one piece for all lanes (the last step again came from
+    // memory a second time, an eighth of the down projection's weights).
+    const u32x4* src = bw + (step < nsteps ? step * kUnits + bl : 0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const u32x4* q = src + j * 256 + (t >> 1) * 64 + (t & 1) * 32;
