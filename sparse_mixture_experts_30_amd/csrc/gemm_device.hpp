@@ -23,8 +23,10 @@
 //
 // Loads go through buffer descriptors that end at the operand's last valid
 // row (row operand) or last valid k (col operand): what lies past it arrives as
-// zeros, so no size has to be a multiple of the tile, a k range that ends
-// inside a step adds nothing, and steps past the last are loaded in vain.
+// zeros, so no size has to be a multiple of the tile and a k range that ends
+// inside a step adds nothing.  Past a range's last step they are empty: those
+// loads keep the waits' count and read nothing (T = 1 in three ranges read 5%
+// more than its weights).
 #pragma once
 
 #include "moe_internal.hpp"
@@ -133,10 +135,12 @@ struct Stager {
       at = (kOp == OP_GATE_UP ? r & 31 : r) * ld + c * 16;
     }
   }
-  __device__ __forceinline__ u32x4 buffer(int step) const {
-    if (kOp != OP_COL) return fixed;
+  // Of a k step, empty from step `end` on.
+  __device__ __forceinline__ u32x4 buffer(int step, int end) const {
     const int64_t k = (int64_t)step * kGemmBK;
-    return buffer_of(p + k * ld, (rows - k) * ld);
+    u32x4 b = kOp == OP_COL ? buffer_of(p + k * ld, (rows - k) * ld) : fixed;
+    b[2] = step < end ? b[2] : 0;
+    return b;
   }
   // Starts load j of k step `step` into the operand's place of a stage.
   __device__ __forceinline__ void load(u32x4 buf, uint32_t lds, int step, int j) const {
@@ -145,7 +149,9 @@ struct Stager {
                     : kOp == OP_GATE_UP ? j * kPass / 64 * 32 * ld + step * (kGemmBK * 2)
                                          : j * kPass * ld + step * (kGemmBK * 2);
     static_assert(kOp != OP_GATE_UP || kPass == 32 || kPass == 64, "rows a load");
-    load_to_lds(kOp == OP_GATE_UP && kPass == 32 && (j & 1) ? second : buf, lds + (j * kThreads + wave * 64) * 16, at + off);
+    if (kOp == OP_GATE_UP && kPass == 32 && (j & 1))
+      buf = (u32x4){second[0], second[1], buf[2], second[3]};   // as long as the other
+    load_to_lds(buf, lds + (j * kThreads + wave * 64) * 16, at + off);
   }
 };
 
@@ -225,8 +231,8 @@ struct GemmTile {
     auto slice = [&](const Slice& f, Slice& next, int s, int kk, bool loads, int step) {
       u32x4 ba, bb;
       if (loads) {
-        ba = sa.buffer(step + kSA);
-        bb = sb.buffer(step + kSB);
+        ba = sa.buffer(step + kSA, s1);
+        bb = sb.buffer(step + kSB, s1);
       }
 #pragma unroll
       for (int q = 0; q < kMfma; ++q) {
@@ -259,7 +265,7 @@ struct GemmTile {
     // In the loop's order: B's of a step, then A's of a step or of the one after.
 #pragma unroll
     for (int i = 0; i < kSA; ++i) {
-      const u32x4 ba = sa.buffer(s0 + i), bb = sb.buffer(s0 + i - (kSA - kSB));
+      const u32x4 ba = sa.buffer(s0 + i, s1), bb = sb.buffer(s0 + i - (kSA - kSB), s1);
       if (i >= kSA - kSB) {
 #pragma unroll
         for (int r = 0; r < sb.kLoads; ++r) load_b(bb, i - (kSA - kSB), s0 + i - (kSA - kSB), r);
