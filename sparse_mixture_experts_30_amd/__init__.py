@@ -4,8 +4,10 @@ expert, SwiGLU grouped expert GEMMs (bf16 MFMA, e4m3 block-scaled variant),
 an always-active shared expert, the weighted combine, the load-balancing
 update of the selection bias, and the backward of the layer (gate, combine,
 expert FFNs).  Decode batches take a three-launch routing schedule, and the
-shared expert can run on a second stream beside the routed ones.  All compute is in the HIP kernels of
-libmoe.so; this package only marshals arguments."""
+shared expert can run on a second stream beside the routed ones.  Around the
+layer: residual add and RMS norm, sorted token rows, their gradients; experts
+in 4-bit and 8-bit integers; dense SwiGLU layers with their backward; the global
+gradient norm and clipping.  All compute is in the HIP kernels of libmoe.so; this package only marshals arguments."""
 from ._lib import (EXPORTS, MOE_BF16, MOE_ERR_DEVICE_CHECK, MOE_ERR_HIP, MOE_ERR_INVALID_ARG,
                    MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_F32, MOE_FP8_E4M3, MOE_FP8_E4M3_E8M0, MOE_OK,
                    MOE_W13, MOE_W2, MOE_WS13, MOE_WS2, moe_pack_weight, moe_packed_bytes,
