@@ -113,3 +113,46 @@ def test_in_place_and_without_dx_are_the_same_bits():
         torch.cuda.synchronize()
         assert torch.equal(outs[0][0], outs[1][0])
         assert all(torch.equal(outs[0][i], o[i]) for o in outs[1:] for i in (1, 2))
+
+
+def test_more_than_two_billion_values():
+    """Offsets past 31 and 32 bits: rows from the start, around the middle and at the end, and the weights' gradients."""
+    T, H, I = (1 << 20) + 77, 2112, 64
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=DEV)
+    for c in x.split(1 << 16):
+        c.copy_(torch.randn(c.shape, generator=g, device=DEV))
+    dy = x.roll(1, 0)
+    w13, w2 = _rand(g, 2 * I, H, scale=H ** -0.5), _rand(g, H, I, scale=I ** -0.5)
+    C, W = moe.config(H, 2, 1, 1, 1, 64, I, 1.0, "bf16", "bf16"), moe.weights(ws13=w13, ws2=w2)
+    ws = torch.empty(max(moe.moe_dense_ffn_workspace_bytes(C, T), moe.moe_dense_ffn_backward_workspace_bytes(C, T)),
+                     dtype=torch.uint8, device=DEV)
+    y, gu, dx = _room(T, H), _room(T, 2 * I, torch.float32), _room(T, H)
+    dw13, dw2 = torch.empty_like(w13), torch.empty_like(w2)
+    moe.moe_dense_ffn(C, T, x, W, y, ws, gu=gu)
+    moe.moe_dense_ffn_backward(C, T, x, W, dy, dx, dw13, dw2, ws, gu=gu)
+    torch.cuda.synchronize()
+    a, b = w13.double(), w2.double()
+    rdw13, rdw2 = torch.zeros_like(a), torch.zeros_like(b)
+
+    def ref(r):
+        xr, dyr = x[r].double(), dy[r].double()
+        gt, u = (xr @ a.T).chunk(2, 1)
+        s = torch.sigmoid(gt)
+        dh = dyr @ b
+        da = torch.cat([dh * u * (s + gt * s * (1 - s)), dh * gt * s], 1)
+        return xr, dyr, gt * s * u, da
+
+    for at in range(0, T, 1 << 16):
+        r = slice(at, min(T, at + (1 << 16)))
+        xr, dyr, h, da = ref(r)
+        rdw13 += da.T @ xr
+        rdw2 += dyr.T @ h
+        # the 2-norm of two roundings each
+        for got, want in ((y[r], h @ b.T), (dx[r], da @ a)):
+            assert float((got.double() - want).norm() / want.norm()) <= 2 * U, at
+    for got, want in ((dw13, rdw13), (dw2, rdw2)):
+        # beside the two roundings those of an fp32 sum of T terms, each at most 2^-24 of the sum so far and as often up
+        # as down: sqrt(T) 2^-24 of the result on average, with room of 16
+        assert float((got.double() - want).norm() / want.norm()) <= 2 * U + T ** 0.5 * E * 16
+    assert torch.isnan(y[T:]).all() and torch.isnan(dx[T:]).all() and torch.isnan(gu[T:]).all()
