@@ -160,7 +160,7 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& p, u32x4* lds, int b
 
   // The operands are read for the last time: the waves share their LDS out.
   const int w = Tile::wave();
-  float* l = reinterpret_cast<float*>(lds) + w * (32 * (Tile::kNJ == 1 ? 32 : 64));
+  float* l = reinterpret_cast<float*>(lds) + w * (32 * 64);
   const int64_t row0 = m0 + Tile::row0(w);
   const int64_t col0 = n0 + (kEpi == EPI_SWIGLU ? Tile::col0(w) / 2 : Tile::col0(w));
   auto keep = [&](int64_t at, const float (&v)[8]) { store8(p.part + at, v); };
@@ -184,7 +184,6 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& p, u32x4* lds, int b
       else epi_store(p, row, col, v);
     });
   } else {
-    static_assert(kEpi != EPI_DSWIGLU || Tile::kNJ == 2, "rows of 64 columns a wave");
     if (!kEarly) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) load_gu(0, t);
@@ -243,10 +242,13 @@ __global__ void __launch_bounds__(256, 2) dense_gemm_grads(DenseGradArgs a) {
   }
 }
 
-// The k ranges' sums joined in their order, eight columns a thread.
+// The k ranges' sums joined in their order, eight columns a thread.  Bound by
+// latency: four ranges under way at a time and workgroups of 256 take 1 us longer
+// (T = 16, H = 2048, I = 5632: block 32.7 instead of 30.7 us).
+constexpr int kJoinThreads = 128;
 template <int kEpi>
-__global__ void __launch_bounds__(256) dense_join(DenseArgs p) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+__global__ void __launch_bounds__(kJoinThreads) dense_join(DenseArgs p) {
+  const int64_t i = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 8;
   if (i >= p.M * p.N) return;
   const int64_t row = i / p.N, col = i % p.N;
   constexpr int kParts = kEpi == EPI_SWIGLU ? 2 : 1;
@@ -256,16 +258,16 @@ __global__ void __launch_bounds__(256) dense_join(DenseArgs p) {
   for (int h = 0; h < kParts; ++h) {
     const float* src = p.part + (row * kParts + h) * p.N + col;
     f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
-    for (int s = 0; s < p.splits; s += 4) {   // four ranges' loads under way at a time
-      f32x4 x[4], y[4];
+    for (int s = 0; s < p.splits; s += 8) {   // eight ranges' loads under way at a time
+      f32x4 x[8], y[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 8; ++q) {
         const float* at = src + min(s + q, p.splits - 1) * all;
         x[q] = *reinterpret_cast<const f32x4*>(at);
         y[q] = *reinterpret_cast<const f32x4*>(at + 4);
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 8; ++q)
         if (s + q < p.splits) {
           a += x[q];
           b += y[q];
@@ -365,8 +367,9 @@ template <int kEpi>
 hipError_t launch_join(const DenseArgs& a, hipStream_t s) {
   if (a.splits == 1) return hipSuccess;
   MOE_TIMED_LAUNCH(s, "dense_join",
-    hipLaunchKernelGGL(dense_join<kEpi>, dim3((unsigned)((a.M * a.N / 8 + 255) / 256)), dim3(256),
-                       0, s, a));
+    hipLaunchKernelGGL(dense_join<kEpi>,
+                       dim3((unsigned)((a.M * a.N / 8 + kJoinThreads - 1) / kJoinThreads)),
+                       dim3(kJoinThreads), 0, s, a));
   return hipGetLastError();
 }
 

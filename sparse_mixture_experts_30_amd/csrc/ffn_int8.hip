@@ -223,8 +223,8 @@ __device__ __forceinline__ void int8_many_tile(const Int8Args& p, u32x4* lds, co
   }
   const uint32_t lds_at = lds_address(lds) + wave * 1024;
   auto load_a = [&](int stage, int step, int i) {
-    load_global_to_lds<false>(src_a[i] + min(step, nsteps - 1) * kStepK,
-                              lds_at + (stage * kStage + i * 256) * 16);
+    load_global_to_lds(src_a[i] + min(step, nsteps - 1) * kStepK,
+                       lds_at + (stage * kStage + i * 256) * 16);
   };
 
   i32x16 acc[kMI][2];

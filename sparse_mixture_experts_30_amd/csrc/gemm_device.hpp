@@ -4,8 +4,8 @@
 // A[k][m], B[k][n]), so that the products of a feed-forward block and of its
 // backward need no transposed copies.
 //
-// Tile kM x kN, k in steps of 64 through two or more LDS stages that loads from
-// memory fill directly.  A row operand's step is [row][64 k] in eight 16-byte
+// Tile kM x kN of kM / kWM x 64 a wave, k in steps of 64 through two or more LDS
+// stages that loads from memory fill directly.  A row operand's step is [row][64 k] in eight 16-byte
 // chunks, chunk c of row r at c ^ (r & 7) ^ (r >> 3 & 3); a col operand's is [64 k][row],
 // the 32-byte piece s of k row k at s ^ f(k), f = (k & 3) ^ (k & 3) << 1, and is
 // transposed by the LDS's 16-bit transposing read: four k rows of 16 values a
@@ -78,15 +78,9 @@ __device__ __forceinline__ void load_to_lds(u32x4 buffer, uint32_t lds, int offs
                ::"s"(lds), "v"(offset), "s"(buffer) : "memory");
 }
 
-// kNt: not kept in cache.
-template <bool kNt>
-__device__ __forceinline__ void load_global_to_lds(const void* p, uint32_t at) {
-  if (kNt)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
-                 ::"s"(at), "v"(p) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 ::"s"(at), "v"(p) : "memory");
+__device__ __forceinline__ void load_global_to_lds(const void* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               ::"s"(lds), "v"(p) : "memory");
 }
 
 // Waits until at most kLeft of this wave's loads to LDS are under way and its
@@ -179,6 +173,7 @@ struct GemmTile {
   static constexpr int kThreads = 64 * kWM * kWN;
   static constexpr int kMI = kM / kWM / 32, kNJ = kN / kWN / 32;
   static constexpr int kPieces = kSA * kM * 8 + kSB * kN * 8;
+  static_assert(kNJ == 2, "64 columns a wave");
 
   static __device__ __forceinline__ int wave() { return (int)scalar(threadIdx.x >> 6); }
   static __device__ __forceinline__ int row0(int wave) { return wave / kWN * (kM / kWM); }
@@ -287,59 +282,51 @@ struct GemmTile {
 };
 
 // Hands a wave's part of a tile out row by row: f(row, column, v) with v the fp32
-// values of eight consecutive columns, through the wave's own 32 x 64 (kNJ 1: 32
-// x 32) floats of LDS.  acc [kMI][kNJ] are 32 x 32 blocks; rows and columns count
-// from the wave's first.  With kPair, column blocks 2 j and 2 j + 1 come together:
-// f(row, column, v, w), the columns of the pairs counted by halves.
-template <bool kPair, int kMI, int kNJ, class F>
-__device__ __forceinline__ void wave_rows(float* l, const f32x16 (&acc)[kMI][kNJ], F f) {
-  constexpr int kB = kNJ == 1 ? 1 : 2, kCols = 32 * kB;   // column blocks at a time
-  static_assert(kNJ % kB == 0 && (!kPair || kB == 2), "pairs of column blocks");
+// values of eight consecutive columns, through the wave's own 32 x 64 floats of
+// LDS.  acc [kMI][2] are 32 x 32 blocks; rows and columns count from the wave's
+// first.  With kPair, the two column blocks come together: f(row, column, v, w).
+template <bool kPair, int kMI, class F>
+__device__ __forceinline__ void wave_rows(float* l, const f32x16 (&acc)[kMI][2], F f) {
   const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
   // physical column: the other half for every second group of four rows
-  auto phys = [](int row, int col) {
-    return row * kCols + (kB == 2 ? col ^ ((row & 4) * 8) : col);
-  };
+  auto phys = [](int row, int col) { return row * 64 + (col ^ ((row & 4) * 8)); };
 #pragma unroll
-  for (int i = 0; i < kMI; ++i)
+  for (int i = 0; i < kMI; ++i) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int j0 = 0; j0 < kNJ; j0 += kB) {
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int j = 0; j < kB; ++j)
+      for (int q = 0; q < 16; ++q)
+        l[phys(8 * (q >> 2) + 4 * lh + (q & 3), j * 32 + lr)] = acc[i][j][q];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    auto get = [&](int row, int col, float (&v)[8]) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(l + phys(row, col));
+      const f32x4 x = p[0], y = p[1];
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          l[phys(8 * (q >> 2) + 4 * lh + (q & 3), j * 32 + lr)] = acc[i][j0 + j][q];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      auto get = [&](int row, int col, float (&v)[8]) {
-        const f32x4* p = reinterpret_cast<const f32x4*>(l + phys(row, col));
-        const f32x4 x = p[0], y = p[1];
+      for (int t = 0; t < 4; ++t) {
+        v[t] = x[t];
+        v[4 + t] = y[t];
+      }
+    };
+    if constexpr (kPair) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          v[t] = x[t];
-          v[4 + t] = y[t];
-        }
-      };
-      if constexpr (kPair) {
+      for (int t = 0; t < 2; ++t) {
+        const int row = t * 16 + (lane >> 2), col = (lane & 3) * 8;
+        float v[8], w[8];
+        get(row, col, v);
+        get(row, 32 + col, w);
+        f(i * 32 + row, col, v, w);
+      }
+    } else {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int row = t * 16 + (lane >> 2), col = (lane & 3) * 8;
-          float v[8], w[8];
-          get(row, col, v);
-          get(row, 32 + col, w);
-          f(i * 32 + row, j0 * 16 + col, v, w);
-        }
-      } else {
-        constexpr int kL = kCols / 8;   // lanes a row
-#pragma unroll
-        for (int t = 0; t < kL / 2; ++t) {
-          const int row = t * (64 / kL) + lane / kL, col = (lane % kL) * 8;
-          float v[8];
-          get(row, col, v);
-          f(i * 32 + row, j0 * 32 + col, v);
-        }
+      for (int t = 0; t < 4; ++t) {
+        const int row = t * 8 + (lane >> 3), col = (lane & 7) * 8;
+        float v[8];
+        get(row, col, v);
+        f(i * 32 + row, col, v);
       }
     }
+  }
 }
 
 }  // namespace moe
