@@ -410,7 +410,8 @@ def moe_dense_ffn_backward(cfg, T, x, w: MoeWeights, dy, dx, dws13, dws2, ws, gu
 
 def gradients(grads, out=None) -> MoeGradients:
     """The list that moe_grad_norm and moe_clip_grads take, made once for buffers that stay where
-    they are: fp32 or bf16 tensors without gaps, and where the clipped ones go (None: in place)."""
+    they are: fp32 or bf16 tensors of one device without gaps, and where the clipped ones go (None:
+    in place)."""
     import torch
     types = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
     grads = list(grads)
@@ -422,6 +423,9 @@ def gradients(grads, out=None) -> MoeGradients:
             raise ValueError(f"gradient of type {g.dtype}, not float32 or bfloat16")
         if o.dtype != g.dtype or o.numel() != g.numel():
             raise ValueError(f"output of {o.numel()} {o.dtype} for a gradient of {g.numel()} {g.dtype}")
+    devices = sorted({str(t.device) for t in grads + out})
+    if len(devices) > 1:
+        raise ValueError(f"gradients and outputs on several devices: {', '.join(devices)}")
     n = len(grads)
     arrays = ((ctypes.c_void_p * n)(*[_flat(t) for t in grads]),
               (ctypes.c_void_p * n)(*[_flat(t) for t in out]),
@@ -429,7 +433,24 @@ def gradients(grads, out=None) -> MoeGradients:
               (ctypes.c_int32 * n)(*[types[t.dtype] for t in grads]))
     m = MoeGradients(n, *[ctypes.addressof(a) for a in arrays])
     m.keep = (arrays, grads, out)
+    m.device = grads[0].device if n else None
     return m
+
+
+def _on_device(g: MoeGradients, **tensors):
+    """Raises where the kernels would read or write host memory, or another GPU's: the list's tensors,
+    norm and workspace are all on the current GPU.  (Addresses are taken as they come.)"""
+    import torch
+    device = getattr(g, "device", None)   # None: an empty list, or one made from addresses
+    if device is None:
+        return
+    if device.type != "cuda":
+        raise ValueError(f"gradients on {device}, not on a GPU")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"gradients on {device}, current GPU is {torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and type(t) is not int and t.device != device:
+            raise ValueError(f"{name} on {t.device}, gradients on {device}")
 
 
 def moe_grad_norm_workspace_bytes(g: MoeGradients) -> int:
@@ -438,12 +459,14 @@ def moe_grad_norm_workspace_bytes(g: MoeGradients) -> int:
 
 def moe_grad_norm(g: MoeGradients, norm, ws, stream=None):
     """norm [1] = the 2-norm of all gradients together."""
+    _on_device(g, norm=norm, ws=ws)
     _check(lib().moe_grad_norm(ctypes.byref(g), _fp32(norm), _flat(ws),
                                _nbytes(ws) if ws is not None else 0, _stream(stream)))
 
 
 def moe_clip_grads(g: MoeGradients, max_norm, norm, ws=None, norm_given=False, stream=None):
     """Gradients times min(1, max_norm / (norm + 1e-6)); norm [1] is written first, or read."""
+    _on_device(g, norm=norm, ws=ws)
     _check(lib().moe_clip_grads(ctypes.byref(g), float(max_norm), _fp32(norm), int(bool(norm_given)),
                                 _flat(ws), _nbytes(ws) if ws is not None else 0, _stream(stream)))
 
