@@ -384,8 +384,10 @@ def moe_dense_ffn_workspace_bytes(cfg: MoeConfig, T: int) -> int:
 
 
 def _fp32(t) -> Optional[int]:
-    """_flat of an fp32 tensor: half the bytes would be written past their end."""
-    if t is not None and type(t) is not int and t.element_size() != 4:
+    """_flat of an fp32 tensor: half the bytes would be written past their end, whole numbers'
+    read as something else."""
+    import torch
+    if t is not None and type(t) is not int and t.dtype != torch.float32:
         raise ValueError(f"{t.dtype} tensor, not float32")
     return _flat(t)
 

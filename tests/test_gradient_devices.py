@@ -43,3 +43,10 @@ def test_another_than_the_current_gpu_is_refused(monkeypatch):
                  lambda: moe.moe_clip_grads(l, 1.0, 0x1000, torch.empty(2048 * 8, dtype=torch.uint8), stream=0)):
         with pytest.raises(ValueError, match="ws on cpu"):
             call()
+
+
+def test_norm_of_whole_numbers_is_refused():
+    l = moe.gradients([])
+    for dtype in (torch.int32, torch.float64, torch.bfloat16):
+        with pytest.raises(ValueError, match="not float32"):
+            moe.moe_grad_norm(l, torch.zeros(1, dtype=dtype), None, stream=0)
