@@ -419,7 +419,9 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
  * 协同设计", section 2.2): the shared expert of cfg and w by itself,
  *   y = W2 (silu(W_gate x) * (W_up x)),
  * with ws13 and ws2 (and their scales) of w, of width shared_intermediate_size;
- * the routed sizes of cfg take no part and the routed weights may be NULL.
+ * the routed sizes of cfg take no part, whatever they are, and the routed weights
+ * may be NULL.  At most 2^31 - 1 tokens, with MOE_INT8 16.7 million
+ * (MOE_ERR_UNSUPPORTED).
  *   x [T, H], y [T, H] act_dtype, 16-byte aligned.  Every weight type and layout
  *   that the shared expert takes.
  *   gu [T, 2Is] fp32 out, for the backward: the gate's and the up projection's

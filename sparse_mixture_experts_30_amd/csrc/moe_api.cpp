@@ -568,10 +568,22 @@ moe_status check_matrix_threads(int64_t threads) {
 }
 
 // ---- dense layers -----------------------------------------------------------
-// The shared expert's matrices alone.
-moe_status check_dense(const moe_config* c, int64_t T) {
+// The shared expert's matrices alone: `c` is cfg without its routed part, whose
+// sizes then decide about nothing (what is refused, the workspace, the choice of
+// kernels).
+moe_status check_dense(const moe_config* cfg, int64_t T, moe_config* c) {
+  NONNULL(cfg);
+  *c = *cfg;
+  c->n_routed_experts = 2;
+  c->n_group = c->topk_group = c->num_experts_per_tok = 1;
+  c->moe_intermediate_size = 128;
+  c->routed_scaling_factor = 1.0f;
   CHECK(check_cfg(c));
-  CHECK(check_T(T, c));
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T < 0");
+  const int64_t most = is_int8(c->weight_dtype) ? moe::quantize_rows_int8_max() : 0x7fffffffLL;
+  if (T > most)
+    return fail(MOE_ERR_UNSUPPORTED, "%lld tokens: a dense layer takes %lld", (long long)T,
+                (long long)most);
   if (c->shared_intermediate_size <= 0)
     return fail(MOE_ERR_INVALID_ARG, "a dense layer needs shared_intermediate_size > 0");
   if (c->weight_dtype == MOE_BF16 &&
@@ -1200,32 +1212,33 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
 }
 
 size_t moe_dense_ffn_workspace_bytes(const moe_config* cfg, int64_t T) {
-  if (check_dense(cfg, T) != MOE_OK) return 0;
-  return dense_layout(cfg, T).total;
+  moe_config c;
+  return check_dense(cfg, T, &c) == MOE_OK ? dense_layout(&c, T).total : 0;
 }
 
 moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const moe_weights* w,
                          float* gu, void* y, void* ws, size_t ws_bytes, void* stream) {
-  CHECK(check_dense(cfg, T));
+  moe_config c;
+  CHECK(check_dense(cfg, T, &c));
   NONNULL(w);
-  const bool rowmajor = cfg->weight_dtype == MOE_BF16 && !w->packed;
+  const bool rowmajor = c.weight_dtype == MOE_BF16 && !w->packed;
   if (gu && !rowmajor)
     return fail(MOE_ERR_UNSUPPORTED, "gu is kept by row-major bf16 weights only");
   if (T == 0) return MOE_OK;
   NONNULL(x);
   NONNULL(y);
-  CHECK(check_weights(cfg, w, false, true));
+  CHECK(check_weights(&c, w, false, true));
   ALIGNED16(x);
   ALIGNED16(y);
   ALIGNED16(gu);
-  const Layout L = dense_layout(cfg, T);
+  const Layout L = dense_layout(&c, T);
   CHECK(check_ws(ws, ws_bytes, L));
   const hipStream_t s = (hipStream_t)stream;
   if (!rowmajor)
-    return run_ffn(cfg, T, x, nullptr, nullptr, w, nullptr, y, ws, L, s, moe::kGroupShared);
+    return run_ffn(&c, T, x, nullptr, nullptr, w, nullptr, y, ws, L, s, moe::kGroupShared);
   ALIGNED16(w->ws13);
   ALIGNED16(w->ws2);
-  const int H = cfg->hidden_size, I = cfg->shared_intermediate_size;
+  const int H = c.hidden_size, I = c.shared_intermediate_size;
   uint16_t* h = at<uint16_t>(ws, L.h);
   HIPCALL(moe::launch_dense_gate_up((const uint16_t*)x, (const uint16_t*)w->ws13, T, H, I,
                                     gu, h, at<float>(ws, L.part), s),
@@ -1237,24 +1250,26 @@ moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const 
 }
 
 size_t moe_dense_ffn_backward_workspace_bytes(const moe_config* cfg, int64_t T) {
-  if (check_dense(cfg, T) != MOE_OK || cfg->weight_dtype != MOE_BF16) return 0;
-  return dense_backward_layout(cfg, T).total;
+  moe_config c;
+  if (check_dense(cfg, T, &c) != MOE_OK || c.weight_dtype != MOE_BF16) return 0;
+  return dense_backward_layout(&c, T).total;
 }
 
 moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* x,
                                   const moe_weights* w, const float* gu, const void* dy, void* dx,
                                   void* dws13, void* dws2, void* ws, size_t ws_bytes,
                                   void* stream) {
-  CHECK(check_dense(cfg, T));
-  if (cfg->weight_dtype != MOE_BF16)
+  moe_config c;
+  CHECK(check_dense(cfg, T, &c));
+  if (c.weight_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "the dense backward takes bf16 weights");
   NONNULL(w);
   if (w->packed)
     return fail(MOE_ERR_UNSUPPORTED, "the dense backward reads row-major weights (packed = 0)");
   NONNULL(dws13);
   NONNULL(dws2);
-  const int H = cfg->hidden_size, I = cfg->shared_intermediate_size;
-  const DenseBackwardLayout L = dense_backward_layout(cfg, T);
+  const int H = c.hidden_size, I = c.shared_intermediate_size;
+  const DenseBackwardLayout L = dense_backward_layout(&c, T);
   if (T) {
     NONNULL(x);
     NONNULL(dy);
