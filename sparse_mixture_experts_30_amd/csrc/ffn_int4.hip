@@ -516,10 +516,26 @@ quantize_int4_kernel(int group, const uint16_t* __restrict__ src, int64_t chunks
 // The choice is the whole layer's, whichever of its groups the launch computes:
 // the few-row kernel adds k in another order, and a layer gives the same bits
 // with its shared expert in a launch of its own.
+// A dense layer (N = 0) is one group of T rows, and the tall workgroups decide
+// alone: its few column tiles leave CUs idle in the tall-tile kernels up to about
+// two workgroups a CU, whatever T is.  Measured few / 32 / 64 rows in us, by
+// tall workgroups (groups of 128; I = 18432 with H = 7168, 5632 with 2048, 2816
+// with 1024, 1024 with 512):
+//   288 (T = 128, I = 18432) 168 / 201 / 263, 308 (T = 400, I = 5632) 57 / 66 / 87,
+//   352 (T = 1000, I = 2816) 39 / 42 / 53, 440 (T = 600, I = 5632) 81 / 78 / 90,
+//   512 (T = 4096, I = 1024) 32 / 28 / 34, 576 (T = 200, I = 18432) 269 / 244 / 322,
+//   704 (T = 1000, I = 5632) 122 / 100 / 110, 1008 (T = 400, I = 18432) 516 / 427 / 400,
+//   1408 (T = 2000, I = 5632) 231 / 176 / 168, 2304 (T = 1000, I = 18432) 1265 / 939
+//   / 850, 9216 (T = 4096, I = 18432) 5246 / 3608 / 3265.
 constexpr int kFewAverage = 8, kMidAverage = 28;
-constexpr int64_t kTallGrid = 512, kTallWork = 32768;
+constexpr int64_t kTallGrid = 512, kTallWork = 32768, kDenseTallest = 1000;
 int tile_rows(FfnDims d) {
   d.groups = kGroupsAll;
+  if (d.N == 0) {
+    const int64_t tall = ffn_grid_mtiles(d, kManyRows) * (d.Is / 128);
+    if (d.T <= kFewRows || tall < kTallGrid) return kFewRows;
+    return tall < kDenseTallest ? kMidRows : kManyRows;
+  }
   const int64_t tall = ffn_grid_mtiles(d, kManyRows) * (d.I / 128);
   if (d.T <= kFewRows || d.N <= (int64_t)kFewAverage * d.E ||
       (tall < kTallGrid && tall * d.N < kTallWork * d.E))
