@@ -472,7 +472,8 @@ typedef struct {
 /* The global norm of all gradients together: norm = sqrt(sum of squares), the
  * sum in 64 bits in a fixed order, the result rounded to fp32.
  *   norm [1] fp32 out (device); a NaN or infinity among the gradients gives
- *   NaN or infinity; 0 for an empty list.
+ *   NaN or infinity, a norm above fp32's largest number (3.4e38) infinity; 0 for
+ *   an empty list.
  * Workspace: moe_grad_norm_workspace_bytes(g) bytes (it depends on n and on
  * counts past 2^30; 0 for a list that is refused), 256-byte aligned; not needed
  * for n == 0. */
@@ -482,8 +483,8 @@ moe_status moe_grad_norm(const moe_gradients* g, float* norm, void* ws, size_t w
 
 /* Clipping by the global norm: out = grad * min(1, max_norm / (norm + 1e-6)), the
  * product in fp32, rounded once to the gradient's type.  The factor is 1 if the
- * norm is not finite: the gradients stay what they are, and the caller sees
- * the norm.
+ * norm is not finite (in fp32, see moe_grad_norm): the gradients stay what they
+ * are, and the caller sees the norm.
  *   norm_given = 0: norm [1] is written first, as by moe_grad_norm (ws as there);
  *   norm_given = 1: norm [1] is read (device), e.g. after the squares of several
  *   ranks' norms were added; ws may be NULL.

@@ -1,9 +1,11 @@
 // Global norm over many gradients, and clipping to it (gfx950).
 //   norm = sqrt(sum over all of g^2),  out = g min(1, max_norm / (norm + 1e-6)).
 // Squares are summed in 64 bits, which the vector units have at half the rate
-// of fp32, far above what memory delivers: no range is lost to overflow and
-// the order of the sums does not show.  Bound by memory: one read for the
-// norm, one read and one write for the scaling.
+// of fp32, far above what memory delivers: no square and no sum overflows and
+// the order of the sums does not show.  The norm itself is an fp32 number, which
+// the caller has and the factor is made from: above 3.4e38 it is infinite, and
+// counts as not finite.  Bound by memory: one read for the norm, one read and
+// one write for the scaling.
 //
 // Gradients that lie one behind the other, like their outputs, count as one (the
 // pieces of flat buffers; one run per type is watched).  They are cut into
