@@ -79,7 +79,8 @@ typedef enum {
     MOE_INT8 = 6       /* 8-bit integers, one fp32 scale per output channel; the
                           activations are quantised to 8-bit integers with one
                           scale per token row (packed weights only, forward
-                          only; sizes up to 131072; see moe_quantize_weight)  */
+                          only; codes -127..127, sizes up to 131072: sums then
+                          fit 32 bits; see moe_quantize_weight)               */
 } moe_dtype;
 
 /* Layer shape: the MoEGate constructor arguments of the first page's
@@ -428,8 +429,10 @@ moe_status moe_combine_backward(const moe_config* cfg, int64_t T, const void* do
  *   outputs side by side (NULL: not kept; row-major bf16 weights only,
  *   MOE_ERR_UNSUPPORTED otherwise).
  * bf16 weights: h kept in bf16; fp32 accumulation.
- * Row-major bf16 weights serve training and prompts; a few tokens at a time
- * read either layout at the rate of memory.
+ * For bf16 the row-major layout is the one to use, for training, prompts and
+ * single tokens.  Packed copies run in the shared expert's kernels, which are
+ * laid out for the many groups of a routed layer: one token takes about four
+ * times as long, a prompt of thousands of tokens the same.
  * Workspace: moe_dense_ffn_workspace_bytes(cfg, T) bytes (0 for a configuration
  * it does not handle, shared_intermediate_size == 0 among them); one for the
  * largest batch does for the smaller ones. */
@@ -449,7 +452,9 @@ moe_status moe_dense_ffn(const moe_config* cfg, int64_t T, const void* x, const 
  *   that a call without tokens writes).
  * Workspace: moe_dense_ffn_backward_workspace_bytes(cfg, T) bytes, 256-byte
  * aligned (0 for a configuration it does not handle; not needed for T == 0); one
- * for the largest batch does for the smaller ones. */
+ * for the largest batch does for the smaller ones.  8 T Is bytes of it are for g
+ * and u where they are computed again and not used otherwise: the size is the
+ * same with and without gu. */
 size_t moe_dense_ffn_backward_workspace_bytes(const moe_config* cfg, int64_t T);
 moe_status moe_dense_ffn_backward(const moe_config* cfg, int64_t T, const void* x,
                                   const moe_weights* w, const float* gu, const void* dy, void* dx,

@@ -168,9 +168,14 @@ __global__ void __launch_bounds__(kThreads8) grouped_gemm_int8_few(Int8Args p) {
 // --------------------------------------------------------------- many rows
 // A tile of at most 128 rows and two packed output tiles, four waves of all rows
 // x 64 columns, two workgroups a CU.  Each weight goes straight to the registers
-// of the one wave that multiplies it, two steps ahead; the rows pass through
-// three LDS stages that loads from memory fill directly.  Bound by HBM up to
-// about 128 rows an expert: T = 4096 (H = 7168, I = 2048, top-8 of 256) 2.83 ms
+// of the one wave that multiplies it, its load started two steps ahead; the rows
+// pass through three LDS stages that loads from memory fill directly.  The waits
+// for a slice's weights are the compiler's, which counts the 14 loads of weights
+// behind them but not the rows' loads to LDS in between (inline assembly): with
+// four row blocks the newest 14 loads of both kinds may be under way, 1.2 steps.
+// Waits for the weights alone (22 and 21 loads behind) were not measured.
+// Bound by HBM up to about 128 rows an expert: T = 4096 (H = 7168, I = 2048,
+// top-8 of 256) 2.83 ms
 // with both quantisers, 4.2 TB/s of weights and rows counted once; the kernels
 // themselves move 5.0 (experts of several tiles, rows read by more than one XCD).
 // A step of a workgroup takes 1.2 us, about what its matrix instructions, its LDS
@@ -478,6 +483,9 @@ pack_int8_kernel(bool gate_up, const int8_t* __restrict__ codes, u32x4* __restri
 // expert: 92 x 50 34 / 46 us, 114 x 100 34 / 44, 156 x 500 34 / 42, 160 x 32 67 / 64,
 // 288 x 16 143 / 128, 368 x 250 207 / 137, 540 x 47 117 / 101.
 // The choice is the whole layer's, whichever of its groups the launch computes.
+// The shared expert's T rows do not count beside routed ones, which costs layers
+// with few experts a token: E = 256, K = 1, T = 3000 (12 rows an expert) 2.23 ms,
+// all in tall tiles 1.93; with Is = 18432 5.50 and 2.94.
 constexpr int kFewAverage = 14;
 constexpr int64_t kTallGrid = 256, kTallWork = 100000;
 int tile_rows(FfnDims d) {
