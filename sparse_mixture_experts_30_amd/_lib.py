@@ -386,8 +386,10 @@ def moe_dense_ffn_workspace_bytes(cfg: MoeConfig, T: int) -> int:
 def _fp32(t) -> Optional[int]:
     """_flat of an fp32 tensor: half the bytes would be written past their end, whole numbers'
     read as something else."""
+    if t is None or type(t) is int:
+        return t
     import torch
-    if t is not None and type(t) is not int and t.dtype != torch.float32:
+    if t.dtype is not torch.float32:
         raise ValueError(f"{t.dtype} tensor, not float32")
     return _flat(t)
 
@@ -439,20 +441,22 @@ def gradients(grads, out=None) -> MoeGradients:
     return m
 
 
-def _on_device(g: MoeGradients, **tensors):
+def _on_device(g: MoeGradients, norm, ws):
     """Raises where the kernels would read or write host memory, or another GPU's: the list's tensors,
     norm and workspace are all on the current GPU.  (Addresses are taken as they come.)"""
-    import torch
     device = getattr(g, "device", None)   # None: an empty list, or one made from addresses
     if device is None:
         return
-    if device.type != "cuda":
+    import torch
+    index = device.index   # None: not a GPU
+    if index is None:
         raise ValueError(f"gradients on {device}, not on a GPU")
-    if device.index != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise ValueError(f"gradients on {device}, current GPU is {torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and type(t) is not int and t.device != device:
-            raise ValueError(f"{name} on {t.device}, gradients on {device}")
+    if norm is not None and type(norm) is not int and norm.get_device() != index:
+        raise ValueError(f"norm on {norm.device}, gradients on {device}")
+    if ws is not None and type(ws) is not int and ws.get_device() != index:
+        raise ValueError(f"ws on {ws.device}, gradients on {device}")
 
 
 def moe_grad_norm_workspace_bytes(g: MoeGradients) -> int:
@@ -461,14 +465,14 @@ def moe_grad_norm_workspace_bytes(g: MoeGradients) -> int:
 
 def moe_grad_norm(g: MoeGradients, norm, ws, stream=None):
     """norm [1] = the 2-norm of all gradients together."""
-    _on_device(g, norm=norm, ws=ws)
+    _on_device(g, norm, ws)
     _check(lib().moe_grad_norm(ctypes.byref(g), _fp32(norm), _flat(ws),
                                _nbytes(ws) if ws is not None else 0, _stream(stream)))
 
 
 def moe_clip_grads(g: MoeGradients, max_norm, norm, ws=None, norm_given=False, stream=None):
     """Gradients times min(1, max_norm / (norm + 1e-6)); norm [1] is written first, or read."""
-    _on_device(g, norm=norm, ws=ws)
+    _on_device(g, norm, ws)
     _check(lib().moe_clip_grads(ctypes.byref(g), float(max_norm), _fp32(norm), int(bool(norm_given)),
                                 _flat(ws), _nbytes(ws) if ws is not None else 0, _stream(stream)))
 
